@@ -348,6 +348,135 @@ nvfp4_status nvfp4_swizzle_scales(const uint8_t* compact, uint8_t* swizzled, int
                                   int64_t scale_cols, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Expert layers: tokens sorted by expert and back, the cast to E4M3 with one
+ * FP32 scale for each block of 128, and the product of such operands.  These
+ * entry points have no counterpart on the pages this library follows.
+ * The conventions above hold, except that arrays of int32 and of FP32 scales
+ * or weights need their natural (4-byte) alignment only, and that there is no
+ * noop flag.
+ * ---------------------------------------------------------------------------
+ */
+#define NVFP4_MAX_EXPERTS 1024
+#define NVFP4_MAX_TOPK 64
+
+/*
+ * Rows of the sorted tensor (its capacity) and bytes of sort scratch for
+ * tokens x topk slots: rows = floor((slots + experts * (align - 1)) / align) *
+ * align, enough whatever the ids.  Host-only.
+ */
+nvfp4_status nvfp4_token_rows(int64_t tokens, int topk, int num_experts, int align, int64_t* rows,
+                              size_t* scratch_bytes);
+
+/*
+ * Sorts the slots of a router's choices by expert.  Slot s = t * topk + j is
+ * choice j of token t, expert_ids[s] its expert; an id outside 0..num_experts
+ * - 1 (-1, say) drops the slot.  Member e (the rows of expert e) starts at
+ * row offsets[e] and holds the expert's slots in ascending order, followed by
+ * rows without a slot up to a multiple of `align`; offsets[num_experts] is
+ * the end of the last member.
+ *   row_of_slot [tokens * topk]: the slot's row, -1 if dropped;
+ *   slot_of_row [rows]: the row's slot, -1 where there is none (the padding
+ *   of a member, and every row from offsets[num_experts] on);
+ *   offsets [num_experts + 1]; rows: as nvfp4_token_rows gives;
+ *   scratch: scratch_bytes of device memory (NULL where that is 0), contents
+ *   irrelevant, not shared by calls that can run at the same time.
+ * 1 <= num_experts <= NVFP4_MAX_EXPERTS, 1 <= topk <= NVFP4_MAX_TOPK, align
+ * >= 1, tokens >= 0, rows < 2^31.  One launch up to 2048 slots, two above.
+ */
+nvfp4_status nvfp4_sort_tokens(const int32_t* expert_ids, int64_t tokens, int topk, int num_experts, int align,
+                               int32_t* offsets, int32_t* row_of_slot, int32_t* slot_of_row, int64_t rows,
+                               void* scratch, size_t scratch_bytes, void* stream);
+
+/*
+ * out[r] = x[slot_of_row[r] / topk], and zero where there is no slot.  x
+ * [tokens, width], out [rows, width], both of `dtype` (BF16 or FP32), width *
+ * element size a multiple of 16 bytes.  The maps are those of
+ * nvfp4_sort_tokens.  (An entry outside its range counts as -1.)
+ */
+nvfp4_status nvfp4_gather_tokens(const void* x, int dtype, int64_t tokens, int64_t width, int topk,
+                                 const int32_t* row_of_slot, const int32_t* slot_of_row, int64_t rows, void* out,
+                                 void* stream);
+
+/* nvfp4_sort_tokens, then nvfp4_gather_tokens, in one call. */
+nvfp4_status nvfp4_dispatch_tokens(const void* x, int dtype, int64_t tokens, int64_t width,
+                                   const int32_t* expert_ids, int topk, int num_experts, int align,
+                                   int32_t* offsets, int32_t* row_of_slot, int32_t* slot_of_row, int64_t rows,
+                                   void* out, void* scratch, size_t scratch_bytes, void* stream);
+
+/*
+ * y[t] = sum_j weights[t, j] rows[row_of_slot[t, j]] (j ascending, FP32,
+ * rounded once to `dtype`); a dropped slot adds nothing, and a token with
+ * none left gives zero.  rows_in [rows, width], y [tokens, width]; weights
+ * [tokens, topk] FP32, or NULL for 1 (the gradient of the gather).
+ */
+nvfp4_status nvfp4_combine_tokens(const void* rows_in, int dtype, int64_t tokens, int64_t width, int topk,
+                                  const int32_t* row_of_slot, int64_t rows, const float* weights, void* y,
+                                  void* stream);
+
+/*
+ * Gradient of nvfp4_combine_tokens: drows[r] = weights[s] dy[s / topk] for
+ * the row r of slot s, zero for a row without one; dweights[t, j] = <dy[t],
+ * rows_in[row_of_slot[t, j]]> in FP32 (0 for a dropped slot), or NULL.
+ */
+nvfp4_status nvfp4_combine_tokens_grad(const void* dy, const void* rows_in, int dtype, int64_t tokens, int64_t width,
+                                       int topk, const int32_t* row_of_slot, const int32_t* slot_of_row,
+                                       int64_t rows, const float* weights, void* drows, float* dweights,
+                                       void* stream);
+
+/*
+ * Casts x (batch matrices of M x N, row-major, BF16 or FP32) to E4M3 with one
+ * FP32 scale for each block of 128: for a block with a = max(max|x|, 2^-100)
+ *     s = a / 448,  r = 448 / a,  q = E4M3_rn_satfinite(x * r)   (FP32).
+ *   block_rows 1: a block is 128 consecutive elements of a row (the last one
+ *     of a row may be shorter); scale_row [batch][ceil(N/128)][M].
+ *   block_rows 128: a block is a 128 x 128 tile (edges shorter);
+ *     scale_row [batch][ceil(M/128)][ceil(N/128)].
+ * ROWWISE: data_row [batch][M][N] and scale_row.  COLWISE: the same cast of
+ * each matrix transposed, data_col [batch][N][M], scale_col
+ * [batch][ceil(M/128)][N] or [batch][ceil(N/128)][ceil(M/128)].
+ * N % 16 == 0; COLWISE also M % 16 == 0.  An infinity makes its block's scale
+ * infinite and its code NaN, a NaN keeps a NaN code: neither is lost in a
+ * product.
+ */
+nvfp4_status nvfp4_fp8_quantize(const void* x, int dtype, int64_t batch, int64_t M, int64_t N, int block_rows,
+                                uint8_t* data_row, float* scale_row, uint8_t* data_col, float* scale_col,
+                                unsigned flags, void* stream);
+
+/*
+ * out[m][n] = sum_k a[m][k] b[n][k] of E4M3 operands in the layouts of
+ * nvfp4_fp8_quantize: a [M][K] with block_rows 1, b [N][K] with b_block_rows
+ * 1 or 128.  The sum over a block of 128 is accumulated in FP32 by the tensor
+ * cores, scaled and added in FP32; out is rounded once (BF16) or kept (FP32).
+ * K % 16 == 0; any M, N >= 0; K = 0 gives zero.
+ */
+nvfp4_status nvfp4_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_t* b, const float* b_scale,
+                              int b_block_rows, int64_t M, int64_t N, int64_t K, void* out, int out_dtype,
+                              void* stream);
+
+/*
+ * The product by expert: a [rows][K] holds the experts' rows (member e = rows
+ * offsets[e] .. offsets[e+1], device int32, ascending from 0, any alignment),
+ * b [num_experts][N][K] one matrix per expert; out [rows][N], zero for rows
+ * from offsets[num_experts] on.
+ */
+nvfp4_status nvfp4_fp8_matmul_grouped(const uint8_t* a, const float* a_scale, const uint8_t* b, const float* b_scale,
+                                      int b_block_rows, int64_t rows, int64_t N, int64_t K, int num_experts,
+                                      const int32_t* offsets, void* out, int out_dtype, void* stream);
+
+/*
+ * The experts' weight gradients: a [M][rows], b [N][rows] (both block_rows 1;
+ * the column-wise casts of the output gradient and of the input),
+ *     out[e][m][n] = sum over rows r of member e of a[m][r] b[n][r],
+ * zero for an empty member.  rows % 16 == 0, and every offset a multiple of
+ * 128 (nvfp4_sort_tokens with align 128), so that no block spans two members.
+ */
+nvfp4_status nvfp4_fp8_matmul_grouped_wgrad(const uint8_t* a, const float* a_scale, const uint8_t* b,
+                                            const float* b_scale, int64_t M, int64_t N, int64_t rows,
+                                            int num_experts, const int32_t* offsets, void* out, int out_dtype,
+                                            void* stream);
+
+/*
  * Per-device status word of bounded device-side waits: bit 0 = a wait for a
  * tile copy ran out; bit 1 = a grid-wide barrier of a single-pass call ran
  * out.  Synchronizes the current device, copies the word into

@@ -15,6 +15,12 @@ the first dimension, each with its own amax (one launch for bfloat16);
 ``quantize_sr`` rounds the codes stochastically with caller-supplied random
 bytes.
 
+Expert layers: ``dispatch_tokens`` / ``combine_tokens`` sort tokens by expert
+and join them again (``tokens``), ``quantize_fp8`` casts to E4M3 with a scale for
+each block of 128, and ``matmul_fp8`` / ``matmul_fp8_grouped`` /
+``matmul_fp8_grouped_wgrad`` multiply such operands (``fp8``); ``experts``
+runs them together.
+
 Paths for "1d" / "2d" / "rht": "single_pass" (one persistent kernel: amax,
 grid barrier, cast; x read from HBM once; needs a small workspace, which
 this module keeps per device and stream) and "two_pass" (an amax kernel,
@@ -43,7 +49,10 @@ __all__ = ["NVFP4Tensor", "NVFP4Error", "empty", "compute_amax", "compute_amax_r
            "single_pass_workspace", "reset_workspaces",
            "quantize_1d", "quantize_2d", "quantize_rht", "quantize_row_scaled", "quantize_grouped", "quantize_sr",
            "dequantize",
-           "swizzle_scales", "scale_bytes", "device_status"]
+           "swizzle_scales", "scale_bytes", "device_status",
+           "TokenPlan", "sort_tokens", "gather_tokens", "gather_tokens_grad", "dispatch_tokens", "combine_tokens",
+           "combine_tokens_grad", "FP8Operand", "FP8Tensor", "quantize_fp8", "matmul_fp8", "matmul_fp8_grouped",
+           "matmul_fp8_grouped_wgrad"]
 
 
 @dataclass
@@ -456,3 +465,10 @@ def device_status(clear: bool = True) -> int:
     if rc not in (0, 7):
         _lib.check(rc, "nvfp4_device_status")
     return v.value
+
+
+# The operators of expert layers build on the helpers above.
+from .fp8 import (FP8Operand, FP8Tensor, matmul_fp8, matmul_fp8_grouped, matmul_fp8_grouped_wgrad,  # noqa: E402
+                  quantize_fp8)
+from .tokens import (TokenPlan, combine_tokens, combine_tokens_grad, dispatch_tokens, gather_tokens,  # noqa: E402
+                     gather_tokens_grad, sort_tokens)

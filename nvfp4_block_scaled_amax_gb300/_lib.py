@@ -24,9 +24,14 @@ EXPORTS = ("nvfp4_status_string", "nvfp4_scale_bytes", "nvfp4_compute_amax", "nv
            "nvfp4_quantize_2d_single_pass_noalloc", "nvfp4_quantize_grouped_1d", "nvfp4_quantize_grouped_2d",
            "nvfp4_quantize_grouped_1d_single_pass", "nvfp4_quantize_grouped_2d_single_pass",
            "nvfp4_quantize_1d_sr", "nvfp4_quantize_2d_sr",
-           "nvfp4_dequantize", "nvfp4_swizzle_scales", "nvfp4_device_status")
+           "nvfp4_dequantize", "nvfp4_swizzle_scales", "nvfp4_device_status",
+           "nvfp4_token_rows", "nvfp4_sort_tokens", "nvfp4_gather_tokens", "nvfp4_dispatch_tokens",
+           "nvfp4_combine_tokens", "nvfp4_combine_tokens_grad", "nvfp4_fp8_quantize", "nvfp4_fp8_matmul",
+           "nvfp4_fp8_matmul_grouped", "nvfp4_fp8_matmul_grouped_wgrad")
 SINGLE_PASS_WORKSPACE_BYTES = 4096
 MAX_GROUPS = 64
+MAX_EXPERTS = 1024
+MAX_TOPK = 64
 
 
 class Output(ctypes.Structure):
@@ -76,6 +81,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.nvfp4_dequantize.argtypes = [vp, vp, vp, i64, i64, uint, vp, c_int, vp]
         L.nvfp4_swizzle_scales.argtypes = [vp, vp, i64, i64, vp]
         L.nvfp4_device_status.argtypes = [ctypes.POINTER(u32), c_int]
+        size = ctypes.c_size_t
+        L.nvfp4_token_rows.argtypes = [i64, c_int, c_int, c_int, ctypes.POINTER(i64), ctypes.POINTER(size)]
+        L.nvfp4_sort_tokens.argtypes = [vp, i64, c_int, c_int, c_int, vp, vp, vp, i64, vp, size, vp]
+        L.nvfp4_gather_tokens.argtypes = [vp, c_int, i64, i64, c_int, vp, vp, i64, vp, vp]
+        L.nvfp4_dispatch_tokens.argtypes = [vp, c_int, i64, i64, vp, c_int, c_int, c_int, vp, vp, vp, i64, vp, vp,
+                                            size, vp]
+        L.nvfp4_combine_tokens.argtypes = [vp, c_int, i64, i64, c_int, vp, i64, vp, vp, vp]
+        L.nvfp4_combine_tokens_grad.argtypes = [vp, vp, c_int, i64, i64, c_int, vp, vp, i64, vp, vp, vp, vp]
+        L.nvfp4_fp8_quantize.argtypes = [vp, c_int, i64, i64, i64, c_int, vp, vp, vp, vp, uint, vp]
+        L.nvfp4_fp8_matmul.argtypes = [vp, vp, vp, vp, c_int, i64, i64, i64, vp, c_int, vp]
+        L.nvfp4_fp8_matmul_grouped.argtypes = [vp, vp, vp, vp, c_int, i64, i64, i64, c_int, vp, vp, c_int, vp]
+        L.nvfp4_fp8_matmul_grouped_wgrad.argtypes = [vp, vp, vp, vp, i64, i64, i64, c_int, vp, vp, c_int, vp]
         for name in EXPORTS[1:]:
             getattr(L, name).restype = c_int
         if path is None:

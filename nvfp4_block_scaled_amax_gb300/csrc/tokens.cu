@@ -1,0 +1,325 @@
+// tokens.cu -- tokens sorted by expert and back.
+//
+// A token t has topk slots s = t * topk + j, each with an expert e_s.  The
+// sort places the slots in stable order of their expert: with count_e the
+// slots of expert e and offset_e the sum of the earlier experts' counts, each
+// rounded up to `align`,
+//     row(s) = offset_{e_s} + #{s' < s : e_{s'} = e_s}.
+// The gather copies each token to the rows of its slots; the combine adds the
+// rows of a token with its weights, y_t = sum_j w_tj rows[row(t, j)], and its
+// gradient is drows[r] = w_s dy_t and dw_tj = <dy_t, rows[row(t, j)]>.
+// Integer counting only, and every sum in a fixed order: results do not
+// depend on timing.
+#include "common.cuh"
+#include "tokens.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortChunk = 2048;  // slots of one CTA, as long as there are no more chunks than SMs
+
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, int64_t chunk) {
+  extern __shared__ int cnt[];
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) cnt[e] = 0;
+  __syncthreads();
+  const int64_t begin = blockIdx.x * chunk, end = min(begin + chunk, a.slots);
+  for (int64_t s = begin + threadIdx.x; s < end; s += kSortThreads) {
+    const int e = a.ids[s];
+    if ((unsigned)e < (unsigned)a.experts) atomicAdd(&cnt[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads)
+    a.scratch[(int64_t)blockIdx.x * a.experts + e] = cnt[e];
+}
+
+// One CTA per chunk.  Each warp counts its own run of the chunk's slots with
+// match_any (no atomics, so the order inside an expert is the slots' order),
+// the counts become first rows, and a second walk hands the rows out.
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, int64_t chunk) {
+  extern __shared__ int smem[];
+  int* wcnt = smem;                          // [warps][experts]: counts, then the next row of warp and expert
+  int* total = smem + kSortWarps * a.experts;  // [experts]
+  int* first = total + a.experts;            // [experts + 1]: offsets
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nchunks = gridDim.x;
+  if (nchunks > 1) grid_dependency_wait();
+  for (int i = threadIdx.x; i < kSortWarps * a.experts; i += kSortThreads) wcnt[i] = 0;
+  __syncthreads();
+  const int64_t seg = chunk / kSortWarps;
+  const int64_t begin = blockIdx.x * chunk + w * seg;
+  const int64_t end = min(begin + seg, a.slots);
+  int* mine = wcnt + w * a.experts;
+  for (int64_t s0 = begin; s0 < end; s0 += 32) {
+    const int64_t s = s0 + lane;
+    int e = s < end ? a.ids[s] : -1;
+    if ((unsigned)e >= (unsigned)a.experts) e = -1;
+    const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
+    if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) {
+    int before = 0, all = 0;
+    for (int i = 0; i < kSortWarps; ++i) {
+      const int c = wcnt[i * a.experts + e];
+      wcnt[i * a.experts + e] = all;
+      all += c;
+    }
+    if (nchunks > 1) {
+      all = 0;
+      for (int c = 0; c < nchunks; ++c) {
+        const int v = a.scratch[(int64_t)c * a.experts + e];
+        before += c < (int)blockIdx.x ? v : 0;
+        all += v;
+      }
+    }
+    total[e] = all;
+    first[e] = before;  // for now: rows of the earlier chunks
+  }
+  __syncthreads();
+  if (w == 0) {
+    int run = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+      const int e = e0 + lane;
+      const int padded = e < a.experts ? (total[e] + a.align - 1) / a.align * a.align : 0;
+      int incl = padded;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      if (e < a.experts) {
+        const int offset = run + incl - padded, before = first[e];
+        for (int i = 0; i < kSortWarps; ++i) wcnt[i * a.experts + e] += offset + before;
+        first[e] = offset;
+      }
+      run += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    if (lane == 0) first[a.experts] = run;
+  }
+  __syncthreads();
+  for (int64_t s0 = begin; s0 < end; s0 += 32) {
+    const int64_t s = s0 + lane;
+    int e = s < end ? a.ids[s] : -1;
+    if ((unsigned)e >= (unsigned)a.experts) e = -1;
+    const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
+    const int row = e >= 0 ? mine[e] + __popc(peers & ((1u << lane) - 1u)) : -1;
+    __syncwarp();
+    if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+    __syncwarp();
+    if (s < end) {
+      a.row_of_slot[s] = row;
+      if (row >= 0) a.slot_of_row[row] = (int32_t)s;
+    }
+  }
+  // rows without a slot: the end of every member and the end of the capacity
+  for (int e = blockIdx.x; e < a.experts; e += nchunks)
+    for (int r = first[e] + total[e] + threadIdx.x; r < first[e + 1]; r += kSortThreads) a.slot_of_row[r] = -1;
+  for (int64_t r = first[a.experts] + (int64_t)blockIdx.x * kSortThreads + threadIdx.x; r < a.rows;
+       r += (int64_t)nchunks * kSortThreads)
+    a.slot_of_row[r] = -1;
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= a.experts; e += kSortThreads) a.offsets[e] = first[e];
+}
+
+// ---------------------------------------------------------------------------
+constexpr int kRowThreads = 128;
+
+// One CTA per row, 16 bytes per thread and step.
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(const uint4* x, uint4* out, TokenArgs a, int vecs) {
+  grid_dependency_wait();
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const int slot = a.slot_of_row[r];
+    const bool there = slot >= 0 && slot < a.tokens * a.topk;
+    const uint4* src = x + (there ? slot / a.topk : 0) * (int64_t)vecs;
+    for (int i = threadIdx.x; i < vecs; i += kRowThreads)
+      out[r * vecs + i] = there ? src[i] : make_uint4(0, 0, 0, 0);
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[kBf16 ? 8 : 4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kBf16) {
+      f[2 * i] = bf16_lo(w[i]);
+      f[2 * i + 1] = bf16_hi(w[i]);
+    } else {
+      f[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+template <bool kBf16>
+__device__ __forceinline__ uint4 pack(const float (&f)[kBf16 ? 8 : 4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kBf16)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+    else
+      w[i] = __float_as_uint(f[i]);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One CTA per token: y = sum_j w_j rows[row_j], j ascending, in FP32, rounded
+// once.  A slot without a row is skipped, so what its row might hold (or
+// what its weight is) does not matter.
+template <bool kBf16>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const uint4* rows, uint4* y, TokenArgs a, int vecs) {
+  constexpr int kN = kBf16 ? 8 : 4;
+  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    for (int i = threadIdx.x; i < vecs; i += kRowThreads) {
+      float acc[kN] = {};
+      for (int j = 0; j < a.topk; ++j) {
+        const int r = a.row_of_slot[t * a.topk + j];
+        if (r < 0 || r >= a.rows) continue;
+        const float w = a.weights ? a.weights[t * a.topk + j] : 1.0f;
+        float v[kN];
+        unpack<kBf16>(rows[(int64_t)r * vecs + i], v);
+#pragma unroll
+        for (int c = 0; c < kN; ++c) acc[c] = __fmaf_rn(w, v[c], acc[c]);
+      }
+      y[t * vecs + i] = pack<kBf16>(acc);
+    }
+  }
+}
+
+// One CTA per token: dy_t is read once, each of its rows gets w dy, and the
+// dot products are summed per thread, then over the warp by halving
+// distances, then over the warps in order.  CTAs past the tokens zero the
+// rows that have no slot.
+template <bool kBf16>
+__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const uint4* dy, const uint4* rows, uint4* drows,
+                                                                   float* dweights, TokenArgs a, int vecs) {
+  constexpr int kN = kBf16 ? 8 : 4;
+  __shared__ float part[kRowThreads / 32];
+  if (blockIdx.x >= a.tokens) {
+    const int64_t r0 = (blockIdx.x - a.tokens) * 32;
+    for (int64_t r = r0; r < min(r0 + 32, a.rows); ++r) {
+      const int slot = a.slot_of_row[r];
+      if (slot >= 0 && slot < a.tokens * a.topk) continue;
+      for (int i = threadIdx.x; i < vecs; i += kRowThreads) drows[r * vecs + i] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const int64_t t = blockIdx.x;
+  for (int j = 0; j < a.topk; ++j) {
+    const int r = a.row_of_slot[t * a.topk + j];
+    const bool there = r >= 0 && r < a.rows;
+    const float w = a.weights ? a.weights[t * a.topk + j] : 1.0f;
+    float dot = 0.0f;
+    if (there) {
+      for (int i = threadIdx.x; i < vecs; i += kRowThreads) {
+        float g[kN], v[kN];
+        unpack<kBf16>(dy[t * vecs + i], g);
+        unpack<kBf16>(rows[(int64_t)r * vecs + i], v);
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          dot = __fmaf_rn(g[c], v[c], dot);
+          g[c] = __fmul_rn(w, g[c]);
+        }
+        drows[(int64_t)r * vecs + i] = pack<kBf16>(g);
+      }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) dot = __fadd_rn(dot, __shfl_xor_sync(0xFFFFFFFFu, dot, d));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0 && dweights != nullptr) {
+      float sum = part[0];
+      for (int i = 1; i < kRowThreads / 32; ++i) sum = __fadd_rn(sum, part[i]);
+      dweights[t * a.topk + j] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+int64_t chunk_of(int64_t slots, int sms) {
+  const int64_t c = (slots + sms - 1) / sms;
+  const int64_t unit = 32 * kSortWarps;  // whole warps' runs
+  return c <= kSortChunk ? kSortChunk : (c + unit - 1) / unit * unit;
+}
+
+}  // namespace
+
+int sort_chunks(int64_t slots, const LaunchCtx& ctx) {
+  const int64_t c = chunk_of(slots, ctx.num_sms);
+  const int64_t n = (slots + c - 1) / c;
+  return n < 1 ? 1 : (int)n;
+}
+
+// Enough for any number of SMs: chunks hold at least kSortChunk slots.
+int64_t sort_scratch_ints(int64_t slots, int experts) {
+  const int64_t n = (slots + kSortChunk - 1) / kSortChunk;
+  return n <= 1 ? 0 : n * experts;
+}
+
+cudaError_t launch_sort_tokens(const SortArgs& args, const LaunchCtx& ctx) {
+  SortArgs a = args;
+  int64_t chunk = chunk_of(a.slots, ctx.num_sms);
+  const int n = sort_chunks(a.slots, ctx);
+  const size_t smem = sizeof(int) * ((size_t)(kSortWarps + 2) * a.experts + 1);
+  cudaError_t e;
+  if (smem > 48 * 1024 &&
+      (e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
+          cudaSuccess)
+    return e;
+  if (n > 1) {
+    sort_count_kernel<<<n, kSortThreads, sizeof(int) * a.experts, ctx.stream>>>(a, chunk);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    void* p[] = {&a, &chunk};
+    return launch_pdl(reinterpret_cast<const void*>(&sort_place_kernel), dim3(n), dim3(kSortThreads), smem, ctx.stream,
+                      p);
+  }
+  sort_place_kernel<<<1, kSortThreads, smem, ctx.stream>>>(a, chunk);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gather_tokens(const void* x, void* out, const TokenArgs& args, bool pdl, const LaunchCtx& ctx) {
+  TokenArgs a = args;
+  if (a.rows == 0 || a.width == 0) return cudaSuccess;
+  int vecs = (int)(a.width * (a.bf16 ? 2 : 4) / 16);
+  const uint4* xv = static_cast<const uint4*>(x);
+  uint4* ov = static_cast<uint4*>(out);
+  const int64_t grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
+  if (pdl) {
+    void* p[] = {&xv, &ov, &a, &vecs};
+    return launch_pdl(reinterpret_cast<const void*>(&gather_kernel), dim3((unsigned)grid), dim3(kRowThreads), 0,
+                      ctx.stream, p);
+  }
+  gather_kernel<<<(unsigned)grid, kRowThreads, 0, ctx.stream>>>(xv, ov, a, vecs);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_tokens(const void* rows, void* y, const TokenArgs& a, const LaunchCtx& ctx) {
+  if (a.tokens == 0 || a.width == 0) return cudaSuccess;
+  const int vecs = (int)(a.width * (a.bf16 ? 2 : 4) / 16);
+  const unsigned grid = (unsigned)(a.tokens < (1 << 30) ? a.tokens : (1 << 30));
+  if (a.bf16)
+    combine_kernel<true><<<grid, kRowThreads, 0, ctx.stream>>>(static_cast<const uint4*>(rows),
+                                                               static_cast<uint4*>(y), a, vecs);
+  else
+    combine_kernel<false><<<grid, kRowThreads, 0, ctx.stream>>>(static_cast<const uint4*>(rows),
+                                                                static_cast<uint4*>(y), a, vecs);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_tokens_grad(const void* dy, const void* rows, void* drows, float* dweights,
+                                       const TokenArgs& a, const LaunchCtx& ctx) {
+  const int vecs = (int)(a.width * (a.bf16 ? 2 : 4) / 16);
+  const int64_t grid = a.tokens + (vecs > 0 ? (a.rows + 31) / 32 : 0);
+  if (grid == 0) return cudaSuccess;
+  if (a.bf16)
+    combine_grad_kernel<true><<<(unsigned)grid, kRowThreads, 0, ctx.stream>>>(
+        static_cast<const uint4*>(dy), static_cast<const uint4*>(rows), static_cast<uint4*>(drows), dweights, a, vecs);
+  else
+    combine_grad_kernel<false><<<(unsigned)grid, kRowThreads, 0, ctx.stream>>>(
+        static_cast<const uint4*>(dy), static_cast<const uint4*>(rows), static_cast<uint4*>(drows), dweights, a, vecs);
+  return cudaGetLastError();
+}
+
+}  // namespace nvfp4
