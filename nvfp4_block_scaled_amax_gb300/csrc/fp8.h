@@ -40,4 +40,8 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, const LaunchCtx& ctx);
 // 128-byte swizzle, zero fill outside.
 cudaError_t make_fp8_tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int box_rows);
 
+// Tensor map of a product [rows][cols] in BF16 or FP32: box 128 bytes x 32
+// rows, 128-byte swizzle.  Needs a 16-byte aligned base and row pitch.
+cudaError_t make_matmul_out_map(CUtensorMap* map, void* out, bool bf16, int64_t rows, int64_t cols);
+
 }  // namespace nvfp4

@@ -11,182 +11,66 @@
 // contracted dimension instead (in blocks of 128) and each gives a product
 // of its own; an empty member's product is zero.
 //
-// Warp-specialised persistent kernel, one CTA per SM: warp 8 streams 128-byte
-// slices of both operands through a TMA ring, warp 9 issues the MMAs of each
-// block into one of two tensor-memory accumulators, and warps 0-7 read the
-// finished accumulator and add it, scaled, to their registers while the next
-// block is multiplied.
-#include <cudaTypedefs.h>
-
-#include "common.cuh"
-#include "fp8.h"
-#include "tokens.h"
+// Persistent, warp-specialised, one pair of CTAs (two SMs) per 256 x 256
+// tile: each CTA stages 128 rows of A and 128 rows of B per block by TMA, one
+// lane of the first CTA issues the pair's MMAs (256 x 256 x 32) into one of
+// two accumulators that fill tensor memory (256 columns each), and eight
+// warps of each CTA read the finished accumulator of their 128 rows and add
+// it, scaled, to their registers (128 per thread) while the next block is
+// multiplied.  Output leaves through shared memory by TMA while the next
+// tile is summed.
+//
+// Measured at 8192 x 5120 x 8192 (BF16 out, 128 x 128 blocks of B): 228 us,
+// 3.0 PFLOP/s.  The MMAs alone take 168 us, with their operand copies 185 us
+// (256 x 128 MMAs: 240 us, so the tile is 256 wide although two accumulators
+// then leave no third to run ahead).  What bounds it is the hand-over: an
+// accumulator must be heard of, read, scaled and given back within the time
+// of one block's MMAs (about 500 cycles), of which the scaled sums alone
+// (256 FMAs per scheduler) take half.
+#include "fp8_tiles.cuh"
 
 namespace nvfp4 {
+namespace fp8 {
 namespace {
 
-constexpr int kBM = 128, kBN = 128, kBK = 128;
-constexpr int kStages = 6;
-constexpr int kStageA = kBM * kBK, kStageB = kBN * kBK, kStageBytes = kStageA + kStageB;
-constexpr int kSumWarps = 8;
-constexpr int kThreads = 32 * (kSumWarps + 2);
-constexpr int kColsPerThread = kBN / 2;
+constexpr int kStages = 4;
+constexpr int kStageA = 128 * kBK, kStageBytes = 2 * kStageA;
+constexpr int kScaleStages = 2;
+constexpr int kScaleBatch = 8;  // blocks per scale stage: one hand-over for eight blocks
+constexpr int kBufCols = 256;
+constexpr int kChunk = 64;  // columns read at a time
 
-struct KernelArgs {
-  const float* sa;
-  const float* sb;
-  int64_t a_rows, a_cols, b_rows;
-  int b_block_rows, experts, wgrad;
-  const int32_t* offsets;
-  void* out;
-  int out_bf16;
-  unsigned* status;
-};
+constexpr int kScaleFloats = 128 + 256;  // of A's 128 rows, of B's 256
+constexpr int kSumWarps = 8;
+constexpr int kOutBox = 32 * 128;   // bytes of one output box: 32 rows of 128 bytes
+constexpr int kOutBoxes = 2;        // per warp: one is written while the other is stored
+constexpr int kThreads = 32 * (4 + kSumWarps);
+using Tiles = TileList<256, 256, 8>;
 
 struct Barriers {
-  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2];
+  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], sfull[kScaleStages], sempty[kScaleStages];
   uint32_t tmem;
+  uint32_t pad[3];
 };
 
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-// Instruction descriptor of kind::f8f6f4: E4M3 A and B, both K-major, FP32 D.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
-  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-               " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
-               "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-               : "memory");
-}
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kSumWarps * kOutBoxes * kOutBox + kScaleStages * kScaleBatch * kScaleFloats * 4 + (int)sizeof(Barriers) +
+                           4 * (kMaxExperts + 2);
 
-// Tiles of all members in one list: first[i] is the first tile of member i
-// (forward: one more member, the rows past the last one, with nothing to sum).
-struct TileList {
-  int* first;  // shared, [members + 1]
-  int members;
-  int64_t tiles_n;
-};
-
-struct Tile {
-  int64_t a_row, b_row, n0, out_row;
-  int rows, cols;  // of the tile, inside the output
-  int kb0, nkb;    // blocks of the contracted dimension
-  int member;
-};
-
-__device__ __forceinline__ int64_t clamp_offset(const KernelArgs& p, int e) {
-  const int64_t limit = p.wgrad ? p.a_cols : p.a_rows;
-  const int64_t v = p.offsets[e];
-  return v < 0 ? 0 : v > limit ? limit : v;
-}
-__device__ __forceinline__ void member_range(const KernelArgs& p, int e, int64_t& begin, int64_t& end) {
-  const int64_t limit = p.wgrad ? p.a_cols : p.a_rows;
-  if (p.offsets == nullptr) {
-    begin = 0;
-    end = limit;
-  } else if (e == p.experts) {  // the rows past the last member
-    begin = clamp_offset(p, e);
-    end = limit;
-  } else {
-    begin = clamp_offset(p, e);
-    end = clamp_offset(p, e + 1);
-    if (end < begin) end = begin;
-  }
-}
-
-__device__ __forceinline__ Tile tile_at(const KernelArgs& p, const TileList& l, int t) {
-  int lo = 0, hi = l.members;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (l.first[mid] <= t) lo = mid; else hi = mid;
-  }
-  Tile r;
-  r.member = lo;
-  const int i = t - l.first[lo];
-  int64_t begin, end;
-  member_range(p, lo, begin, end);
-  const int64_t M = p.wgrad ? p.a_rows : end - begin;
-  const int mt = (int)((M + kBM - 1) / kBM);
-  const int64_t m0 = (int64_t)(i % mt) * kBM;
-  r.n0 = (int64_t)(i / mt) * kBN;
-  r.rows = (int)min((int64_t)kBM, M - m0);
-  r.cols = (int)min((int64_t)kBN, p.b_rows - r.n0);
-  if (p.wgrad) {
-    r.a_row = m0;
-    r.b_row = r.n0;
-    r.out_row = lo * p.a_rows + m0;
-    r.kb0 = (int)(begin / kBK);
-    r.nkb = (int)((end + kBK - 1) / kBK) - r.kb0;
-    if (begin == end) r.nkb = 0;
-  } else {
-    r.a_row = begin + m0;
-    r.out_row = r.a_row;
-    const bool tail = lo == p.experts;
-    r.b_row = tail ? 0 : lo * p.b_rows + r.n0;
-    r.kb0 = 0;
-    r.nkb = tail ? 0 : (int)((p.a_cols + kBK - 1) / kBK);
-  }
-  return r;
-}
-
-__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-__global__ void __launch_bounds__(kThreads, 1)
-fp8_matmul_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-                  const __grid_constant__ KernelArgs p) {
+template <bool kColScales>  // B has a scale per row (block_rows 1)
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                   const __grid_constant__ CUtensorMap omap,
+                   const __grid_constant__ MatmulKernelArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  Barriers* bar = reinterpret_cast<Barriers*>(smem + kStages * kStageBytes);
-  TileList list;
-  list.first = reinterpret_cast<int*>(bar + 1);
-  list.members = p.offsets == nullptr ? 1 : p.experts + (p.wgrad ? 0 : 1);
-  list.tiles_n = (p.b_rows + kBN - 1) / kBN;
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* out_stage = smem + kStages * kStageBytes;
+  float* scales = reinterpret_cast<float*>(out_stage + kSumWarps * kOutBoxes * kOutBox);
+  Barriers* bar = reinterpret_cast<Barriers*>(scales + kScaleStages * kScaleBatch * kScaleFloats);
+  int* first = reinterpret_cast<int*>(bar + 1);
+  const int w = warp_index(), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
 
   if (w == 0) {
-    int run = 0;
-    for (int e0 = 0; e0 < list.members; e0 += 32) {
-      const int e = e0 + lane;
-      int tiles = 0;
-      if (e < list.members) {
-        int64_t begin, end;
-        member_range(p, e, begin, end);
-        const int64_t M = p.wgrad ? p.a_rows : end - begin;
-        tiles = (int)((M + kBM - 1) / kBM * list.tiles_n);
-      }
-      int incl = tiles;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-        if (lane >= d) incl += v;
-      }
-      if (e < list.members) list.first[e] = run + incl - tiles;
-      run += __shfl_sync(0xFFFFFFFFu, incl, 31);
-    }
-    if (lane == 0) list.first[list.members] = run;
-  } else if (w == kSumWarps) {
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) {
         mbar_init(&bar->full[i], 1);
@@ -194,153 +78,317 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constan
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&bar->tfull[i], 1);
-        mbar_init(&bar->tempty[i], kSumWarps);
+        mbar_init(&bar->tempty[i], 2 * kSumWarps);
+      }
+      for (int i = 0; i < kScaleStages; ++i) {
+        mbar_init(&bar->sfull[i], 32);
+        mbar_init(&bar->sempty[i], kSumWarps);
       }
       fence_mbar_init();
       tma_prefetch_desc(&amap);
       tma_prefetch_desc(&bmap);
+      if (p.out_map) tma_prefetch_desc(&omap);
     }
-  } else if (w == kSumWarps + 1) {
-    tmem_alloc(&bar->tmem, 2 * kBN);
+  } else if (w == 1) {
+    tmem_alloc_pair(&bar->tmem, 512);
+  } else if (w == 2) {
+    Tiles::fill(p, first);
   }
   tcgen05_before_sync();
   __syncthreads();
+  cluster_sync();
   tcgen05_after_sync();
-  const uint32_t tmem = bar->tmem;
-  const int tiles = list.first[list.members];
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem, 0);
+  const int tiles = first[member_count(p)];
+  const int t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-  if (w == kSumWarps) {
-    if (lane == 0) {
-      uint32_t it = 0;
+  if (w < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // These loops are the same in all lanes of their warp; one lane issues.
+    if (w == 0) {
+      // both operands' slices, counted on the first CTA's barrier
+      uint32_t s = 0, phase = 1;
       bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const Tile tl = tile_at(p, list, t);
-        for (int kb = 0; kb < tl.nkb; ++kb, ++it) {
-          const uint32_t s = it % kStages;
-          if (!mbar_wait_bounded(&bar->empty[s], ((it / kStages) & 1) ^ 1, p.status)) {
+      for (int t = t0; t < tiles && ok; t += step) {
+        const Tile tl = Tiles::at(p, first, t);
+        const int32_t arow = (int32_t)tl.a_row + 128 * rank, brow = (int32_t)tl.b_row + 128 * rank;
+        int32_t x = tl.kb0 * kBK;
+        for (int kb = 0; kb < tl.nkb; ++kb, x += kBK) {
+          if (!mbar_wait(&bar->empty[s], phase, p.status)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&bar->full[s], kStageBytes);
-          const uint32_t dst = smem_u32(smem + s * kStageBytes);
-          tma_load(dst, &amap, (tl.kb0 + kb) * kBK, (int32_t)tl.a_row, &bar->full[s]);
-          tma_load(dst + kStageA, &bmap, (tl.kb0 + kb) * kBK, (int32_t)tl.b_row, &bar->full[s]);
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], 2 * kStageBytes);
+            const uint32_t dst = smem_u32(smem + s * kStageBytes);
+            const uint32_t full = map_to_cta(smem_u32(&bar->full[s]), 0);
+            tma_load_pair(dst, &amap, x, arow, full);
+            tma_load_pair(dst + kStageA, &bmap, x, brow, full);
+          }
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
       }
-      if (!ok)  // let the copies in flight land before the CTA leaves
-        for (uint32_t i = it < kStages ? 0 : it - kStages; i < it; ++i)
-          mbar_wait_bounded(&bar->full[i % kStages], (i / kStages) & 1, p.status);
-    }
-    __syncwarp();
-  } else if (w == kSumWarps + 1) {
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = idesc_e4m3(kBM, kBN);
-      uint32_t it = 0;
+      if (!ok) {  // given up: the copies in flight land long before this ends
+        const long long c0 = clock64();
+        while (clock64() - c0 < 50000000LL) {
+        }
+      }
+    } else if (w == 1 && rank == 0) {
+      constexpr uint32_t kIdesc = idesc_e4m3(256, 256);
+      const uint64_t desc0 = operand_desc(smem_u32(smem));
+      uint32_t s = 0, phase = 0, buf = 0, tphase = 1;
       bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const int nkb = tile_at(p, list, t).nkb;
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const uint32_t s = it % kStages, buf = it & 1;
-          if (!mbar_wait_bounded(&bar->tempty[buf], ((it >> 1) & 1) ^ 1, p.status) ||
-              !mbar_wait_bounded(&bar->full[s], (it / kStages) & 1, p.status)) {
+      for (int t = t0; t < tiles && ok; t += step) {
+        const int nkb = Tiles::at(p, first, t).nkb;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait(&bar->full[s], phase, p.status) || !mbar_wait(&bar->tempty[buf], tphase, p.status)) {
             ok = false;
             break;
           }
           tcgen05_after_sync();
-          const uint32_t a = smem_u32(smem + s * kStageBytes), b = a + kStageA;
+          if (elect_one()) {
+            const uint64_t a = desc0 + s * (kStageBytes / 16), b = a + kStageA / 16;
+            const uint32_t d = tmem + buf * kBufCols;
 #pragma unroll
-          for (int k = 0; k < kBK / 32; ++k)  // 32 bytes further inside the 128-byte swizzled rows
-            umma_e4m3(tmem + buf * kBN, umma_smem_desc(a + 32 * k, 16, 1024, 2), umma_smem_desc(b + 32 * k, 16, 1024, 2),
-                      kIdesc, k > 0);
-          umma_commit(&bar->empty[s]);
-          umma_commit(&bar->tfull[buf]);
+            for (int k = 0; k < kBK / 32; ++k)  // 32 bytes further inside the 128-byte swizzled rows
+              umma_e4m3<2>(d, a + 2 * k, b + 2 * k, kIdesc, k > 0);
+            umma_commit_pair(&bar->tfull[buf]);
+            umma_commit_pair(&bar->empty[s]);
+          }
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
+          buf ^= 1;
+          tphase ^= buf ^ 1;
         }
       }
+    } else if (w == 2) {
+      // the block's scales: 128 of this CTA's rows of A, 256 (or 2) of B
+      const int64_t kblocks = (p.a_cols + kBK - 1) / kBK, nblocks = (p.b_rows + 127) / 128;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = t0; t < tiles && ok; t += step) {
+        const Tile tl = Tiles::at(p, first, t);
+        const int64_t member = p.wgrad || tl.nkb == 0 ? 0 : tl.member;
+        const float* pa = p.sa + tl.kb0 * p.a_rows + tl.a_row;
+        const float* pb;
+        int oa[4], ob[8], nb;  // offsets of this lane's scales; how many of B's exist
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          oa[i] = (int)min((int64_t)(128 * rank + lane + 32 * i), p.a_rows - 1 - tl.a_row);
+        if constexpr (kColScales) {
+          pb = p.sb + (member * kblocks + tl.kb0) * p.b_rows + tl.n0;
+          nb = tl.cols;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ob[i] = min(lane + 32 * i, nb - 1);
+        } else {
+          pb = p.sb + (member * nblocks + tl.n0 / 128) * kblocks + tl.kb0;
+          nb = (int)min((int64_t)2, nblocks - tl.n0 / 128);
+          ob[0] = lane < nb ? lane * (int)kblocks : 0;
+        }
+        for (int kb = 0; kb < tl.nkb; kb += kScaleBatch, ++it) {
+          const uint32_t s = it % kScaleStages;
+          if (!mbar_wait(&bar->sempty[s], ((it / kScaleStages) & 1) ^ 1, p.status)) {
+            ok = false;
+            break;
+          }
+          uint32_t dst = smem_u32(scales + s * kScaleBatch * kScaleFloats) + 4 * lane;
+          const int n = min(kScaleBatch, tl.nkb - kb);
+          for (int j = 0; j < n; ++j, dst += 4 * kScaleFloats) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cp_async4(dst + 128 * i, pa + oa[i], true);
+            pa += p.a_rows;
+            if constexpr (kColScales) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) cp_async4(dst + 512 + 128 * i, pb + ob[i], lane + 32 * i < nb);
+              pb += p.b_rows;
+            } else {
+              if (lane < 2) cp_async4(dst + 512, pb + ob[0], lane < nb);
+              ++pb;
+            }
+          }
+          cp_async_arrive(&bar->sfull[s]);
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncwarp();
   } else {
-    const int q = w & 3, half = w >> 2;
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + half * kColsPerThread;
-    const int64_t kblocks = (p.a_cols + kBK - 1) / kBK, nblocks = (p.b_rows + kBN - 1) / kBN;
-    uint32_t it = 0;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int q = w & 3, half = (w - 4) >> 2;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + half * 128;
+    const uint32_t tempty0 = map_to_cta(smem_u32(&bar->tempty[0]), 0);
+    const int64_t pitch = p.b_rows;
+    const uint32_t box = smem_u32(out_stage + (w - 4) * kOutBoxes * kOutBox);
+    uint32_t boxes = 0;
+    // Shared-memory addresses of what the loop touches.
+    const uint32_t bsfull = smem_u32(&bar->sfull[0]), bsempty = smem_u32(&bar->sempty[0]);
+    const uint32_t btfull = smem_u32(&bar->tfull[0]), btempty = tempty0;
+    const uint32_t sc_row = smem_u32(scales) + 4 * (32 * q + lane), sc_col = smem_u32(scales) + 4 * (128 + 128 * half);
+    const uint32_t sc_blk = smem_u32(scales) + 4 * (128 + half);
+    uint32_t it = 0, batch = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile tl = tile_at(p, list, t);
-      float acc[kColsPerThread];
+    for (int t = t0; t < tiles && ok
+; t += step) {
+      const Tile tl = Tiles::at(p, first, t);
+      float acc[128];
 #pragma unroll
-      for (int i = 0; i < kColsPerThread; ++i) acc[i] = 0.0f;
-      const int row = 32 * q + lane;
-      const int64_t arow = min(tl.a_row + row, p.a_rows - 1);
-      const int64_t c0 = tl.n0 + half * kColsPerThread;
-      const int64_t member = p.wgrad || tl.nkb == 0 ? 0 : tl.member;
-      for (int kb = 0; kb < tl.nkb; ++kb, ++it) {
-        const uint32_t buf = it & 1;
-        const float sa = p.sa[(tl.kb0 + kb) * p.a_rows + arow];
-        if (!mbar_wait_bounded(&bar->tfull[buf], (it >> 1) & 1, p.status)) {
-          ok = false;
-          break;
+      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+      // Scalar FMAs: the packed form issues at half their rate here and gains nothing.
+      auto add = [&](const uint32_t (&x)[kChunk], int c, uint32_t sb, float scale) {
+#pragma unroll
+        for (int i = 0; i < kChunk; i += 4) {
+          float f[4] = {__uint_as_float(x[i]), __uint_as_float(x[i + 1]), __uint_as_float(x[i + 2]),
+                        __uint_as_float(x[i + 3])};
+          if constexpr (kColScales) {
+            float b[4];
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3])
+                         : "r"(sb + 4 * (c + i)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = __fmul_rn(f[j], b[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[c + i + j] = __fmaf_rn(f[j], scale, acc[c + i + j]);
         }
+      };
+      float scale = 0.0f;
+      auto load_scale = [&](uint32_t off) {
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(scale) : "r"(sc_row + off));
+        if constexpr (!kColScales) {
+          float sb;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sb) : "r"(sc_blk + off));
+          scale = __fmul_rn(scale, sb);
+        }
+      };
+      const int nkb = tl.nkb;
+      uint32_t off = 0;  // of the block's scales
+#pragma unroll 1
+      for (int kb = 0; kb < nkb; ++kb) {
+        if ((kb & (kScaleBatch - 1)) == 0) {
+          const uint32_t ss = batch % kScaleStages;
+          off = ss * (kScaleBatch * kScaleFloats * 4);
+          ok = mbar_wait_at(bsfull + 8 * ss, (batch / kScaleStages) & 1, p.status);
+          if (!ok) break;
+        }
+        load_scale(off);
+        const uint32_t src = lane_base + (it & 1) * kBufCols;
+        ok = mbar_wait_at(btfull + 8 * (it & 1), (it >> 1) & 1, p.status);
+        if (!ok) break;
         __syncwarp();
         tcgen05_after_sync();
-        uint32_t v[kColsPerThread / 32][32];
 #pragma unroll
-        for (int c = 0; c < kColsPerThread / 32; ++c) tmem_ld32_nowait(lane_base + buf * kBN + 32 * c, v[c]);
-        tmem_ld_wait();
-        tcgen05_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->tempty[buf]);
-        if (p.b_block_rows == 128) {
-          const float s = __fmul_rn(sa, p.sb[(member * nblocks + tl.n0 / kBN) * kblocks + tl.kb0 + kb]);
-#pragma unroll
-          for (int c = 0; c < kColsPerThread / 32; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[32 * c + i] = __fmaf_rn(__uint_as_float(v[c][i]), s, acc[32 * c + i]);
-        } else {
-          const float* sb = p.sb + (member * kblocks + tl.kb0 + kb) * p.b_rows;
-#pragma unroll
-          for (int c = 0; c < kColsPerThread / 32; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int64_t n = min(c0 + 32 * c + i, p.b_rows - 1);
-              acc[32 * c + i] =
-                  __fmaf_rn(__fmul_rn(__uint_as_float(v[c][i]), __ldg(sb + n)), sa, acc[32 * c + i]);
-            }
+        for (int c = 0; c < 128; c += kChunk) {
+          uint32_t v[kChunk];
+          tmem_read(src + c, v);
+          if (c == 128 - kChunk) {
+            // everything is read: the accumulator may be overwritten
+            tcgen05_before_sync();
+            if (lane == 0) mbar_arrive_cluster(btempty + 8 * (it & 1));
+          }
+          add(v, c, sc_col + off, scale);
+        }
+        ++it;
+        off += 4 * kScaleFloats;
+        if (kb + 1 == nkb || (kb & (kScaleBatch - 1)) == kScaleBatch - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(bsempty + 8 * (batch % kScaleStages));
+          ++batch;
         }
       }
-      if (!ok || row >= tl.rows) continue;
-      const int64_t at = (tl.out_row + row) * p.b_rows + c0;
+      if (!ok) break;
+      // The 32 rows of this warp go out through shared memory, 128 bytes of
+      // each row at a time, stored by TMA while the next tile is summed.  Rows
+      // that end inside another member's, or rows whose pitch TMA cannot take,
+      // are written directly.
+      const int row0 = 128 * (int)rank + 32 * q, c0 = 128 * half;
+      if (row0 >= tl.rows || c0 >= tl.cols) continue;
+      if (p.out_map && row0 + 32 <= tl.rows) {
+        auto put = [&](const uint32_t (&word)[32], int c) {  // 128 bytes of the lane's row, from column c of the tile
+          const uint32_t dst = box + (boxes % kOutBoxes) * kOutBox;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBoxes - 1) : "memory");
+          __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kColsPerThread; ++i) {
-        if (c0 + i >= p.b_rows) continue;
+          for (int j = 0; j < 8; ++j)
+            sts_v4(dst + lane * 128 + ((j ^ (lane & 7)) * 16), word[4 * j], word[4 * j + 1], word[4 * j + 2],
+                   word[4 * j + 3]);
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            if (c < tl.cols) tma_store(&omap, dst, (int32_t)(tl.n0 + c), (int32_t)(tl.out_row + row0));
+            bulk_commit();
+          }
+          ++boxes;
+        };
+        uint32_t word[32];
         if (p.out_bf16) {
-          uint16_t h;
-          asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(acc[i]));
-          static_cast<uint16_t*>(p.out)[at + i] = h;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(word[i]) : "f"(acc[64 * g + 2 * i + 1]), "f"(acc[64 * g + 2 * i]));
+            put(word, c0 + 64 * g);
+          }
         } else {
-          static_cast<float*>(p.out)[at + i] = acc[i];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) word[i] = __float_as_uint(acc[32 * g + i]);
+            put(word, c0 + 32 * g);
+          }
+        }
+      } else if (row0 + lane < tl.rows) {
+        const int64_t at = (tl.out_row + row0 + lane) * pitch + tl.n0 + c0;
+        const int n = tl.cols - c0;
+        if (p.out_bf16) {
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) {
+            uint16_t h;
+            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(acc[i]));
+            if (i < n) dst[i] = h;
+          }
+        } else {
+          float* dst = static_cast<float*>(p.out) + at;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i < n) dst[i] = acc[i];
         }
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
   tcgen05_before_sync();
   __syncthreads();
+  cluster_sync();
   tcgen05_after_sync();
-  if (w == kSumWarps + 1) tmem_dealloc(tmem, 2 * kBN);
+  if (w == 1) tmem_dealloc_pair(tmem, 512);
 }
 
 }  // namespace
+}  // namespace fp8
 
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
+  using namespace fp8;
   if (a.a_rows == 0 || a.b_rows == 0) return cudaSuccess;
   const int64_t out_rows = a.wgrad ? a.a_rows * a.experts : a.a_rows;
   if (a.a_cols == 0)
     return cudaMemsetAsync(a.out, 0, (size_t)out_rows * a.b_rows * (a.out_bf16 ? 2 : 4), ctx.stream);
-  CUtensorMap amap, bmap;
-  cudaError_t e = make_fp8_tensor_map(&amap, a.a, a.a_rows, a.a_cols, kBM);
+  CUtensorMap amap, bmap, omap = {};
+  cudaError_t e = make_fp8_tensor_map(&amap, a.a, a.a_rows, a.a_cols, 128);
   if (e != cudaSuccess) return e;
-  e = make_fp8_tensor_map(&bmap, a.b, a.wgrad ? a.b_rows : a.b_rows * a.experts, a.a_cols, kBN);
+  e = make_fp8_tensor_map(&bmap, a.b, a.wgrad ? a.b_rows : a.b_rows * a.experts, a.a_cols, 128);
   if (e != cudaSuccess) return e;
-  KernelArgs p = {};
+  MatmulKernelArgs p = {};
+  // TMA writes the output where its rows start on 16 bytes.
+  p.out_map = a.b_rows * (a.out_bf16 ? 2 : 4) % 16 == 0;
+  if (p.out_map && (e = make_matmul_out_map(&omap, a.out, a.out_bf16, out_rows, a.b_rows)) != cudaSuccess) return e;
   p.sa = a.sa;
   p.sb = a.sb;
   p.a_rows = a.a_rows;
@@ -354,14 +402,13 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   p.out_bf16 = a.out_bf16;
   p.status = ctx.status;
   // No more tiles than this, whatever the offsets.
-  const int64_t tn = (a.b_rows + kBN - 1) / kBN;
-  const int64_t tm = (a.a_rows + kBM - 1) / kBM;
+  const int64_t tn = (a.b_rows + 255) / 256, tm = (a.a_rows + 255) / 256;
   const int64_t tiles = tn * (a.wgrad ? tm * a.experts : tm + (a.offsets ? a.experts : 0));
-  const unsigned grid = (unsigned)(tiles < ctx.num_sms ? tiles : ctx.num_sms);
-  const int smem = 1024 + kStages * kStageBytes + (int)sizeof(Barriers) + 4 * (kMaxExperts + 2);
-  e = cudaFuncSetAttribute(fp8_matmul_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const unsigned pairs = (unsigned)(tiles < ctx.num_sms / 2 ? tiles : ctx.num_sms / 2);
+  const auto kernel = a.b_block_rows == 1 ? matmul_pair_kernel<true> : matmul_pair_kernel<false>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  fp8_matmul_kernel<<<grid, kThreads, smem, ctx.stream>>>(amap, bmap, p);
+  kernel<<<2 * pairs, kThreads, kSmemBytes, ctx.stream>>>(amap, bmap, omap, p);
   return cudaGetLastError();
 }
 

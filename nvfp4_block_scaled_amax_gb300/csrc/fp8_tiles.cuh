@@ -1,0 +1,350 @@
+// fp8_tiles.cuh -- what the product kernels of block-scaled E4M3 operands
+// share: the list of output tiles over all members, tensor-core and copy
+// primitives, and the scaled accumulation.
+#pragma once
+
+#include "common.cuh"
+#include "fp8.h"
+#include "tokens.h"
+
+namespace nvfp4 {
+namespace fp8 {
+
+constexpr int kBK = 128;  // elements (bytes) of a block along the contracted dimension
+
+struct MatmulKernelArgs {
+  const float* sa;
+  const float* sb;
+  int64_t a_rows, a_cols, b_rows;
+  int b_block_rows, experts, wgrad;
+  const int32_t* offsets;
+  void* out;
+  int out_bf16, out_map;
+  unsigned* status;
+};
+
+// ---------------------------------------------------------------------------
+// Members and tiles
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int64_t clamp_offset(const MatmulKernelArgs& p, int e) {
+  const int64_t limit = p.wgrad ? p.a_cols : p.a_rows;
+  const int64_t v = p.offsets[e];
+  return v < 0 ? 0 : v > limit ? limit : v;
+}
+// Rows (wgrad: columns) of A that member e holds.  Member `experts` of a
+// forward product is the rows past the last member: nothing to sum, zeros to
+// write.
+__device__ __forceinline__ void member_range(const MatmulKernelArgs& p, int e, int64_t& begin, int64_t& end) {
+  const int64_t limit = p.wgrad ? p.a_cols : p.a_rows;
+  if (p.offsets == nullptr) {
+    begin = 0;
+    end = limit;
+  } else if (e == p.experts) {
+    begin = clamp_offset(p, e);
+    end = limit;
+  } else {
+    begin = clamp_offset(p, e);
+    end = clamp_offset(p, e + 1);
+    if (end < begin) end = begin;
+  }
+}
+__device__ __forceinline__ int member_count(const MatmulKernelArgs& p) {
+  return p.offsets == nullptr ? 1 : p.experts + (p.wgrad ? 0 : 1);
+}
+
+// One tile: rows a_row .. of A and b_row .. of B (coordinates of the tensor
+// maps), blocks kb0 .. kb0 + nkb, its place in the output and how much of it
+// exists.
+struct Tile {
+  int64_t a_row, b_row, n0, out_row;
+  int rows, cols;
+  int kb0, nkb;
+  int member;
+};
+
+// Tiles of kTM rows of A by kTN rows of B, all members in one list: first[i]
+// is the first tile of member i.  Inside a member, bands of kBand row tiles,
+// and in a band all row tiles of a column before the next column, so that the
+// tiles in flight share both operands' rows in L2.
+template <int kTM, int kTN, int kBand>
+struct TileList {
+  static __device__ __forceinline__ int64_t rows_of(const MatmulKernelArgs& p, int e) {
+    if (p.wgrad) return p.a_rows;
+    int64_t begin, end;
+    member_range(p, e, begin, end);
+    return end - begin;
+  }
+  // One warp fills first[0 .. members].
+  static __device__ __forceinline__ void fill(const MatmulKernelArgs& p, int* first) {
+    const int lane = threadIdx.x & 31, members = member_count(p);
+    const int64_t tn = (p.b_rows + kTN - 1) / kTN;
+    int run = 0;
+    for (int e0 = 0; e0 < members; e0 += 32) {
+      const int e = e0 + lane;
+      const int tiles = e < members ? (int)((rows_of(p, e) + kTM - 1) / kTM * tn) : 0;
+      int incl = tiles;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      if (e < members) first[e] = run + incl - tiles;
+      run += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    if (lane == 0) first[members] = run;
+  }
+  static __device__ __forceinline__ Tile at(const MatmulKernelArgs& p, const int* first, int t) {
+    int lo = 0, hi = member_count(p);
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= t) lo = mid; else hi = mid;
+    }
+    Tile r;
+    r.member = lo;
+    const int i = t - first[lo];
+    int64_t begin, end;
+    member_range(p, lo, begin, end);
+    const int64_t M = p.wgrad ? p.a_rows : end - begin;
+    const int mt = (int)((M + kTM - 1) / kTM), nt = (int)((p.b_rows + kTN - 1) / kTN);
+    const int band = i / (kBand * nt), in_band = i - band * kBand * nt;
+    const int height = min(kBand, mt - band * kBand);
+    const int64_t m0 = (int64_t)(band * kBand + in_band % height) * kTM;
+    r.n0 = (int64_t)(in_band / height) * kTN;
+    r.rows = (int)min((int64_t)kTM, M - m0);
+    r.cols = (int)min((int64_t)kTN, p.b_rows - r.n0);
+    if (p.wgrad) {
+      r.a_row = m0;
+      r.b_row = r.n0;
+      r.out_row = lo * p.a_rows + m0;
+      r.kb0 = (int)(begin / kBK);
+      r.nkb = begin == end ? 0 : (int)((end + kBK - 1) / kBK) - r.kb0;
+    } else {
+      const bool past = lo == p.experts;
+      r.a_row = r.out_row = begin + m0;
+      r.b_row = past ? 0 : lo * p.b_rows + r.n0;
+      r.kb0 = 0;
+      r.nkb = past ? 0 : (int)((p.a_cols + kBK - 1) / kBK);
+    }
+    return r;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Copies, barriers, tensor cores
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+// The same, completing on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+// The bounded wait of common.cuh without a time hint on the try: a hinted try
+// that does not succeed at once sleeps, and its sleep ends up to half a
+// microsecond late, which the hand-overs below (one every ~0.27 us) cannot
+// afford.  The limit is checked every 1024 tries.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_at(uint32_t b, uint32_t parity, unsigned* status) {
+  // units of 2^20 cycles, so that a 32-bit clock serves
+  unsigned start = 0;
+#pragma unroll 1
+  for (unsigned i = 0;; ++i) {
+    if (mbar_try(b, parity)) return true;
+    if ((i & 1023) != 1023) continue;
+    const unsigned now = (unsigned)(clock64() >> 20);
+    if (i == 1023) start = now;
+    if (now - start > (unsigned)(kWaitLimitCycles >> 20)) {
+      atomicOr(status, kStatusWaitTimeout);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsigned* status) {
+  return mbar_wait_at(smem_u32(bar), parity, status);
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Arrive on a barrier of the cluster (an address from map_to_cta).  The
+// arrival orders tensor-memory reads only (complete, and fenced with
+// tcgen05.fence::before_thread_sync), so it needs no cluster-scope release: that
+// waits for every outstanding memory operation of the thread, about 1 us.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// 2D tiled store of the box at (c0, c1) from shared memory, in this thread's
+// bulk group; what lies outside the tensor is not written.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Four bytes to shared memory, asynchronously; zeros when `there` is false.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+// One of the barrier's expected arrivals when this thread's cp.async copies so far are done.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// The warp's index as a value the compiler knows to be the same in all lanes:
+// the roles' loops then run on the uniform datapath, which the tensor-core
+// instructions take their operands from.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0); }
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+
+// Instruction descriptor of kind::f8f6f4: E4M3 A and B, both K-major, FP32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// Operand descriptor of a K-major tile of 128-byte rows in the 128-byte
+// swizzle (8-row groups 1024 bytes apart).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) { return umma_smem_desc(addr, 16, 1024, 2); }
+template <int kGroup>
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  if constexpr (kGroup == 2)
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+  else
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// One arrival on the barrier at this offset in both CTAs of the pair when
+// every MMA this thread issued so far is complete.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Whole warp: consecutive columns of the lane into registers, complete on
+// return.  (The load and its wait are one statement: with loads in flight
+// across statements the compiler kept moving their registers, and the sum
+// loop ran at half its speed.)
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
+        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, "
+      "%45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+      "%62, %63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
+        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=r"(v[32]), "=r"(v[33]), "=r"(v[34]),
+        "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]), "=r"(v[41]),
+        "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]),
+        "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
+        "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]),
+        "=r"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Scaled accumulation, two FP32 values at a time
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pack2(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) { return pair_to_bf16x2(v); }
+
+}  // namespace fp8
+}  // namespace nvfp4
