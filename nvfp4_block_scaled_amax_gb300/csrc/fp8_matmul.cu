@@ -224,7 +224,6 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     const int q = w & 3, half = (w - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + half * 128;
     const uint32_t tempty0 = map_to_cta(smem_u32(&bar->tempty[0]), 0);
-    const int64_t pitch = p.b_rows;
     const uint32_t box = smem_u32(out_stage + (w - 4) * kOutBoxes * kOutBox);
     uint32_t boxes = 0;
     // Shared-memory addresses of what the loop touches.
@@ -305,60 +304,61 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       if (!ok) break;
       // The 32 rows of this warp go out through shared memory, 128 bytes of
       // each row at a time, stored by TMA while the next tile is summed.  Rows
-      // that end inside another member's, or rows whose pitch TMA cannot take,
-      // are written directly.
+      // past a member's end, and rows whose pitch TMA cannot take, are written
+      // by the warp itself, a row at a time.
       const int row0 = 128 * (int)rank + 32 * q, c0 = 128 * half;
       if (row0 >= tl.rows || c0 >= tl.cols) continue;
-      if (p.out_map && row0 + 32 <= tl.rows) {
-        auto put = [&](const uint32_t (&word)[32], int c) {  // 128 bytes of the lane's row, from column c of the tile
-          const uint32_t dst = box + (boxes % kOutBoxes) * kOutBox;
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBoxes - 1) : "memory");
-          __syncwarp();
+      const bool by_tma = p.out_map && row0 + 32 <= tl.rows;
+      auto put = [&](const uint32_t (&word)[32], int c) {  // 128 bytes of the lane's row, from column c of the tile
+        if (c >= tl.cols) return;
+        const uint32_t src = box + (boxes % kOutBoxes) * kOutBox;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBoxes - 1) : "memory");
+        __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            sts_v4(dst + lane * 128 + ((j ^ (lane & 7)) * 16), word[4 * j], word[4 * j + 1], word[4 * j + 2],
-                   word[4 * j + 3]);
+        for (int j = 0; j < 8; ++j)
+          sts_v4(src + lane * 128 + ((j ^ (lane & 7)) * 16), word[4 * j], word[4 * j + 1], word[4 * j + 2],
+                 word[4 * j + 3]);
+        ++boxes;
+        if (by_tma) {
           fence_proxy_async_shared();
           __syncwarp();
-          if (lane == 0) {
-            if (c < tl.cols) tma_store(&omap, dst, (int32_t)(tl.n0 + c), (int32_t)(tl.out_row + row0));
-            bulk_commit();
-          }
-          ++boxes;
-        };
-        uint32_t word[32];
-        if (p.out_bf16) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(word[i]) : "f"(acc[64 * g + 2 * i + 1]), "f"(acc[64 * g + 2 * i]));
-            put(word, c0 + 64 * g);
-          }
+          if (lane == 0) tma_store(&omap, src, (int32_t)(tl.n0 + c), (int32_t)(tl.out_row + row0));
         } else {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) word[i] = __float_as_uint(acc[32 * g + i]);
-            put(word, c0 + 32 * g);
+          __syncwarp();
+          const int rows = min(32, tl.rows - row0);
+          for (int r = 0; r < rows; ++r) {
+            uint32_t x;
+            asm volatile("ld.shared.u32 %0, [%1];"
+                         : "=r"(x)
+                         : "r"(src + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4)
+                         : "memory");
+            const int64_t at = (tl.out_row + row0 + r) * p.b_rows + tl.n0 + c;
+            if (p.out_bf16) {
+              uint16_t* dst = static_cast<uint16_t*>(p.out) + at + 2 * lane;
+              if (c + 2 * lane < tl.cols) dst[0] = (uint16_t)x;
+              if (c + 2 * lane + 1 < tl.cols) dst[1] = (uint16_t)(x >> 16);
+            } else if (c + lane < tl.cols) {
+              static_cast<uint32_t*>(p.out)[at + lane] = x;
+            }
           }
         }
-      } else if (row0 + lane < tl.rows) {
-        const int64_t at = (tl.out_row + row0 + lane) * pitch + tl.n0 + c0;
-        const int n = tl.cols - c0;
-        if (p.out_bf16) {
-          uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
+        if (lane == 0) bulk_commit();  // a group of its own (empty if the warp wrote)
+      };
+      uint32_t word[32];
+      if (p.out_bf16) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) {
-            uint16_t h;
-            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(acc[i]));
-            if (i < n) dst[i] = h;
-          }
-        } else {
-          float* dst = static_cast<float*>(p.out) + at;
+        for (int g = 0; g < 2; ++g) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i < n) dst[i] = acc[i];
+          for (int i = 0; i < 32; ++i)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(word[i]) : "f"(acc[64 * g + 2 * i + 1]), "f"(acc[64 * g + 2 * i]));
+          put(word, c0 + 64 * g);
+        }
+      } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) word[i] = __float_as_uint(acc[32 * g + i]);
+          put(word, c0 + 32 * g);
         }
       }
     }
@@ -371,6 +371,29 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   if (w == 1) tmem_dealloc_pair(tmem, 512);
 }
 
+// Which of the two kernels a product runs on.  Up to 64 rows per member the
+// thin kernel's tiles fit and it is ahead everywhere (5120 x 4096 weights, 1 /
+// 16 / 64 rows: 7.9 / 8.7 / 13.0 us against 16.6 / 18.2 / 16.3).  Above, the
+// estimated times decide, in us, fitted to both kernels measured at 96 to 512
+// rows, N 1024 to 5120, K 1024 and 4096: a start, then the blocks that each
+// CTA or pair sums one after another.  For instance, thin against pair at 128
+// rows: N 1024, K 4096 10.8 / 16.7; N 5120, K 4096 19.2 / 16.9; N = K = 1024
+// 12.6 / 8.9.
+bool thin_is_faster(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
+  const int64_t members = a.offsets ? a.experts : 1;
+  const int64_t rows = a.wgrad ? a.a_rows : (a.a_rows + members - 1) / members;
+  if (rows <= 64) return true;
+  const int64_t k = a.wgrad ? (a.a_cols + members - 1) / members : a.a_cols;
+  const double kb = (double)((k + kBK - 1) / kBK);
+  const int64_t pair_tiles = members * ((rows + 255) / 256) * ((a.b_rows + 255) / 256);
+  const int64_t pair_turns = (pair_tiles + ctx.num_sms / 2 - 1) / (ctx.num_sms / 2);
+  const double pair = 4.5 + pair_turns * kb * (a.b_block_rows == 1 ? 0.78 : 0.38);
+  const ThinPlan t = thin_plan(a, ctx);
+  const int64_t thin_turns = (t.tiles * t.split + 2 * ctx.num_sms - 1) / (2 * ctx.num_sms);
+  const double thin = 6.0 + (t.split > 1 ? 3.5 : 0.0) + thin_turns * kb / t.split * 0.45;
+  return thin < pair;
+}
+
 }  // namespace
 }  // namespace fp8
 
@@ -380,15 +403,7 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   const int64_t out_rows = a.wgrad ? a.a_rows * a.experts : a.a_rows;
   if (a.a_cols == 0)
     return cudaMemsetAsync(a.out, 0, (size_t)out_rows * a.b_rows * (a.out_bf16 ? 2 : 4), ctx.stream);
-  CUtensorMap amap, bmap, omap = {};
-  cudaError_t e = make_fp8_tensor_map(&amap, a.a, a.a_rows, a.a_cols, 128);
-  if (e != cudaSuccess) return e;
-  e = make_fp8_tensor_map(&bmap, a.b, a.wgrad ? a.b_rows : a.b_rows * a.experts, a.a_cols, 128);
-  if (e != cudaSuccess) return e;
   MatmulKernelArgs p = {};
-  // TMA writes the output where its rows start on 16 bytes.
-  p.out_map = a.b_rows * (a.out_bf16 ? 2 : 4) % 16 == 0;
-  if (p.out_map && (e = make_matmul_out_map(&omap, a.out, a.out_bf16, out_rows, a.b_rows)) != cudaSuccess) return e;
   p.sa = a.sa;
   p.sb = a.sb;
   p.a_rows = a.a_rows;
@@ -401,6 +416,15 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   p.out = a.out;
   p.out_bf16 = a.out_bf16;
   p.status = ctx.status;
+  if (thin_is_faster(a, ctx)) return launch_matmul_thin(a, p, ctx);
+  CUtensorMap amap, bmap, omap = {};
+  cudaError_t e = make_fp8_tensor_map(&amap, a.a, a.a_rows, a.a_cols, 128);
+  if (e != cudaSuccess) return e;
+  e = make_fp8_tensor_map(&bmap, a.b, a.wgrad ? a.b_rows : a.b_rows * a.experts, a.a_cols, 128);
+  if (e != cudaSuccess) return e;
+  // TMA writes the output where its rows start on 16 bytes.
+  p.out_map = a.b_rows * (a.out_bf16 ? 2 : 4) % 16 == 0;
+  if (p.out_map && (e = make_matmul_out_map(&omap, a.out, a.out_bf16, out_rows, a.b_rows)) != cudaSuccess) return e;
   // No more tiles than this, whatever the offsets.
   const int64_t tn = (a.b_rows + 255) / 256, tm = (a.a_rows + 255) / 256;
   const int64_t tiles = tn * (a.wgrad ? tm * a.experts : tm + (a.offsets ? a.experts : 0));

@@ -200,6 +200,28 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, 
                "r"(c0), "r"(c1), "r"(src)
                : "memory");
 }
+// For data written to the cluster's shared memory: the arrival that publishes
+// it and the wait that sees it.
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, unsigned* status) {
+  const long long t0 = clock64();
+  uint32_t ok = 0;
+  while (!ok) {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (!ok && clock64() - t0 > kWaitLimitCycles) {
+      atomicOr(status, kStatusWaitTimeout);
+      return false;
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -345,6 +367,15 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t both(float v) { return pack2(__float_as_uint(v), __float_as_uint(v)); }
 __device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) { return pair_to_bf16x2(v); }
+
+// fp8_matmul_thin.cu: how it would cut a product (rows of A per tile, tiles
+// expected, CTAs that share a tile's blocks), and the product so cut.
+struct ThinPlan {
+  int bn, split;
+  int64_t tiles;
+};
+ThinPlan thin_plan(const Fp8MatmulArgs& a, const LaunchCtx& ctx);
+cudaError_t launch_matmul_thin(const Fp8MatmulArgs& a, const MatmulKernelArgs& p, const LaunchCtx& ctx);
 
 }  // namespace fp8
 }  // namespace nvfp4
