@@ -430,7 +430,8 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   const int64_t tiles = tn * (a.wgrad ? tm * a.experts : tm + (a.offsets ? a.experts : 0));
   const unsigned pairs = (unsigned)(tiles < ctx.num_sms / 2 ? tiles : ctx.num_sms / 2);
   const auto kernel = a.b_block_rows == 1 ? matmul_pair_kernel<true> : matmul_pair_kernel<false>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  static std::atomic<uint64_t> allowed[2];
+  e = allow_smem(reinterpret_cast<const void*>(kernel), kSmemBytes, allowed[a.b_block_rows == 1]);
   if (e != cudaSuccess) return e;
   kernel<<<2 * pairs, kThreads, kSmemBytes, ctx.stream>>>(amap, bmap, omap, p);
   return cudaGetLastError();

@@ -340,7 +340,8 @@ cudaError_t launch(const Fp8MatmulArgs& a, const MatmulKernelArgs& p, int64_t ti
   if (stages > kMaxStages) stages = kMaxStages;
   const int smem = rest + stages * L::kStageBytes;
   const auto kernel = a.b_block_rows == 1 ? matmul_thin_kernel<kBN, true> : matmul_thin_kernel<kBN, false>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPerCta);
+  static std::atomic<uint64_t> allowed[2];
+  e = allow_smem(reinterpret_cast<const void*>(kernel), kPerCta, allowed[a.b_block_rows == 1]);
   if (e != cudaSuccess) return e;
   const int64_t room = 2 * ctx.num_sms / split;
   cudaLaunchConfig_t cfg = {};

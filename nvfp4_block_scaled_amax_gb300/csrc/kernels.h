@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace nvfp4 {
 
 // Launches `func` so that it may start while the preceding kernel on the
@@ -26,6 +28,19 @@ inline cudaError_t launch_pdl(const void* func, dim3 grid, dim3 block, size_t sm
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelExC(&cfg, func, args);
+}
+
+// Lets `func` use `bytes` of dynamic shared memory on the current device, once
+// per device (`allowed`: the devices where it is done, one bit each).
+inline cudaError_t allow_smem(const void* func, int bytes, std::atomic<uint64_t>& allowed) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (allowed.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 struct LaunchCtx {

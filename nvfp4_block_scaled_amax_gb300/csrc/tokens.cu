@@ -125,19 +125,86 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
 }
 
 // ---------------------------------------------------------------------------
-constexpr int kRowThreads = 128;
+// Gather: one pass over the tokens by bulk copies.  Each of a CTA's warps
+// streams pieces of tokens (up to 8 KB) through its own ring in shared memory:
+// one load per piece, then a store per kept slot, no register in between, so
+// a token is read once however many rows it goes to.  Rows without a slot
+// are stored from a zeroed piece.  Memory-bound.
+constexpr int kPiece = 8192;
+constexpr int kGatherWarps = 4;
+constexpr int kGatherRing = 6;    // pieces per warp
+constexpr int kGatherAhead = 4;   // loads in flight
+constexpr int kGatherSmem = kPiece * (kGatherWarps * kGatherRing + 1);
 
-// One CTA per row, 16 bytes per thread and step.
-__global__ void __launch_bounds__(kRowThreads) gather_kernel(const uint4* x, uint4* out, TokenArgs a, int vecs) {
+__global__ void __launch_bounds__(32 * kGatherWarps, 1)
+gather_kernel(const uint8_t* x, uint8_t* out, TokenArgs a, int64_t row_bytes, unsigned* status) {
+  extern __shared__ __align__(128) uint8_t pieces[];
+  __shared__ uint64_t loaded[kGatherWarps][kGatherRing];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* zeros = pieces + kPiece * kGatherWarps * kGatherRing;
+  for (int i = threadIdx.x; i < kPiece / 16; i += 32 * kGatherWarps)
+    reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
+  if (lane == 0)
+    for (int i = 0; i < kGatherRing; ++i) mbar_init(&loaded[w][i], 1);
+  fence_proxy_async_shared();
+  __syncthreads();
   grid_dependency_wait();
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const int slot = a.slot_of_row[r];
-    const bool there = slot >= 0 && slot < a.tokens * a.topk;
-    const uint4* src = x + (there ? slot / a.topk : 0) * (int64_t)vecs;
-    for (int i = threadIdx.x; i < vecs; i += kRowThreads)
-      out[r * vecs + i] = there ? src[i] : make_uint4(0, 0, 0, 0);
+  const int64_t slots = a.tokens * a.topk;
+  const int parts = (int)((row_bytes + kPiece - 1) / kPiece);
+  const int64_t warp = (int64_t)blockIdx.x * kGatherWarps + w, warps = (int64_t)gridDim.x * kGatherWarps;
+  const int64_t items = a.tokens * parts;
+  const int64_t mine = items > warp ? (items - warp + warps - 1) / warps : 0;  // items warp, warp + warps, ...
+  const uint32_t ring = smem_u32(pieces + w * kGatherRing * kPiece);
+  auto load = [&](int64_t i) {
+    const int64_t item = warp + i * warps, t = item / parts, off = (item - t * parts) * kPiece;
+    const uint32_t n = (uint32_t)min((int64_t)kPiece, row_bytes - off);
+    uint64_t* bar = &loaded[w][i % kGatherRing];
+    mbar_arrive_expect_tx(bar, n);
+    bulk_load(ring + (uint32_t)(i % kGatherRing) * kPiece, x + t * row_bytes + off, n, bar);
+  };
+  // Lane j stores slot j of the token (and j + 32); its row is looked up one
+  // piece ahead.
+  auto row_at = [&](int64_t i, int j) {
+    return i < mine && j < a.topk ? a.row_of_slot[(warp + i * warps) / parts * a.topk + j] : -1;
+  };
+  if (lane == 0)
+    for (int64_t i = 0; i < min((int64_t)kGatherAhead, mine); ++i) load(i);
+  int next = row_at(0, lane);
+  int64_t i = 0;
+  for (; i < mine; ++i) {
+    const int64_t item = warp + i * warps, off = (item % parts) * kPiece;
+    const uint32_t n = (uint32_t)min((int64_t)kPiece, row_bytes - off);
+    const uint32_t src = ring + (uint32_t)(i % kGatherRing) * kPiece;
+    const int row = next, row2 = row_at(i, lane + 32);
+    next = row_at(i + 1, lane);
+    if (!mbar_wait_bounded(&loaded[w][i % kGatherRing], (uint32_t)(i / kGatherRing) & 1, status)) break;
+    if (row >= 0 && row < a.rows) bulk_store(out + row * row_bytes + off, src, n);
+    if (row2 >= 0 && row2 < a.rows) bulk_store(out + row2 * row_bytes + off, src, n);
+    bulk_commit();
+    // The piece that the next load overwrites was stored kGatherRing -
+    // kGatherAhead items ago.
+    if (i + kGatherAhead < mine) {
+      asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kGatherRing - kGatherAhead) : "memory");
+      __syncwarp();
+      if (lane == 0) load(i + kGatherAhead);
+    }
   }
+  if (i < mine)  // given up: let the copies in flight land
+    for (int64_t k = i + 1; k < min(i + kGatherAhead, mine); ++k)
+      mbar_wait_bounded(&loaded[w][k % kGatherRing], (uint32_t)(k / kGatherRing) & 1, status);
+  __syncwarp();
+  for (int64_t r0 = warp * 32; r0 < a.rows; r0 += warps * 32) {
+    const int64_t r = r0 + lane;
+    const int slot = r < a.rows ? a.slot_of_row[r] : 0;
+    if (r < a.rows && (slot < 0 || slot >= slots))
+      for (int64_t off = 0; off < row_bytes; off += kPiece)
+        bulk_store(out + r * row_bytes + off, smem_u32(zeros), (uint32_t)min((int64_t)kPiece, row_bytes - off));
+  }
+  bulk_commit();
+  bulk_wait_all();
 }
+
+constexpr int kRowThreads = 128;
 
 template <bool kBf16>
 __device__ __forceinline__ void unpack(const uint4& v, float (&f)[kBf16 ? 8 : 4]) {
@@ -167,72 +234,104 @@ __device__ __forceinline__ uint4 pack(const float (&f)[kBf16 ? 8 : 4]) {
 
 // One CTA per token: y = sum_j w_j rows[row_j], j ascending, in FP32, rounded
 // once.  A slot without a row is skipped, so what its row might hold (or
-// what its weight is) does not matter.
+// what its weight is) does not matter.  Four rows are read before the first
+// is added; memory-bound.
 template <bool kBf16>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const uint4* rows, uint4* y, TokenArgs a, int vecs) {
   constexpr int kN = kBf16 ? 8 : 4;
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    const int32_t* at = a.row_of_slot + t * a.topk;
+    const float* wt = a.weights ? a.weights + t * a.topk : nullptr;
     for (int i = threadIdx.x; i < vecs; i += kRowThreads) {
       float acc[kN] = {};
-      for (int j = 0; j < a.topk; ++j) {
-        const int r = a.row_of_slot[t * a.topk + j];
-        if (r < 0 || r >= a.rows) continue;
-        const float w = a.weights ? a.weights[t * a.topk + j] : 1.0f;
-        float v[kN];
-        unpack<kBf16>(rows[(int64_t)r * vecs + i], v);
+      for (int j0 = 0; j0 < a.topk; j0 += 4) {
+        uint4 v[4];
+        float w[4];
+        bool there[4];
 #pragma unroll
-        for (int c = 0; c < kN; ++c) acc[c] = __fmaf_rn(w, v[c], acc[c]);
+        for (int j = 0; j < 4; ++j) {
+          const int r = j0 + j < a.topk ? at[j0 + j] : -1;
+          there[j] = r >= 0 && r < a.rows;
+          if (there[j]) {
+            v[j] = __ldcs(rows + (int64_t)r * vecs + i);
+            w[j] = wt ? wt[j0 + j] : 1.0f;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (!there[j]) continue;
+          float f[kN];
+          unpack<kBf16>(v[j], f);
+#pragma unroll
+          for (int c = 0; c < kN; ++c) acc[c] = __fmaf_rn(w[j], f[c], acc[c]);
+        }
       }
-      y[t * vecs + i] = pack<kBf16>(acc);
+      __stcs(y + t * vecs + i, pack<kBf16>(acc));
     }
   }
 }
 
-// One CTA per token: dy_t is read once, each of its rows gets w dy, and the
-// dot products are summed per thread, then over the warp by halving
-// distances, then over the warps in order.  CTAs past the tokens zero the
-// rows that have no slot.
+// One CTA per token, one pass: dy_t is read once per four of its rows, each
+// row gets w dy, and the dot products are summed per thread, then over the
+// warp by halving distances, then over the warps in order.  CTAs past the
+// tokens zero the rows that have no slot.
 template <bool kBf16>
 __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const uint4* dy, const uint4* rows, uint4* drows,
                                                                    float* dweights, TokenArgs a, int vecs) {
   constexpr int kN = kBf16 ? 8 : 4;
-  __shared__ float part[kRowThreads / 32];
+  __shared__ float part[kRowThreads / 32][4];
   if (blockIdx.x >= a.tokens) {
     const int64_t r0 = (blockIdx.x - a.tokens) * 32;
-    for (int64_t r = r0; r < min(r0 + 32, a.rows); ++r) {
-      const int slot = a.slot_of_row[r];
-      if (slot >= 0 && slot < a.tokens * a.topk) continue;
-      for (int i = threadIdx.x; i < vecs; i += kRowThreads) drows[r * vecs + i] = make_uint4(0, 0, 0, 0);
+    const int mine = r0 + (threadIdx.x & 31) < a.rows ? a.slot_of_row[r0 + (threadIdx.x & 31)] : 0;
+    unsigned empty = __ballot_sync(0xFFFFFFFFu, mine < 0 || mine >= a.tokens * a.topk);
+    for (; empty; empty &= empty - 1) {
+      uint4* dst = drows + (r0 + __ffs(empty) - 1) * vecs;
+      for (int i = threadIdx.x; i < vecs; i += kRowThreads) __stcs(dst + i, make_uint4(0, 0, 0, 0));
     }
     return;
   }
   const int64_t t = blockIdx.x;
-  for (int j = 0; j < a.topk; ++j) {
-    const int r = a.row_of_slot[t * a.topk + j];
-    const bool there = r >= 0 && r < a.rows;
-    const float w = a.weights ? a.weights[t * a.topk + j] : 1.0f;
-    float dot = 0.0f;
-    if (there) {
-      for (int i = threadIdx.x; i < vecs; i += kRowThreads) {
-        float g[kN], v[kN];
-        unpack<kBf16>(dy[t * vecs + i], g);
-        unpack<kBf16>(rows[(int64_t)r * vecs + i], v);
+  const int32_t* at = a.row_of_slot + t * a.topk;
+  for (int j0 = 0; j0 < a.topk; j0 += 4) {
+    int r[4];
+    float w[4], dot[4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r[j] = j0 + j < a.topk ? at[j0 + j] : -1;
+      if (r[j] >= a.rows) r[j] = -1;
+      w[j] = a.weights && j0 + j < a.topk ? a.weights[t * a.topk + j0 + j] : 1.0f;
+    }
+    for (int i = threadIdx.x; i < vecs; i += kRowThreads) {
+      float g[kN];
+      uint4 v[4];
+      unpack<kBf16>(dy[t * vecs + i], g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r[j] >= 0) v[j] = __ldcs(rows + (int64_t)r[j] * vecs + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (r[j] < 0) continue;
+        float f[kN], d[kN];
+        unpack<kBf16>(v[j], f);
 #pragma unroll
         for (int c = 0; c < kN; ++c) {
-          dot = __fmaf_rn(g[c], v[c], dot);
-          g[c] = __fmul_rn(w, g[c]);
+          dot[j] = __fmaf_rn(g[c], f[c], dot[j]);
+          d[c] = __fmul_rn(w[j], g[c]);
         }
-        drows[(int64_t)r * vecs + i] = pack<kBf16>(g);
+        __stcs(drows + (int64_t)r[j] * vecs + i, pack<kBf16>(d));
       }
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) dot = __fadd_rn(dot, __shfl_xor_sync(0xFFFFFFFFu, dot, d));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) dot[j] = __fadd_rn(dot[j], __shfl_xor_sync(0xFFFFFFFFu, dot[j], d));
+      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][j] = dot[j];
+    }
     __syncthreads();
-    if (threadIdx.x == 0 && dweights != nullptr) {
-      float sum = part[0];
-      for (int i = 1; i < kRowThreads / 32; ++i) sum = __fadd_rn(sum, part[i]);
-      dweights[t * a.topk + j] = sum;
+    if (threadIdx.x < 4 && j0 + (int)threadIdx.x < a.topk && dweights != nullptr) {
+      float sum = part[0][threadIdx.x];
+      for (int i = 1; i < kRowThreads / 32; ++i) sum = __fadd_rn(sum, part[i][threadIdx.x]);
+      dweights[t * a.topk + j0 + threadIdx.x] = sum;
     }
     __syncthreads();
   }
@@ -282,16 +381,23 @@ cudaError_t launch_sort_tokens(const SortArgs& args, const LaunchCtx& ctx) {
 cudaError_t launch_gather_tokens(const void* x, void* out, const TokenArgs& args, bool pdl, const LaunchCtx& ctx) {
   TokenArgs a = args;
   if (a.rows == 0 || a.width == 0) return cudaSuccess;
-  int vecs = (int)(a.width * (a.bf16 ? 2 : 4) / 16);
-  const uint4* xv = static_cast<const uint4*>(x);
-  uint4* ov = static_cast<uint4*>(out);
-  const int64_t grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
+  int64_t row_bytes = a.width * (a.bf16 ? 2 : 4);
+  const uint8_t* xv = static_cast<const uint8_t*>(x);
+  uint8_t* ov = static_cast<uint8_t*>(out);
+  unsigned* status = ctx.status;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&gather_kernel), kGatherSmem, allowed);
+  if (e != cudaSuccess) return e;
+  // every warp has a piece to copy, or rows to look at
+  const int64_t items = a.tokens * ((row_bytes + kPiece - 1) / kPiece), looks = (a.rows + 31) / 32;
+  const int64_t want = ((items > looks ? items : looks) + kGatherWarps - 1) / kGatherWarps;
+  const unsigned grid = (unsigned)(want < ctx.num_sms ? want : ctx.num_sms);
   if (pdl) {
-    void* p[] = {&xv, &ov, &a, &vecs};
-    return launch_pdl(reinterpret_cast<const void*>(&gather_kernel), dim3((unsigned)grid), dim3(kRowThreads), 0,
+    void* p[] = {&xv, &ov, &a, &row_bytes, &status};
+    return launch_pdl(reinterpret_cast<const void*>(&gather_kernel), dim3(grid), dim3(32 * kGatherWarps), kGatherSmem,
                       ctx.stream, p);
   }
-  gather_kernel<<<(unsigned)grid, kRowThreads, 0, ctx.stream>>>(xv, ov, a, vecs);
+  gather_kernel<<<grid, 32 * kGatherWarps, kGatherSmem, ctx.stream>>>(xv, ov, a, row_bytes, status);
   return cudaGetLastError();
 }
 

@@ -18,7 +18,8 @@ from __future__ import annotations
 
 import torch
 
-from . import COLWISE, ROWWISE, BF16, FP32, _OnDevice, _lib
+from . import BF16, COLWISE, FP32, ROWWISE
+from ._call import call
 
 BLOCK = 128
 CODES = torch.float8_e4m3fn
@@ -63,8 +64,7 @@ def _scale_shape(lead: tuple, rows: int, cols: int, block_rows: int) -> tuple:
     return lead + ((_blocks(cols), rows) if block_rows == 1 else (_blocks(rows), _blocks(cols)))
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+_DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
 
 
 def quantize_fp8(x: torch.Tensor, block_rows: int = 1, rowwise: bool = True, colwise: bool = False) -> FP8Tensor:
@@ -73,48 +73,52 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1, rowwise: bool = True, col
     or 128 x 128 tile (block_rows 128).  colwise: also the cast of each matrix
     transposed, from the same pass over x.  N % 16 == 0; colwise also
     M % 16 == 0."""
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    if len(shape) not in (2, 3):
         raise ValueError("x must be [M, N] or [B, M, N]")
     if not x.is_cuda or not x.is_contiguous():
         raise ValueError("tensors passed to libnvfp4 must be contiguous CUDA tensors")
-    dtype = BF16 if x.dtype == torch.bfloat16 else FP32 if x.dtype == torch.float32 else None
+    dtype = _DTYPES.get(x.dtype)
     if dtype is None:
         raise TypeError(f"quantize_fp8 takes bfloat16 or float32 input, got {x.dtype}")
-    lead, (M, N) = tuple(x.shape[:-2]), x.shape[-2:]
+    lead, (M, N) = tuple(shape[:-2]), shape[-2:]
     dev = x.device
     row = col = None
+    pointers = [None] * 4
     if rowwise:
-        row = FP8Operand(torch.empty(x.shape, dtype=CODES, device=dev),
-                         torch.empty(_scale_shape(lead, M, N, block_rows), dtype=torch.float32, device=dev), block_rows)
+        data = torch.empty(shape, dtype=CODES, device=dev)
+        scale = torch.empty(_scale_shape(lead, M, N, block_rows), dtype=torch.float32, device=dev)
+        row = FP8Operand(data, scale, block_rows)
+        pointers[:2] = data.data_ptr(), scale.data_ptr()
     if colwise:
-        col = FP8Operand(torch.empty(lead + (N, M), dtype=CODES, device=dev),
-                         torch.empty(_scale_shape(lead, N, M, block_rows), dtype=torch.float32, device=dev), block_rows)
-    with _OnDevice(dev):
-        rc = _lib.load().nvfp4_fp8_quantize(
-            x.data_ptr(), dtype, lead[0] if lead else 1, M, N, block_rows,
-            row.data.data_ptr() if row else None, row.scale.data_ptr() if row else None,
-            col.data.data_ptr() if col else None, col.scale.data_ptr() if col else None,
-            (ROWWISE if row else 0) | (COLWISE if col else 0), _stream(dev))
-    _lib.check(rc, "nvfp4_fp8_quantize")
+        data = torch.empty(lead + (N, M), dtype=CODES, device=dev)
+        scale = torch.empty(_scale_shape(lead, N, M, block_rows), dtype=torch.float32, device=dev)
+        col = FP8Operand(data, scale, block_rows)
+        pointers[2:] = data.data_ptr(), scale.data_ptr()
+    call("nvfp4_fp8_quantize", dev, x.data_ptr(), dtype, lead[0] if lead else 1, M, N, block_rows, *pointers,
+         (ROWWISE if rowwise else 0) | (COLWISE if colwise else 0))
     return FP8Tensor(row, col)
 
 
-def _check_operand(name: str, q: FP8Operand, dims: int) -> None:
-    d, s = q.data, q.scale
-    if d.dtype != CODES or s.dtype != torch.float32:
+def _check_operand(name: str, q: FP8Operand, dims: int) -> tuple:
+    """The codes' shape; raises where codes and scales do not fit each other."""
+    d, s, block_rows = q.data, q.scale, q.block_rows
+    shape = d.shape
+    if d.dtype is not CODES or s.dtype is not torch.float32:
         raise TypeError(f"{name}: float8_e4m3fn codes and float32 scales, got {d.dtype} and {s.dtype}")
-    if d.dim() != dims:
-        raise ValueError(f"{name}: codes with {dims} dimensions, got {tuple(d.shape)}")
-    if q.block_rows not in (1, BLOCK):
-        raise ValueError(f"{name}: block_rows 1 or {BLOCK}, got {q.block_rows}")
+    if len(shape) != dims:
+        raise ValueError(f"{name}: codes with {dims} dimensions, got {tuple(shape)}")
+    if block_rows != 1 and block_rows != BLOCK:
+        raise ValueError(f"{name}: block_rows 1 or {BLOCK}, got {block_rows}")
     if not (d.is_cuda and s.is_cuda and d.is_contiguous() and s.is_contiguous()):
         raise ValueError("tensors passed to libnvfp4 must be contiguous CUDA tensors")
+    *lead, rows, cols = shape
+    if s.shape != _scale_shape(tuple(lead), rows, cols, block_rows):
+        raise ValueError(f"{name}: scales {tuple(s.shape)} do not fit codes {tuple(shape)} with block_rows "
+                         f"{block_rows}")
     if s.device != d.device:
         raise ValueError(f"{name}: codes and scales on one device")
-    shape = d.shape
-    if s.shape != _scale_shape(tuple(shape[:-2]), shape[-2], shape[-1], q.block_rows):
-        raise ValueError(f"{name}: scales {tuple(s.shape)} do not fit codes {tuple(shape)} with block_rows "
-                         f"{q.block_rows}")
+    return shape
 
 
 def _output(out: torch.Tensor | None, shape: tuple, dtype: torch.dtype, dev: torch.device) -> tuple:
@@ -122,21 +126,22 @@ def _output(out: torch.Tensor | None, shape: tuple, dtype: torch.dtype, dev: tor
         out = torch.empty(shape, dtype=dtype, device=dev)
     elif out.shape != shape or out.device != dev or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {shape} tensor on {dev}")
-    code = BF16 if out.dtype == torch.bfloat16 else FP32 if out.dtype == torch.float32 else None
+    code = _DTYPES.get(out.dtype)
     if code is None:
         raise TypeError(f"products are bfloat16 or float32, not {out.dtype}")
     return out, code
 
 
-def _check_pair(a: FP8Operand, b: FP8Operand, b_dims: int) -> None:
-    _check_operand("a", a, 2)
-    _check_operand("b", b, b_dims)
+def _check_pair(a: FP8Operand, b: FP8Operand, b_dims: int) -> tuple:
+    a_shape, b_shape = _check_operand("a", a, 2), _check_operand("b", b, b_dims)
     if a.block_rows != 1:
         raise ValueError("a needs block_rows 1")
-    if a.data.shape[-1] != b.data.shape[-1]:
-        raise ValueError(f"the last dimensions of a {tuple(a.data.shape)} and b {tuple(b.data.shape)} differ")
-    if a.data.device != b.data.device:
+    if a_shape[-1] != b_shape[-1]:
+        raise ValueError(f"the last dimensions of a {tuple(a_shape)} and b {tuple(b_shape)} differ")
+    dev = a.data.device
+    if dev != b.data.device:
         raise ValueError("a and b on one device")
+    return a_shape, b_shape, dev
 
 
 def _check_offsets(offsets: torch.Tensor, dev: torch.device) -> None:
@@ -152,15 +157,10 @@ def matmul_fp8(a: FP8Operand, b: FP8Operand, out_dtype: torch.dtype = torch.bflo
 
     a has block_rows 1, b 1 or 128.  Each block of 128 is summed on the tensor
     cores in FP32, scaled, and added in FP32.  K % 16 == 0."""
-    _check_pair(a, b, 2)
-    dev = a.data.device
-    M, K = a.data.shape
-    N = b.data.shape[0]
+    (M, K), (N, _), dev = _check_pair(a, b, 2)
     out, code = _output(out, (M, N), out_dtype, dev)
-    with _OnDevice(dev):
-        rc = _lib.load().nvfp4_fp8_matmul(a.data.data_ptr(), a.scale.data_ptr(), b.data.data_ptr(), b.scale.data_ptr(),
-                                          b.block_rows, M, N, K, out.data_ptr(), code, _stream(dev))
-    _lib.check(rc, "nvfp4_fp8_matmul")
+    call("nvfp4_fp8_matmul", dev, a.data.data_ptr(), a.scale.data_ptr(), b.data.data_ptr(), b.scale.data_ptr(),
+         b.block_rows, M, N, K, out.data_ptr(), code)
     return out
 
 
@@ -169,19 +169,13 @@ def matmul_fp8_grouped(a: FP8Operand, b: FP8Operand, offsets: torch.Tensor,
     """The product by expert: rows offsets[e] .. offsets[e+1] of a [R, K] times
     b[e] transposed, b [E, N, K]; [R, N], zero past offsets[E].  offsets: device
     int32, as ``TokenPlan.offsets`` (any alignment of the members)."""
-    _check_pair(a, b, 3)
-    dev = a.data.device
+    (R, K), (E, N, _), dev = _check_pair(a, b, 3)
     _check_offsets(offsets, dev)
-    R, K = a.data.shape
-    E, N = b.data.shape[:2]
     if offsets.numel() != E + 1:
         raise ValueError(f"{E} experts need {E + 1} offsets, got {offsets.numel()}")
     out, code = _output(out, (R, N), out_dtype, dev)
-    with _OnDevice(dev):
-        rc = _lib.load().nvfp4_fp8_matmul_grouped(a.data.data_ptr(), a.scale.data_ptr(), b.data.data_ptr(),
-                                                  b.scale.data_ptr(), b.block_rows, R, N, K, E, offsets.data_ptr(),
-                                                  out.data_ptr(), code, _stream(dev))
-    _lib.check(rc, "nvfp4_fp8_matmul_grouped")
+    call("nvfp4_fp8_matmul_grouped", dev, a.data.data_ptr(), a.scale.data_ptr(), b.data.data_ptr(), b.scale.data_ptr(),
+         b.block_rows, R, N, K, E, offsets.data_ptr(), out.data_ptr(), code)
     return out
 
 
@@ -191,18 +185,12 @@ def matmul_fp8_grouped_wgrad(a: FP8Operand, b: FP8Operand, offsets: torch.Tensor
     e] transposed, a [N, R] and b [K, R] the column-wise casts of the output
     gradient and the input; [E, N, K], zero for an empty member.  Every offset
     a multiple of 128 (``dispatch_tokens`` with align=128)."""
-    _check_pair(a, b, 2)
+    (N, R), (K, _), dev = _check_pair(a, b, 2)
     if b.block_rows != 1:
         raise ValueError("b needs block_rows 1")
-    dev = a.data.device
     _check_offsets(offsets, dev)
-    N, R = a.data.shape
-    K = b.data.shape[0]
     E = offsets.numel() - 1
     out, code = _output(out, (E, N, K), out_dtype, dev)
-    with _OnDevice(dev):
-        rc = _lib.load().nvfp4_fp8_matmul_grouped_wgrad(a.data.data_ptr(), a.scale.data_ptr(), b.data.data_ptr(),
-                                                        b.scale.data_ptr(), N, K, R, E, offsets.data_ptr(),
-                                                        out.data_ptr(), code, _stream(dev))
-    _lib.check(rc, "nvfp4_fp8_matmul_grouped_wgrad")
+    call("nvfp4_fp8_matmul_grouped_wgrad", dev, a.data.data_ptr(), a.scale.data_ptr(), b.data.data_ptr(),
+         b.scale.data_ptr(), N, K, R, E, offsets.data_ptr(), out.data_ptr(), code)
     return out
