@@ -40,6 +40,12 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, const LaunchCtx& ctx);
 // 128-byte swizzle, zero fill outside.
 cudaError_t make_fp8_tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int box_rows);
 
+// Tensor map of `batch` row-major matrices M x N of `bytes`-byte elements
+// (1: bytes, 2: BF16, 4: FP32), box 128 bytes x 128 rows of one matrix, 128-byte
+// swizzle, zero fill outside the matrix.  Needs a 16-byte aligned base and row
+// pitch.
+cudaError_t make_batch_tensor_map(CUtensorMap* map, const void* p, int bytes, int64_t batch, int64_t M, int64_t N);
+
 // Tensor map of a product [rows][cols] in BF16 or FP32: box 128 bytes x 32
 // rows, 128-byte swizzle.  Needs a 16-byte aligned base and row pitch.
 cudaError_t make_matmul_out_map(CUtensorMap* map, void* out, bool bf16, int64_t rows, int64_t cols);
