@@ -169,8 +169,7 @@ nvfp4_status nvfp4_dispatch_tokens(const void* x, int dtype, int64_t tokens, int
   const SortArgs s =
       sort_args(expert_ids, tokens, topk, num_experts, align, offsets, row_of_slot, slot_of_row, rows, scratch);
   const TokenArgs a = token_args(dtype, tokens, width, topk, rows, row_of_slot, slot_of_row, nullptr);
-  if (launch_sort_tokens(s, ctx) != cudaSuccess) return NVFP4_ERR_CUDA;
-  return status_of(launch_gather_tokens(x, out, a, true, ctx));
+  return status_of(launch_dispatch_tokens(s, x, out, a, ctx));
 }
 
 nvfp4_status nvfp4_combine_tokens(const void* rows_in, int dtype, int64_t tokens, int64_t width, int topk,

@@ -59,6 +59,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
+// Per BF16 half, the larger magnitude (its sign is of no use): one instruction
+// where masking the signs away takes two more on the same pipe.
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // Two FP32 values -> two E4M3 codes, v0 in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float v0, float v1) {
   uint16_t h;
@@ -138,32 +145,33 @@ fp8_cast_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
         uint32_t m = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if (kRow || kTileScale) m = bf16x2_absmax(m, x[i][k]);
-          if (kCol && !kTileScale) cm[k] = bf16x2_absmax(cm[k], x[i][k]);
+          if (kRow || kTileScale) m = larger(m, x[i][k]);
+          if (kCol && !kTileScale) cm[k] = larger(cm[k], x[i][k]);
         }
         // the larger half of rows i and i + 1 side by side in one word
-        m = bf16x2_absmax(m, __byte_perm(m, m, 0x1032));
+        m = larger(m, __byte_perm(m, m, 0x1032));
         if (i & 1) rm[i >> 1] = __byte_perm(rm[i >> 1], m, 0x5410); else rm[i >> 1] = m;
       }
       if (kRow || kTileScale) {
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) rm[k] = bf16x2_absmax(rm[k], __shfl_xor_sync(0xFFFFFFFFu, rm[k], d));
+          for (int k = 0; k < 4; ++k) rm[k] = larger(rm[k], __shfl_xor_sync(0xFFFFFFFFu, rm[k], d));
         if (g == 0) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<float2*>(&row_max[8 * rg + 2 * k]) = make_float2(bf16_lo(rm[k]), bf16_hi(rm[k]));
+            *reinterpret_cast<float2*>(&row_max[8 * rg + 2 * k]) = make_float2(fabsf(bf16_lo(rm[k])), fabsf(bf16_hi(rm[k])));
         }
       }
       if (kCol && !kTileScale) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) cm[k] = bf16x2_absmax(cm[k], __shfl_xor_sync(0xFFFFFFFFu, cm[k], 16));
+        for (int k = 0; k < 4; ++k) cm[k] = larger(cm[k], __shfl_xor_sync(0xFFFFFFFFu, cm[k], 16));
         if (lane < 16) {
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             *reinterpret_cast<float4*>(&col_max[w][8 * g + 4 * k]) =
-                make_float4(bf16_lo(cm[2 * k]), bf16_hi(cm[2 * k]), bf16_lo(cm[2 * k + 1]), bf16_hi(cm[2 * k + 1]));
+                make_float4(fabsf(bf16_lo(cm[2 * k])), fabsf(bf16_hi(cm[2 * k])), fabsf(bf16_lo(cm[2 * k + 1])),
+                            fabsf(bf16_hi(cm[2 * k + 1])));
         }
       }
     } else {
@@ -244,25 +252,35 @@ fp8_cast_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
       if constexpr (kBf16) return k & 1 ? bf16_hi(x[i][k >> 1]) : bf16_lo(x[i][k >> 1]);
       else return __uint_as_float(x[i][k]);
     };
-    if constexpr (kRow) {
+    // Four rows at a time, unpacked once for both directions.
+    uint32_t c[8][2];  // [column][rows 0-3, 4-7]
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t c[2];
+    for (int h = 0; h < 2; ++h) {
+      float v[4][8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          c[k] = e4m3x2(__fmul_rn(value(i, 4 * k), rf[i]), __fmul_rn(value(i, 4 * k + 1), rf[i])) |
-                 e4m3x2(__fmul_rn(value(i, 4 * k + 2), rf[i]), __fmul_rn(value(i, 4 * k + 3), rf[i])) << 16;
-        sts_v2(out_row + (8 * rg + i) * 128 + (((g >> 1) ^ i) * 16) + (g & 1) * 8, c[0], c[1]);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = value(4 * h + i, k);
+      if constexpr (kRow) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = rf[4 * h + i];
+          uint32_t q[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            q[k] = e4m3x2(__fmul_rn(v[i][4 * k], f), __fmul_rn(v[i][4 * k + 1], f)) |
+                   e4m3x2(__fmul_rn(v[i][4 * k + 2], f), __fmul_rn(v[i][4 * k + 3], f)) << 16;
+          sts_v2(out_row + (8 * rg + 4 * h + i) * 128 + (((g >> 1) ^ (4 * h + i)) * 16) + (g & 1) * 8, q[0], q[1]);
+        }
+      }
+      if constexpr (kCol) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          c[k][h] = e4m3x2(__fmul_rn(v[0][k], cf[k]), __fmul_rn(v[1][k], cf[k])) |
+                    e4m3x2(__fmul_rn(v[2][k], cf[k]), __fmul_rn(v[3][k], cf[k])) << 16;
       }
     }
     if constexpr (kCol) {
-      uint32_t c[8][2];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          c[k][i] = e4m3x2(__fmul_rn(value(4 * i, k), cf[k]), __fmul_rn(value(4 * i + 1, k), cf[k])) |
-                    e4m3x2(__fmul_rn(value(4 * i + 2, k), cf[k]), __fmul_rn(value(4 * i + 3, k), cf[k])) << 16;
       // Lane g stores its column k ^ (g & 7) in turn k (three rounds of swaps
       // arrange them), so that a turn's stores fall into different banks.
 #pragma unroll

@@ -37,18 +37,31 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, in
 // One CTA per chunk.  Each warp counts its own run of the chunk's slots with
 // match_any (no atomics, so the order inside an expert is the slots' order),
 // the counts become first rows, and a second walk hands the rows out.
-__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, int64_t chunk) {
+//
+// kCopy (few slots): the sort and the gather in one launch.  Every CTA sorts
+// all slots for itself, which costs less than a second launch would, the
+// first one writes the maps, and each copies its share of the rows, a warp
+// per piece of 2 KB.
+constexpr int kCopyPiece = 2048;
+
+template <bool kCopy>
+__global__ void __launch_bounds__(kSortThreads)
+sort_place_kernel(SortArgs a, int64_t chunk, const uint8_t* x, uint8_t* out, int64_t row_bytes, int topk) {
   extern __shared__ int smem[];
-  int* wcnt = smem;                          // [warps][experts]: counts, then the next row of warp and expert
+  int* wcnt = smem;                            // [warps][experts]: counts, then the next row of warp and expert
   int* total = smem + kSortWarps * a.experts;  // [experts]
-  int* first = total + a.experts;            // [experts + 1]: offsets
+  int* first = total + a.experts;              // [experts + 1]: offsets
+  int* map = first + a.experts + 1;            // kCopy: [rows], slot of each row
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nchunks = gridDim.x;
+  const int nchunks = kCopy ? 1 : gridDim.x, self = kCopy ? 0 : blockIdx.x;
+  const bool writes = !kCopy || blockIdx.x == 0;
   if (nchunks > 1) grid_dependency_wait();
   for (int i = threadIdx.x; i < kSortWarps * a.experts; i += kSortThreads) wcnt[i] = 0;
+  if (kCopy)
+    for (int i = threadIdx.x; i < a.rows; i += kSortThreads) map[i] = -1;
   __syncthreads();
   const int64_t seg = chunk / kSortWarps;
-  const int64_t begin = blockIdx.x * chunk + w * seg;
+  const int64_t begin = self * chunk + w * seg;
   const int64_t end = min(begin + seg, a.slots);
   int* mine = wcnt + w * a.experts;
   for (int64_t s0 = begin; s0 < end; s0 += 32) {
@@ -59,24 +72,33 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
     if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
     __syncwarp();
   }
+  if (nchunks > 1)  // a warp per expert: its rows in the earlier chunks and in all of them
+    for (int e = w; e < a.experts; e += kSortWarps) {
+      int before = 0, all = 0;
+      for (int c = lane; c < nchunks; c += 32) {
+        const int v = a.scratch[(int64_t)c * a.experts + e];
+        before += c < self ? v : 0;
+        all += v;
+      }
+      before = __reduce_add_sync(0xFFFFFFFFu, before);
+      all = __reduce_add_sync(0xFFFFFFFFu, all);
+      if (lane == 0) {
+        total[e] = all;
+        first[e] = before;  // for now
+      }
+    }
   __syncthreads();
   for (int e = threadIdx.x; e < a.experts; e += kSortThreads) {
-    int before = 0, all = 0;
+    int all = 0;
     for (int i = 0; i < kSortWarps; ++i) {
       const int c = wcnt[i * a.experts + e];
       wcnt[i * a.experts + e] = all;
       all += c;
     }
-    if (nchunks > 1) {
-      all = 0;
-      for (int c = 0; c < nchunks; ++c) {
-        const int v = a.scratch[(int64_t)c * a.experts + e];
-        before += c < (int)blockIdx.x ? v : 0;
-        all += v;
-      }
+    if (nchunks == 1) {
+      total[e] = all;
+      first[e] = 0;
     }
-    total[e] = all;
-    first[e] = before;  // for now: rows of the earlier chunks
   }
   __syncthreads();
   if (w == 0) {
@@ -110,18 +132,43 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
     if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
     __syncwarp();
     if (s < end) {
-      a.row_of_slot[s] = row;
-      if (row >= 0) a.slot_of_row[row] = (int32_t)s;
+      if (writes) {
+        a.row_of_slot[s] = row;
+        if (row >= 0) a.slot_of_row[row] = (int32_t)s;
+      }
+      if (kCopy && row >= 0) map[row] = (int)s;
     }
   }
-  // rows without a slot: the end of every member and the end of the capacity
-  for (int e = blockIdx.x; e < a.experts; e += nchunks)
-    for (int r = first[e] + total[e] + threadIdx.x; r < first[e + 1]; r += kSortThreads) a.slot_of_row[r] = -1;
-  for (int64_t r = first[a.experts] + (int64_t)blockIdx.x * kSortThreads + threadIdx.x; r < a.rows;
-       r += (int64_t)nchunks * kSortThreads)
-    a.slot_of_row[r] = -1;
-  if (blockIdx.x == 0)
-    for (int e = threadIdx.x; e <= a.experts; e += kSortThreads) a.offsets[e] = first[e];
+  if (writes) {
+    // rows without a slot: the end of every member and the end of the capacity
+    for (int e = self; e < a.experts; e += nchunks)
+      for (int r = first[e] + total[e] + threadIdx.x; r < first[e + 1]; r += kSortThreads) a.slot_of_row[r] = -1;
+    for (int64_t r = first[a.experts] + (int64_t)self * kSortThreads + threadIdx.x; r < a.rows;
+         r += (int64_t)nchunks * kSortThreads)
+      a.slot_of_row[r] = -1;
+    if (self == 0)
+      for (int e = threadIdx.x; e <= a.experts; e += kSortThreads) a.offsets[e] = first[e];
+  }
+  if constexpr (kCopy) {
+    __syncthreads();
+    const int pieces = (int)((row_bytes + kCopyPiece - 1) / kCopyPiece);
+    for (int64_t u = (int64_t)blockIdx.x * kSortWarps + w; u < a.rows * pieces; u += (int64_t)gridDim.x * kSortWarps) {
+      const int64_t r = u / pieces, off = (u - r * pieces) * kCopyPiece;
+      const int slot = map[r], n = (int)min((int64_t)kCopyPiece, row_bytes - off);
+      const uint8_t* src = x + (slot >= 0 ? slot / topk : 0) * row_bytes + off;
+      uint8_t* dst = out + r * row_bytes + off;
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = (lane + 32 * i) * 16;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (slot >= 0 && at < n) v[i] = *reinterpret_cast<const uint4*>(src + at);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((lane + 32 * i) * 16 < n) *reinterpret_cast<uint4*>(dst + (lane + 32 * i) * 16) = v[i];
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -239,31 +286,40 @@ __device__ __forceinline__ uint4 pack(const float (&f)[kBf16 ? 8 : 4]) {
 template <bool kBf16>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const uint4* rows, uint4* y, TokenArgs a, int vecs) {
   constexpr int kN = kBf16 ? 8 : 4;
+  __shared__ int64_t start[64];  // of each kept row, in vectors
+  __shared__ float weight[64];
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-    const int32_t* at = a.row_of_slot + t * a.topk;
-    const float* wt = a.weights ? a.weights + t * a.topk : nullptr;
+    // the kept slots, in order
+    __syncthreads();
+    int kept = 0;
+    for (int j0 = 0; j0 < a.topk; j0 += 32) {  // every warp looks, so that every thread knows how many
+      const int j = j0 + (threadIdx.x & 31);
+      const int r = j < a.topk ? a.row_of_slot[t * a.topk + j] : -1;
+      const bool there = r >= 0 && r < a.rows;
+      const unsigned m = __ballot_sync(0xFFFFFFFFu, there);
+      if (there && threadIdx.x < 32) {
+        const int at = kept + __popc(m & ((1u << threadIdx.x) - 1u));
+        start[at] = (int64_t)r * vecs;
+        weight[at] = a.weights ? a.weights[t * a.topk + j] : 1.0f;
+      }
+      kept += __popc(m);
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < vecs; i += kRowThreads) {
       float acc[kN] = {};
-      for (int j0 = 0; j0 < a.topk; j0 += 4) {
+      for (int j0 = 0; j0 < kept; j0 += 4) {
         uint4 v[4];
-        float w[4];
-        bool there[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j0 + j < kept) v[j] = __ldcs(rows + start[j0 + j] + i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int r = j0 + j < a.topk ? at[j0 + j] : -1;
-          there[j] = r >= 0 && r < a.rows;
-          if (there[j]) {
-            v[j] = __ldcs(rows + (int64_t)r * vecs + i);
-            w[j] = wt ? wt[j0 + j] : 1.0f;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (!there[j]) continue;
+          if (j0 + j >= kept) break;
+          const float w = weight[j0 + j];
           float f[kN];
           unpack<kBf16>(v[j], f);
 #pragma unroll
-          for (int c = 0; c < kN; ++c) acc[c] = __fmaf_rn(w[j], f[c], acc[c]);
+          for (int c = 0; c < kN; ++c) acc[c] = __fmaf_rn(w, f[c], acc[c]);
         }
       }
       __stcs(y + t * vecs + i, pack<kBf16>(acc));
@@ -357,24 +413,51 @@ int64_t sort_scratch_ints(int64_t slots, int experts) {
   return n <= 1 ? 0 : n * experts;
 }
 
+namespace {
+int sort_smem(int experts, int64_t map) { return (int)sizeof(int) * ((kSortWarps + 2) * experts + 1 + (int)map); }
+}  // namespace
+
 cudaError_t launch_sort_tokens(const SortArgs& args, const LaunchCtx& ctx) {
   SortArgs a = args;
-  int64_t chunk = chunk_of(a.slots, ctx.num_sms);
+  int64_t chunk = chunk_of(a.slots, ctx.num_sms), row_bytes = 0;
   const int n = sort_chunks(a.slots, ctx);
-  const size_t smem = sizeof(int) * ((size_t)(kSortWarps + 2) * a.experts + 1);
-  cudaError_t e;
-  if (smem > 48 * 1024 &&
-      (e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
-          cudaSuccess)
-    return e;
+  const int smem = sort_smem(a.experts, 0);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&sort_place_kernel<false>), sort_smem(kMaxExperts, 0), allowed);
+  if (e != cudaSuccess) return e;
+  const uint8_t* x = nullptr;
+  uint8_t* out = nullptr;
+  int topk = 1;
   if (n > 1) {
     sort_count_kernel<<<n, kSortThreads, sizeof(int) * a.experts, ctx.stream>>>(a, chunk);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    void* p[] = {&a, &chunk};
-    return launch_pdl(reinterpret_cast<const void*>(&sort_place_kernel), dim3(n), dim3(kSortThreads), smem, ctx.stream,
-                      p);
+    void* p[] = {&a, &chunk, &x, &out, &row_bytes, &topk};
+    return launch_pdl(reinterpret_cast<const void*>(&sort_place_kernel<false>), dim3(n), dim3(kSortThreads), smem,
+                      ctx.stream, p);
   }
-  sort_place_kernel<<<1, kSortThreads, smem, ctx.stream>>>(a, chunk);
+  sort_place_kernel<false><<<1, kSortThreads, smem, ctx.stream>>>(a, chunk, x, out, row_bytes, topk);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dispatch_tokens(const SortArgs& s, const void* x, void* out, const TokenArgs& t,
+                                   const LaunchCtx& ctx) {
+  // Few slots and rows: one launch (8 tokens of 1024 BF16, top 2: 4.4 + 4.0 us
+  // for the two kernels and a gap between them, against one kernel).
+  const int64_t row_bytes = t.width * (t.bf16 ? 2 : 4);
+  if (s.slots > 1024 || s.rows > 4096 || row_bytes == 0) {
+    const cudaError_t e = launch_sort_tokens(s, ctx);
+    return e != cudaSuccess ? e : launch_gather_tokens(x, out, t, true, ctx);
+  }
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e =
+      allow_smem(reinterpret_cast<const void*>(&sort_place_kernel<true>), sort_smem(kMaxExperts, 4096), allowed);
+  if (e != cudaSuccess) return e;
+  const int64_t units = s.rows * ((row_bytes + kCopyPiece - 1) / kCopyPiece);
+  const int64_t want = (units + kSortWarps - 1) / kSortWarps;
+  const unsigned grid = (unsigned)(want < 1 ? 1 : want < ctx.num_sms ? want : ctx.num_sms);
+  const int64_t chunk = (s.slots + 32 * kSortWarps - 1) / (32 * kSortWarps) * (32 * kSortWarps);
+  sort_place_kernel<true><<<grid, kSortThreads, sort_smem(s.experts, s.rows), ctx.stream>>>(
+      s, chunk, static_cast<const uint8_t*>(x), static_cast<uint8_t*>(out), row_bytes, t.topk);
   return cudaGetLastError();
 }
 

@@ -36,6 +36,9 @@ struct TokenArgs {
 // out[r] = x[slot_of_row[r] / topk], zero where there is no slot.  `pdl`: a
 // programmatic dependent of the sort launched just before.
 cudaError_t launch_gather_tokens(const void* x, void* out, const TokenArgs& a, bool pdl, const LaunchCtx& ctx);
+// The sort, then the gather; in one launch where there are few slots.
+cudaError_t launch_dispatch_tokens(const SortArgs& s, const void* x, void* out, const TokenArgs& t,
+                                   const LaunchCtx& ctx);
 cudaError_t launch_combine_tokens(const void* rows, void* y, const TokenArgs& a, const LaunchCtx& ctx);
 cudaError_t launch_combine_tokens_grad(const void* dy, const void* rows, void* drows, float* dweights,
                                        const TokenArgs& a, const LaunchCtx& ctx);
