@@ -229,8 +229,9 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     // Shared-memory addresses of what the loop touches.
     const uint32_t bsfull = smem_u32(&bar->sfull[0]), bsempty = smem_u32(&bar->sempty[0]);
     const uint32_t btfull = smem_u32(&bar->tfull[0]), btempty = tempty0;
-    const uint32_t sc_row = smem_u32(scales) + 4 * (32 * q + lane), sc_col = smem_u32(scales) + 4 * (128 + 128 * half);
-    const uint32_t sc_blk = smem_u32(scales) + 4 * (128 + half);
+    const uint32_t sc = smem_u32(scales);
+    const uint32_t sc_row = sc + 4 * (32 * q + (kColScales ? lane >> 2 : lane));
+    const uint32_t sc_col = sc + 4 * (128 + (kColScales ? 128 * half + 2 * (lane & 3) : half));
     uint32_t it = 0, batch = 0;
     bool ok = true;
     for (int t = t0; t < tiles && ok
@@ -239,33 +240,6 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-      // Scalar FMAs: the packed form issues at half their rate here and gains nothing.
-      auto add = [&](const uint32_t (&x)[kChunk], int c, uint32_t sb, float scale) {
-#pragma unroll
-        for (int i = 0; i < kChunk; i += 4) {
-          float f[4] = {__uint_as_float(x[i]), __uint_as_float(x[i + 1]), __uint_as_float(x[i + 2]),
-                        __uint_as_float(x[i + 3])};
-          if constexpr (kColScales) {
-            float b[4];
-            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3])
-                         : "r"(sb + 4 * (c + i)));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = __fmul_rn(f[j], b[j]);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[c + i + j] = __fmaf_rn(f[j], scale, acc[c + i + j]);
-        }
-      };
-      float scale = 0.0f;
-      auto load_scale = [&](uint32_t off) {
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(scale) : "r"(sc_row + off));
-        if constexpr (!kColScales) {
-          float sb;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sb) : "r"(sc_blk + off));
-          scale = __fmul_rn(scale, sb);
-        }
-      };
       const int nkb = tl.nkb;
       uint32_t off = 0;  // of the block's scales
 #pragma unroll 1
@@ -276,22 +250,57 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           ok = mbar_wait_at(bsfull + 8 * ss, (batch / kScaleStages) & 1, p.status);
           if (!ok) break;
         }
-        load_scale(off);
+        float sa[kColScales ? 4 : 1];
+        if constexpr (kColScales) {
+          // four rows of the lane: lane / 4 + 8 i
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sa[i]) : "r"(sc_row + off + 32 * i));
+        } else {
+          float sb;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sa[0]) : "r"(sc_row + off));
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sb) : "r"(sc_col + off));
+          sa[0] = __fmul_rn(sa[0], sb);
+        }
         const uint32_t src = lane_base + (it & 1) * kBufCols;
         ok = mbar_wait_at(btfull + 8 * (it & 1), (it >> 1) & 1, p.status);
         if (!ok) break;
         __syncwarp();
         tcgen05_after_sync();
+        // Scalar FMAs: the packed form issues at half their rate and gains nothing.
 #pragma unroll
         for (int c = 0; c < 128; c += kChunk) {
-          uint32_t v[kChunk];
-          tmem_read(src + c, v);
-          if (c == 128 - kChunk) {
-            // everything is read: the accumulator may be overwritten
+          // once everything is read, the accumulator may be overwritten
+          auto release = [&]() {
+            if (c != 128 - kChunk) return;
             tcgen05_before_sync();
             if (lane == 0) mbar_arrive_cluster(btempty + 8 * (it & 1));
+          };
+          if constexpr (kColScales) {
+            uint32_t u[32], v[32];
+            tmem_read_16x256(src + c, u, v);
+            release();
+            // a column's scale serves the lane's four rows
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float sb[2];
+              asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                           : "=f"(sb[0]), "=f"(sb[1])
+                           : "r"(sc_col + off + 4 * (c + 8 * j)));
+              float* to = acc + (c / 8 + j) * 8;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float x = __uint_as_float(i < 4 ? u[4 * j + i] : v[4 * j + i - 4]);
+                to[i] = __fmaf_rn(__fmul_rn(x, sb[i & 1]), sa[i >> 1], to[i]);
+              }
+            }
+          } else {
+            uint32_t v[kChunk];
+            tmem_read(src + c, v);
+            release();
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) acc[c + i] = __fmaf_rn(__uint_as_float(v[i]), sa[0], acc[c + i]);
           }
-          add(v, c, sc_col + off, scale);
         }
         ++it;
         off += 4 * kScaleFloats;
@@ -309,15 +318,12 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       const int row0 = 128 * (int)rank + 32 * q, c0 = 128 * half;
       if (row0 >= tl.rows || c0 >= tl.cols) continue;
       const bool by_tma = p.out_map && row0 + 32 <= tl.rows;
-      auto put = [&](const uint32_t (&word)[32], int c) {  // 128 bytes of the lane's row, from column c of the tile
+      auto put = [&](int c, auto&& fill) {  // 128 bytes of the rows, from column c of the tile
         if (c >= tl.cols) return;
         const uint32_t src = box + (boxes % kOutBoxes) * kOutBox;
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBoxes - 1) : "memory");
         __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          sts_v4(src + lane * 128 + ((j ^ (lane & 7)) * 16), word[4 * j], word[4 * j + 1], word[4 * j + 2],
-                 word[4 * j + 3]);
+        fill(src);
         ++boxes;
         if (by_tma) {
           fence_proxy_async_shared();
@@ -344,22 +350,59 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         }
         if (lane == 0) bulk_commit();  // a group of its own (empty if the warp wrote)
       };
-      uint32_t word[32];
-      if (p.out_bf16) {
+      auto bf16x2 = [](float lo, float hi) {
+        uint32_t h;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+        return h;
+      };
+      // 16-byte places of a row are swizzled by the row, as TMA expects them.
+      if constexpr (kColScales) {
+        const int r0 = lane >> 2, e = lane & 3;  // the lane's rows r0 + 8 i (r0 & 7 = r0), its two columns of eight
+        if (p.out_bf16) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+          for (int g = 0; g < 2; ++g)
+            put(c0 + 64 * g, [&](uint32_t src) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(word[i]) : "f"(acc[64 * g + 2 * i + 1]), "f"(acc[64 * g + 2 * i]));
-          put(word, c0 + 64 * g);
+              for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  sts_u32(src + (r0 + 8 * i) * 128 + ((j ^ r0) * 16) + 4 * e,
+                          bf16x2(acc[(8 * g + j) * 8 + 2 * i], acc[(8 * g + j) * 8 + 2 * i + 1]));
+            });
+        } else {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            put(c0 + 32 * g, [&](uint32_t src) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  sts_v2(src + (r0 + 8 * i) * 128 + (((2 * j + (e >> 1)) ^ r0) * 16) + 8 * (e & 1),
+                         __float_as_uint(acc[(4 * g + j) * 8 + 2 * i]), __float_as_uint(acc[(4 * g + j) * 8 + 2 * i + 1]));
+            });
         }
+      } else if (p.out_bf16) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          put(c0 + 64 * g, [&](uint32_t src) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float* f = acc + 64 * g + 8 * j;
+              sts_v4(src + lane * 128 + ((j ^ (lane & 7)) * 16), bf16x2(f[0], f[1]), bf16x2(f[2], f[3]),
+                     bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
+            }
+          });
       } else {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 4; ++g)
+          put(c0 + 32 * g, [&](uint32_t src) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) word[i] = __float_as_uint(acc[32 * g + i]);
-          put(word, c0 + 32 * g);
-        }
+            for (int j = 0; j < 8; ++j) {
+              const float* f = acc + 32 * g + 4 * j;
+              sts_v4(src + lane * 128 + ((j ^ (lane & 7)) * 16), __float_as_uint(f[0]), __float_as_uint(f[1]),
+                     __float_as_uint(f[2]), __float_as_uint(f[3]));
+            }
+          });
       }
     }
     if (lane == 0) bulk_wait_all();
