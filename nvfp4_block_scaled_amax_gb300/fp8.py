@@ -101,24 +101,28 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1, rowwise: bool = True, col
 
 
 def _check_operand(name: str, q: FP8Operand, dims: int) -> tuple:
-    """The codes' shape; raises where codes and scales do not fit each other."""
+    """(the codes' shape, their device); raises where codes and scales do not fit each other."""
     d, s, block_rows = q.data, q.scale, q.block_rows
-    shape = d.shape
+    shape, dev = d.shape, d.device
     if d.dtype is not CODES or s.dtype is not torch.float32:
         raise TypeError(f"{name}: float8_e4m3fn codes and float32 scales, got {d.dtype} and {s.dtype}")
     if len(shape) != dims:
         raise ValueError(f"{name}: codes with {dims} dimensions, got {tuple(shape)}")
-    if block_rows != 1 and block_rows != BLOCK:
+    rows, cols = shape[-2:]
+    if block_rows == 1:
+        want = ((cols + 127) // BLOCK, rows)
+    elif block_rows == BLOCK:
+        want = ((rows + 127) // BLOCK, (cols + 127) // BLOCK)
+    else:
         raise ValueError(f"{name}: block_rows 1 or {BLOCK}, got {block_rows}")
-    if not (d.is_cuda and s.is_cuda and d.is_contiguous() and s.is_contiguous()):
-        raise ValueError("tensors passed to libnvfp4 must be contiguous CUDA tensors")
-    *lead, rows, cols = shape
-    if s.shape != _scale_shape(tuple(lead), rows, cols, block_rows):
+    if s.shape != (want if dims == 2 else (shape[0], *want)):
         raise ValueError(f"{name}: scales {tuple(s.shape)} do not fit codes {tuple(shape)} with block_rows "
                          f"{block_rows}")
-    if s.device != d.device:
+    if not (d.is_cuda and d.is_contiguous() and s.is_contiguous()):
+        raise ValueError("tensors passed to libnvfp4 must be contiguous CUDA tensors")
+    if s.device != dev:
         raise ValueError(f"{name}: codes and scales on one device")
-    return shape
+    return shape, dev
 
 
 def _output(out: torch.Tensor | None, shape: tuple, dtype: torch.dtype, dev: torch.device) -> tuple:
@@ -133,13 +137,13 @@ def _output(out: torch.Tensor | None, shape: tuple, dtype: torch.dtype, dev: tor
 
 
 def _check_pair(a: FP8Operand, b: FP8Operand, b_dims: int) -> tuple:
-    a_shape, b_shape = _check_operand("a", a, 2), _check_operand("b", b, b_dims)
+    a_shape, dev = _check_operand("a", a, 2)
+    b_shape, b_dev = _check_operand("b", b, b_dims)
     if a.block_rows != 1:
         raise ValueError("a needs block_rows 1")
     if a_shape[-1] != b_shape[-1]:
         raise ValueError(f"the last dimensions of a {tuple(a_shape)} and b {tuple(b_shape)} differ")
-    dev = a.data.device
-    if dev != b.data.device:
+    if dev != b_dev:
         raise ValueError("a and b on one device")
     return a_shape, b_shape, dev
 
