@@ -151,7 +151,7 @@ nvfp4_status nvfp4_gather_tokens(const void* x, int dtype, int64_t tokens, int64
   LaunchCtx ctx;
   if ((st = make_launch_ctx(stream, &ctx)) != NVFP4_OK) return st;
   return status_of(launch_gather_tokens(
-      x, out, token_args(dtype, tokens, width, topk, rows, row_of_slot, slot_of_row, nullptr), false, ctx));
+      x, out, token_args(dtype, tokens, width, topk, rows, row_of_slot, slot_of_row, nullptr), ctx));
 }
 
 nvfp4_status nvfp4_dispatch_tokens(const void* x, int dtype, int64_t tokens, int64_t width,

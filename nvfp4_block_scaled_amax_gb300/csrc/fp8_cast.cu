@@ -93,6 +93,7 @@ fp8_cast_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
     if (kRow) tma_prefetch_desc(&rmap);
     if (kCol) tma_prefetch_desc(&cmap);
   }
+  grid_begin();
   __syncthreads();
   constexpr int kBox = kBf16 ? 64 : 32;  // columns of an input box (128 bytes)
   auto load = [&](int64_t t) {
@@ -322,8 +323,11 @@ cudaError_t launch(const CUtensorMap& x, const CUtensorMap& r, const CUtensorMap
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Smem<kBf16>::kBytes, allowed);
   if (e != cudaSuccess) return e;
   const int64_t room = (int64_t)ctx.num_sms * (kBf16 ? 3 : 2);
-  kernel<<<(unsigned)(k.tiles < room ? k.tiles : room), kThreads, Smem<kBf16>::kBytes, ctx.stream>>>(x, r, c, k);
-  return cudaGetLastError();
+  CUtensorMap maps[3] = {x, r, c};
+  CastKernelArgs args = k;
+  void* p[] = {&maps[0], &maps[1], &maps[2], &args};
+  return launch_pdl(reinterpret_cast<const void*>(kernel), dim3((unsigned)(k.tiles < room ? k.tiles : room)),
+                    dim3(kThreads), Smem<kBf16>::kBytes, ctx.stream, p);
 }
 
 template <bool kBf16, bool kTileScale>

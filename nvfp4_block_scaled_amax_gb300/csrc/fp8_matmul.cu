@@ -91,9 +91,9 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     }
   } else if (w == 1) {
     tmem_alloc_pair(&bar->tmem, 512);
-  } else if (w == 2) {
-    Tiles::fill(p, first);
   }
+  grid_begin();
+  if (w == 2) Tiles::fill(p, first);
   tcgen05_before_sync();
   __syncthreads();
   cluster_sync();
@@ -485,8 +485,8 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   static std::atomic<uint64_t> allowed[2];
   e = allow_smem(reinterpret_cast<const void*>(kernel), kSmemBytes, allowed[a.b_block_rows == 1]);
   if (e != cudaSuccess) return e;
-  kernel<<<2 * pairs, kThreads, kSmemBytes, ctx.stream>>>(amap, bmap, omap, p);
-  return cudaGetLastError();
+  void* args[] = {&amap, &bmap, &omap, &p};
+  return launch_pdl(reinterpret_cast<const void*>(kernel), dim3(2 * pairs), dim3(kThreads), kSmemBytes, ctx.stream, args);
 }
 
 }  // namespace nvfp4

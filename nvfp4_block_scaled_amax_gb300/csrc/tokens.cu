@@ -23,6 +23,7 @@ constexpr int kSortChunk = 2048;  // slots of one CTA, as long as there are no m
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, int64_t chunk) {
   extern __shared__ int cnt[];
   for (int e = threadIdx.x; e < a.experts; e += kSortThreads) cnt[e] = 0;
+  grid_begin();
   __syncthreads();
   const int64_t begin = blockIdx.x * chunk, end = min(begin + chunk, a.slots);
   for (int64_t s = begin + threadIdx.x; s < end; s += kSortThreads) {
@@ -55,10 +56,10 @@ sort_place_kernel(SortArgs a, int64_t chunk, const uint8_t* x, uint8_t* out, int
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nchunks = kCopy ? 1 : gridDim.x, self = kCopy ? 0 : blockIdx.x;
   const bool writes = !kCopy || blockIdx.x == 0;
-  if (nchunks > 1) grid_dependency_wait();
   for (int i = threadIdx.x; i < kSortWarps * a.experts; i += kSortThreads) wcnt[i] = 0;
   if (kCopy)
     for (int i = threadIdx.x; i < a.rows; i += kSortThreads) map[i] = -1;
+  grid_begin();
   __syncthreads();
   const int64_t seg = chunk / kSortWarps;
   const int64_t begin = self * chunk + w * seg;
@@ -195,7 +196,7 @@ gather_kernel(const uint8_t* x, uint8_t* out, TokenArgs a, int64_t row_bytes, un
     for (int i = 0; i < kGatherRing; ++i) mbar_init(&loaded[w][i], 1);
   fence_proxy_async_shared();
   __syncthreads();
-  grid_dependency_wait();
+  grid_begin();
   const int64_t slots = a.tokens * a.topk;
   const int parts = (int)((row_bytes + kPiece - 1) / kPiece);
   const int64_t warp = (int64_t)blockIdx.x * kGatherWarps + w, warps = (int64_t)gridDim.x * kGatherWarps;
@@ -288,6 +289,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const uint4* rows,
   constexpr int kN = kBf16 ? 8 : 4;
   __shared__ int64_t start[64];  // of each kept row, in vectors
   __shared__ float weight[64];
+  grid_begin();
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     // the kept slots, in order
     __syncthreads();
@@ -336,6 +338,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const uint4* 
                                                                    float* dweights, TokenArgs a, int vecs) {
   constexpr int kN = kBf16 ? 8 : 4;
   __shared__ float part[kRowThreads / 32][4];
+  grid_begin();
   if (blockIdx.x >= a.tokens) {
     const int64_t r0 = (blockIdx.x - a.tokens) * 32;
     const int mine = r0 + (threadIdx.x & 31) < a.rows ? a.slot_of_row[r0 + (threadIdx.x & 31)] : 0;
@@ -428,15 +431,12 @@ cudaError_t launch_sort_tokens(const SortArgs& args, const LaunchCtx& ctx) {
   const uint8_t* x = nullptr;
   uint8_t* out = nullptr;
   int topk = 1;
-  if (n > 1) {
-    sort_count_kernel<<<n, kSortThreads, sizeof(int) * a.experts, ctx.stream>>>(a, chunk);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    void* p[] = {&a, &chunk, &x, &out, &row_bytes, &topk};
-    return launch_pdl(reinterpret_cast<const void*>(&sort_place_kernel<false>), dim3(n), dim3(kSortThreads), smem,
-                      ctx.stream, p);
-  }
-  sort_place_kernel<false><<<1, kSortThreads, smem, ctx.stream>>>(a, chunk, x, out, row_bytes, topk);
-  return cudaGetLastError();
+  void* p[] = {&a, &chunk, &x, &out, &row_bytes, &topk};
+  if (n > 1 && (e = launch_pdl(reinterpret_cast<const void*>(&sort_count_kernel), dim3(n), dim3(kSortThreads),
+                               sizeof(int) * a.experts, ctx.stream, p)) != cudaSuccess)  // (its two arguments come first)
+    return e;
+  return launch_pdl(reinterpret_cast<const void*>(&sort_place_kernel<false>), dim3(n), dim3(kSortThreads), smem,
+                    ctx.stream, p);
 }
 
 cudaError_t launch_dispatch_tokens(const SortArgs& s, const void* x, void* out, const TokenArgs& t,
@@ -446,7 +446,7 @@ cudaError_t launch_dispatch_tokens(const SortArgs& s, const void* x, void* out, 
   const int64_t row_bytes = t.width * (t.bf16 ? 2 : 4);
   if (s.slots > 1024 || s.rows > 4096 || row_bytes == 0) {
     const cudaError_t e = launch_sort_tokens(s, ctx);
-    return e != cudaSuccess ? e : launch_gather_tokens(x, out, t, true, ctx);
+    return e != cudaSuccess ? e : launch_gather_tokens(x, out, t, ctx);
   }
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e =
@@ -455,13 +455,17 @@ cudaError_t launch_dispatch_tokens(const SortArgs& s, const void* x, void* out, 
   const int64_t units = s.rows * ((row_bytes + kCopyPiece - 1) / kCopyPiece);
   const int64_t want = (units + kSortWarps - 1) / kSortWarps;
   const unsigned grid = (unsigned)(want < 1 ? 1 : want < ctx.num_sms ? want : ctx.num_sms);
-  const int64_t chunk = (s.slots + 32 * kSortWarps - 1) / (32 * kSortWarps) * (32 * kSortWarps);
-  sort_place_kernel<true><<<grid, kSortThreads, sort_smem(s.experts, s.rows), ctx.stream>>>(
-      s, chunk, static_cast<const uint8_t*>(x), static_cast<uint8_t*>(out), row_bytes, t.topk);
-  return cudaGetLastError();
+  SortArgs sort = s;
+  int64_t chunk = (s.slots + 32 * kSortWarps - 1) / (32 * kSortWarps) * (32 * kSortWarps), bytes = row_bytes;
+  const uint8_t* src = static_cast<const uint8_t*>(x);
+  uint8_t* dst = static_cast<uint8_t*>(out);
+  int topk = t.topk;
+  void* p[] = {&sort, &chunk, &src, &dst, &bytes, &topk};
+  return launch_pdl(reinterpret_cast<const void*>(&sort_place_kernel<true>), dim3(grid), dim3(kSortThreads),
+                    sort_smem(s.experts, s.rows), ctx.stream, p);
 }
 
-cudaError_t launch_gather_tokens(const void* x, void* out, const TokenArgs& args, bool pdl, const LaunchCtx& ctx) {
+cudaError_t launch_gather_tokens(const void* x, void* out, const TokenArgs& args, const LaunchCtx& ctx) {
   TokenArgs a = args;
   if (a.rows == 0 || a.width == 0) return cudaSuccess;
   int64_t row_bytes = a.width * (a.bf16 ? 2 : 4);
@@ -475,40 +479,32 @@ cudaError_t launch_gather_tokens(const void* x, void* out, const TokenArgs& args
   const int64_t items = a.tokens * ((row_bytes + kPiece - 1) / kPiece), looks = (a.rows + 31) / 32;
   const int64_t want = ((items > looks ? items : looks) + kGatherWarps - 1) / kGatherWarps;
   const unsigned grid = (unsigned)(want < ctx.num_sms ? want : ctx.num_sms);
-  if (pdl) {
-    void* p[] = {&xv, &ov, &a, &row_bytes, &status};
-    return launch_pdl(reinterpret_cast<const void*>(&gather_kernel), dim3(grid), dim3(32 * kGatherWarps), kGatherSmem,
-                      ctx.stream, p);
-  }
-  gather_kernel<<<grid, 32 * kGatherWarps, kGatherSmem, ctx.stream>>>(xv, ov, a, row_bytes, status);
-  return cudaGetLastError();
+  void* p[] = {&xv, &ov, &a, &row_bytes, &status};
+  return launch_pdl(reinterpret_cast<const void*>(&gather_kernel), dim3(grid), dim3(32 * kGatherWarps), kGatherSmem,
+                    ctx.stream, p);
 }
 
-cudaError_t launch_combine_tokens(const void* rows, void* y, const TokenArgs& a, const LaunchCtx& ctx) {
+cudaError_t launch_combine_tokens(const void* rows, void* y, const TokenArgs& args, const LaunchCtx& ctx) {
+  TokenArgs a = args;
   if (a.tokens == 0 || a.width == 0) return cudaSuccess;
-  const int vecs = (int)(a.width * (a.bf16 ? 2 : 4) / 16);
+  int vecs = (int)(a.width * (a.bf16 ? 2 : 4) / 16);
   const unsigned grid = (unsigned)(a.tokens < (1 << 30) ? a.tokens : (1 << 30));
-  if (a.bf16)
-    combine_kernel<true><<<grid, kRowThreads, 0, ctx.stream>>>(static_cast<const uint4*>(rows),
-                                                               static_cast<uint4*>(y), a, vecs);
-  else
-    combine_kernel<false><<<grid, kRowThreads, 0, ctx.stream>>>(static_cast<const uint4*>(rows),
-                                                                static_cast<uint4*>(y), a, vecs);
-  return cudaGetLastError();
+  void* p[] = {&rows, &y, &a, &vecs};
+  return launch_pdl(a.bf16 ? reinterpret_cast<const void*>(&combine_kernel<true>)
+                           : reinterpret_cast<const void*>(&combine_kernel<false>),
+                    dim3(grid), dim3(kRowThreads), 0, ctx.stream, p);
 }
 
 cudaError_t launch_combine_tokens_grad(const void* dy, const void* rows, void* drows, float* dweights,
-                                       const TokenArgs& a, const LaunchCtx& ctx) {
-  const int vecs = (int)(a.width * (a.bf16 ? 2 : 4) / 16);
+                                       const TokenArgs& args, const LaunchCtx& ctx) {
+  TokenArgs a = args;
+  int vecs = (int)(a.width * (a.bf16 ? 2 : 4) / 16);
   const int64_t grid = a.tokens + (vecs > 0 ? (a.rows + 31) / 32 : 0);
   if (grid == 0) return cudaSuccess;
-  if (a.bf16)
-    combine_grad_kernel<true><<<(unsigned)grid, kRowThreads, 0, ctx.stream>>>(
-        static_cast<const uint4*>(dy), static_cast<const uint4*>(rows), static_cast<uint4*>(drows), dweights, a, vecs);
-  else
-    combine_grad_kernel<false><<<(unsigned)grid, kRowThreads, 0, ctx.stream>>>(
-        static_cast<const uint4*>(dy), static_cast<const uint4*>(rows), static_cast<uint4*>(drows), dweights, a, vecs);
-  return cudaGetLastError();
+  void* p[] = {&dy, &rows, &drows, &dweights, &a, &vecs};
+  return launch_pdl(a.bf16 ? reinterpret_cast<const void*>(&combine_grad_kernel<true>)
+                           : reinterpret_cast<const void*>(&combine_grad_kernel<false>),
+                    dim3((unsigned)grid), dim3(kRowThreads), 0, ctx.stream, p);
 }
 
 }  // namespace nvfp4

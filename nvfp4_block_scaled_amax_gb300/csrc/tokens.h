@@ -33,9 +33,8 @@ struct TokenArgs {
   const int32_t* slot_of_row;
   const float* weights;  // [tokens, topk] or NULL (all 1)
 };
-// out[r] = x[slot_of_row[r] / topk], zero where there is no slot.  `pdl`: a
-// programmatic dependent of the sort launched just before.
-cudaError_t launch_gather_tokens(const void* x, void* out, const TokenArgs& a, bool pdl, const LaunchCtx& ctx);
+// out[r] = x[slot_of_row[r] / topk], zero where there is no slot.
+cudaError_t launch_gather_tokens(const void* x, void* out, const TokenArgs& a, const LaunchCtx& ctx);
 // The sort, then the gather; in one launch where there are few slots.
 cudaError_t launch_dispatch_tokens(const SortArgs& s, const void* x, void* out, const TokenArgs& t,
                                    const LaunchCtx& ctx);
