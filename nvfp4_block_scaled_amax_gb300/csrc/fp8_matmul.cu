@@ -423,26 +423,28 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   if (w == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-// Which of the two kernels a product runs on.  Up to 64 rows per member the
-// thin kernel's tiles fit and it is ahead everywhere (5120 x 4096 weights, 1 /
-// 16 / 64 rows: 7.9 / 8.7 / 13.0 us against 16.6 / 18.2 / 16.3).  Above, the
-// estimated times decide, in us, fitted to both kernels measured at 96 to 512
-// rows, N 1024 to 5120, K 1024 and 4096: a start, then the blocks that each
-// CTA or pair sums one after another.  For instance, thin against pair at 128
-// rows: N 1024, K 4096 10.8 / 16.7; N 5120, K 4096 19.2 / 16.9; N = K = 1024
-// 12.6 / 8.9.
+// Which of the two kernels a product runs on.  Up to 64 rows (96 per expert)
+// the thin kernel's tiles fit and it is ahead everywhere (5120 x 4096 weights,
+// 1 / 16 / 64 rows: 7.7 / 8.7 / 13.0 us against 16.6 / 18.2 / 16.3).  Above, the
+// estimated times decide, in us, fitted to both kernels at 65 to 1024 rows, N
+// 512 to 8192, K 512 to 8192: a start, then the blocks that each CTA or pair
+// sums one after another.  For instance, thin against pair at 128 rows and
+// 128 x 128 blocks: N 1024, K 4096 10.8 / 15.7; N 5120, K 4096 18.3 / 15.8; N 8192,
+// K 512 8.0 / 6.6.  Of 86 such products the rule picked the faster kernel,
+// within 10 percent, for all but two.
 bool thin_is_faster(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   const int64_t members = a.offsets ? a.experts : 1;
   const int64_t rows = a.wgrad ? a.a_rows : (a.a_rows + members - 1) / members;
-  if (rows <= 64) return true;
+  if (rows <= (members > 1 ? 96 : 64)) return true;
   const int64_t k = a.wgrad ? (a.a_cols + members - 1) / members : a.a_cols;
   const double kb = (double)((k + kBK - 1) / kBK);
   const int64_t pair_tiles = members * ((rows + 255) / 256) * ((a.b_rows + 255) / 256);
   const int64_t pair_turns = (pair_tiles + ctx.num_sms / 2 - 1) / (ctx.num_sms / 2);
   const double pair = 4.5 + pair_turns * kb * (a.b_block_rows == 1 ? 0.56 : 0.39);
   const ThinPlan t = thin_plan(a, ctx);
-  const int64_t thin_turns = (t.tiles * t.split + 2 * ctx.num_sms - 1) / (2 * ctx.num_sms);
-  const double thin = 6.0 + (t.split > 1 ? 3.5 : 0.0) + thin_turns * kb / t.split * 0.45;
+  const int64_t ctas = t.tiles * t.split, turns = (ctas + 2 * ctx.num_sms - 1) / (2 * ctx.num_sms);
+  const double block = ctas > ctx.num_sms ? 0.6 : 0.45;  // two CTAs of an SM slow each other
+  const double thin = 4.5 + (t.split > 1 ? 4.5 : 0.0) + turns * kb / t.split * block;
   return thin < pair;
 }
 
