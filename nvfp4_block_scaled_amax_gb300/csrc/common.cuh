@@ -29,13 +29,6 @@ __device__ __forceinline__ void grid_dependency_wait() {
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-// The start of a kernel that may run beside the end of the one before it:
-// whatever it does before this call touches no global memory, and the next
-// kernel may begin the same way (every thread of every CTA calls it).
-__device__ __forceinline__ void grid_begin() {
-  grid_launch_dependents();
-  grid_dependency_wait();
-}
 
 // ---------------------------------------------------------------------------
 // Scale arithmetic

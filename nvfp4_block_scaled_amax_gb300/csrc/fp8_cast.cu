@@ -15,6 +15,7 @@
 // which also cuts off what lies past the edges.  Memory-bound: 2 or 4 bytes
 // in and 1 byte per direction out for every element.
 #include "common.cuh"
+#include "dependent.h"
 #include "fp8.h"
 
 namespace nvfp4 {
@@ -326,7 +327,7 @@ cudaError_t launch(const CUtensorMap& x, const CUtensorMap& r, const CUtensorMap
   CUtensorMap maps[3] = {x, r, c};
   CastKernelArgs args = k;
   void* p[] = {&maps[0], &maps[1], &maps[2], &args};
-  return launch_pdl(reinterpret_cast<const void*>(kernel), dim3((unsigned)(k.tiles < room ? k.tiles : room)),
+  return launch_dependent(reinterpret_cast<const void*>(kernel), dim3((unsigned)(k.tiles < room ? k.tiles : room)),
                     dim3(kThreads), Smem<kBf16>::kBytes, ctx.stream, p);
 }
 

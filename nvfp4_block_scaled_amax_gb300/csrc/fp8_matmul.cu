@@ -488,7 +488,7 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   e = allow_smem(reinterpret_cast<const void*>(kernel), kSmemBytes, allowed[a.b_block_rows == 1]);
   if (e != cudaSuccess) return e;
   void* args[] = {&amap, &bmap, &omap, &p};
-  return launch_pdl(reinterpret_cast<const void*>(kernel), dim3(2 * pairs), dim3(kThreads), kSmemBytes, ctx.stream, args);
+  return launch_dependent(reinterpret_cast<const void*>(kernel), dim3(2 * pairs), dim3(kThreads), kSmemBytes, ctx.stream, args);
 }
 
 }  // namespace nvfp4

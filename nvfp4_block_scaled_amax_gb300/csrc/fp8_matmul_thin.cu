@@ -346,7 +346,7 @@ cudaError_t launch(const Fp8MatmulArgs& a, const MatmulKernelArgs& p, int64_t ti
   const int64_t room = 2 * ctx.num_sms / split;
   MatmulKernelArgs k = p;
   void* args[] = {&amap, &bmap, &k, &stages, &split};
-  return launch_pdl(reinterpret_cast<const void*>(kernel), dim3((unsigned)((tiles < room ? tiles : room) * split)),
+  return launch_dependent(reinterpret_cast<const void*>(kernel), dim3((unsigned)((tiles < room ? tiles : room) * split)),
                     dim3(kThreads), smem, ctx.stream, args, split);
 }
 

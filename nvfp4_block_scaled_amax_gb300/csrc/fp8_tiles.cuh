@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "dependent.h"
 #include "fp8.h"
 #include "tokens.h"
 

@@ -8,44 +8,24 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 namespace nvfp4 {
 
 // Launches `func` so that it may start while the preceding kernel on the
 // stream is still running (programmatic dependent launch); the kernel's
 // griddepcontrol.wait orders it after that kernel's memory operations.
-// cluster: CTAs of a cluster, along x.
 inline cudaError_t launch_pdl(const void* func, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                              void** args, int cluster = 1) {
+                              void** args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelExC(&cfg, func, args);
-}
-
-// Lets `func` use `bytes` of dynamic shared memory on the current device, once
-// per device (`allowed`: the devices where it is done, one bit each).
-inline cudaError_t allow_smem(const void* func, int bytes, std::atomic<uint64_t>& allowed) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (allowed.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_release);
-  return e;
 }
 
 struct LaunchCtx {

@@ -11,6 +11,7 @@
 // Integer counting only, and every sum in a fixed order: results do not
 // depend on timing.
 #include "common.cuh"
+#include "dependent.h"
 #include "tokens.h"
 
 namespace nvfp4 {
@@ -432,10 +433,10 @@ cudaError_t launch_sort_tokens(const SortArgs& args, const LaunchCtx& ctx) {
   uint8_t* out = nullptr;
   int topk = 1;
   void* p[] = {&a, &chunk, &x, &out, &row_bytes, &topk};
-  if (n > 1 && (e = launch_pdl(reinterpret_cast<const void*>(&sort_count_kernel), dim3(n), dim3(kSortThreads),
+  if (n > 1 && (e = launch_dependent(reinterpret_cast<const void*>(&sort_count_kernel), dim3(n), dim3(kSortThreads),
                                sizeof(int) * a.experts, ctx.stream, p)) != cudaSuccess)  // (its two arguments come first)
     return e;
-  return launch_pdl(reinterpret_cast<const void*>(&sort_place_kernel<false>), dim3(n), dim3(kSortThreads), smem,
+  return launch_dependent(reinterpret_cast<const void*>(&sort_place_kernel<false>), dim3(n), dim3(kSortThreads), smem,
                     ctx.stream, p);
 }
 
@@ -461,7 +462,7 @@ cudaError_t launch_dispatch_tokens(const SortArgs& s, const void* x, void* out, 
   uint8_t* dst = static_cast<uint8_t*>(out);
   int topk = t.topk;
   void* p[] = {&sort, &chunk, &src, &dst, &bytes, &topk};
-  return launch_pdl(reinterpret_cast<const void*>(&sort_place_kernel<true>), dim3(grid), dim3(kSortThreads),
+  return launch_dependent(reinterpret_cast<const void*>(&sort_place_kernel<true>), dim3(grid), dim3(kSortThreads),
                     sort_smem(s.experts, s.rows), ctx.stream, p);
 }
 
@@ -480,7 +481,7 @@ cudaError_t launch_gather_tokens(const void* x, void* out, const TokenArgs& args
   const int64_t want = ((items > looks ? items : looks) + kGatherWarps - 1) / kGatherWarps;
   const unsigned grid = (unsigned)(want < ctx.num_sms ? want : ctx.num_sms);
   void* p[] = {&xv, &ov, &a, &row_bytes, &status};
-  return launch_pdl(reinterpret_cast<const void*>(&gather_kernel), dim3(grid), dim3(32 * kGatherWarps), kGatherSmem,
+  return launch_dependent(reinterpret_cast<const void*>(&gather_kernel), dim3(grid), dim3(32 * kGatherWarps), kGatherSmem,
                     ctx.stream, p);
 }
 
@@ -490,7 +491,7 @@ cudaError_t launch_combine_tokens(const void* rows, void* y, const TokenArgs& ar
   int vecs = (int)(a.width * (a.bf16 ? 2 : 4) / 16);
   const unsigned grid = (unsigned)(a.tokens < (1 << 30) ? a.tokens : (1 << 30));
   void* p[] = {&rows, &y, &a, &vecs};
-  return launch_pdl(a.bf16 ? reinterpret_cast<const void*>(&combine_kernel<true>)
+  return launch_dependent(a.bf16 ? reinterpret_cast<const void*>(&combine_kernel<true>)
                            : reinterpret_cast<const void*>(&combine_kernel<false>),
                     dim3(grid), dim3(kRowThreads), 0, ctx.stream, p);
 }
@@ -502,7 +503,7 @@ cudaError_t launch_combine_tokens_grad(const void* dy, const void* rows, void* d
   const int64_t grid = a.tokens + (vecs > 0 ? (a.rows + 31) / 32 : 0);
   if (grid == 0) return cudaSuccess;
   void* p[] = {&dy, &rows, &drows, &dweights, &a, &vecs};
-  return launch_pdl(a.bf16 ? reinterpret_cast<const void*>(&combine_grad_kernel<true>)
+  return launch_dependent(a.bf16 ? reinterpret_cast<const void*>(&combine_grad_kernel<true>)
                            : reinterpret_cast<const void*>(&combine_grad_kernel<false>),
                     dim3((unsigned)grid), dim3(kRowThreads), 0, ctx.stream, p);
 }
