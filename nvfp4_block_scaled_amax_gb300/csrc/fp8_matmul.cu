@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kStages = 4;
 constexpr int kStageA = 128 * kBK, kStageBytes = 2 * kStageA;
-constexpr int kScaleStages = 2;
+constexpr int kScaleStages = 2;  // the summing warps toggle between them
 constexpr int kScaleBatch = 8;  // blocks per scale stage: one hand-over for eight blocks
 constexpr int kBufCols = 256;
 constexpr int kChunk = 64;  // columns read at a time
@@ -47,7 +47,7 @@ constexpr int kOutBoxes = 2;        // per warp: one is written while the other 
 constexpr int kThreads = 32 * (4 + kSumWarps);
 using Tiles = TileList<256, 256, 8>;
 
-struct Barriers {
+struct __align__(16) Barriers {
   uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], sfull[kScaleStages], sempty[kScaleStages];
   uint32_t tmem;
   uint32_t pad[3];
@@ -114,7 +114,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         const int32_t arow = (int32_t)tl.a_row + 128 * rank, brow = (int32_t)tl.b_row + 128 * rank;
         int32_t x = tl.kb0 * kBK;
         for (int kb = 0; kb < tl.nkb; ++kb, x += kBK) {
-          if (!mbar_wait(&bar->empty[s], phase, p.status)) {
+          if (!mbar_wait(&bar->empty[s], phase)) {
             ok = false;
             break;
           }
@@ -133,6 +133,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         }
       }
       if (!ok) {  // given up: the copies in flight land long before this ends
+        report_timeout(p.status);
         const long long c0 = clock64();
         while (clock64() - c0 < 50000000LL) {
         }
@@ -145,7 +146,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       for (int t = t0; t < tiles && ok; t += step) {
         const int nkb = Tiles::at(p, first, t).nkb;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(&bar->full[s], phase, p.status) || !mbar_wait(&bar->tempty[buf], tphase, p.status)) {
+          if (!mbar_wait(&bar->full[s], phase) || !mbar_wait(&bar->tempty[buf], tphase)) {
             ok = false;
             break;
           }
@@ -168,6 +169,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           tphase ^= buf ^ 1;
         }
       }
+      if (!ok) report_timeout(p.status);
     } else if (w == 2) {
       // the block's scales: 128 of this CTA's rows of A, 256 (or 2) of B
       const int64_t kblocks = (p.a_cols + kBK - 1) / kBK, nblocks = (p.b_rows + 127) / 128;
@@ -194,7 +196,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         }
         for (int kb = 0; kb < tl.nkb; kb += kScaleBatch, ++it) {
           const uint32_t s = it % kScaleStages;
-          if (!mbar_wait(&bar->sempty[s], ((it / kScaleStages) & 1) ^ 1, p.status)) {
+          if (!mbar_wait(&bar->sempty[s], ((it / kScaleStages) & 1) ^ 1)) {
             ok = false;
             break;
           }
@@ -216,6 +218,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           cp_async_arrive(&bar->sfull[s]);
         }
       }
+      if (!ok) report_timeout(p.status);
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncwarp();
@@ -226,95 +229,94 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     const uint32_t tempty0 = map_to_cta(smem_u32(&bar->tempty[0]), 0);
     const uint32_t box = smem_u32(out_stage + (w - 4) * kOutBoxes * kOutBox);
     uint32_t boxes = 0;
-    // Shared-memory addresses of what the loop touches.
-    const uint32_t bsfull = smem_u32(&bar->sfull[0]), bsempty = smem_u32(&bar->sempty[0]);
-    const uint32_t btfull = smem_u32(&bar->tfull[0]), btempty = tempty0;
     const uint32_t sc = smem_u32(scales);
     const uint32_t sc_row = sc + 4 * (32 * q + (kColScales ? lane >> 2 : lane));
-    const uint32_t sc_col = sc + 4 * (128 + (kColScales ? 128 * half + 2 * (lane & 3) : half));
-    uint32_t it = 0, batch = 0;
+    const uint32_t sc_col = 4 * (128 + (kColScales ? 128 * half + 2 * (lane & 3) : half)) -
+                            4 * (32 * q + (kColScales ? lane >> 2 : lane));  // from sc_row
+    // The accumulator the next block is in: its barriers and its columns, the
+    // other one 8 bytes and 256 columns further or back.
+    uint32_t tfull = smem_u32(&bar->tfull[0]), tempty = tempty0, src = lane_base, tphase = 0;
+    uint32_t stage = 0, sphase = 0;
     bool ok = true;
-    for (int t = t0; t < tiles && ok
-; t += step) {
+    for (int t = t0; t < tiles && ok; t += step) {
       const Tile tl = Tiles::at(p, first, t);
       uint64_t sum[64];  // pairs of columns
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
-      const int nkb = tl.nkb;
-      uint32_t off = 0;  // of the block's scales
+      for (int kb = 0; kb < tl.nkb; kb += kScaleBatch) {
+        ok = mbar_wait_at(smem_u32(&bar->sfull[stage]), sphase);
+        if (!ok) break;
+        uint32_t scale = sc_row + stage * (kScaleBatch * kScaleFloats * 4);
+        // This loop is kept as small as it can be: it has to fit the scheduler's
+        // own instruction store (a few instructions more cost a third of its speed).
 #pragma unroll 1
-      for (int kb = 0; kb < nkb; ++kb) {
-        if ((kb & (kScaleBatch - 1)) == 0) {
-          const uint32_t ss = batch % kScaleStages;
-          off = ss * (kScaleBatch * kScaleFloats * 4);
-          ok = mbar_wait_at(bsfull + 8 * ss, (batch / kScaleStages) & 1, p.status);
-          if (!ok) break;
-        }
-        float sa[kColScales ? 4 : 1];
-        if constexpr (kColScales) {
-          // four rows of the lane: lane / 4 + 8 i
+        for (int n = min(kScaleBatch, tl.nkb - kb); n > 0; --n, scale += 4 * kScaleFloats) {
+          float sa[kColScales ? 4 : 1];
+          if constexpr (kColScales) {
+            // four rows of the lane: lane / 4 + 8 i
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sa[i]) : "r"(sc_row + off + 32 * i));
-        } else {
-          float sb;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sa[0]) : "r"(sc_row + off));
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sb) : "r"(sc_col + off));
-          sa[0] = __fmul_rn(sa[0], sb);
+            for (int i = 0; i < 4; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sa[i]) : "r"(scale + 32 * i));
+          } else {
+            float sb;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sa[0]) : "r"(scale));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sb) : "r"(scale + sc_col));
+            sa[0] = __fmul_rn(sa[0], sb);
+          }
+          ok = mbar_wait_at(tfull, tphase);
+          if (!ok) break;
+          __syncwarp();
+          tcgen05_after_sync();
+#pragma unroll
+          for (int c = 0; c < 128; c += kChunk) {
+            // once everything is read, the accumulator may be overwritten
+            auto release = [&]() {
+              if (c != 128 - kChunk) return;
+              tcgen05_before_sync();
+              if (lane == 0) mbar_arrive_cluster(tempty);
+            };
+            if constexpr (kColScales) {
+              // A column's scale serves the lane's four rows.  Two steps an
+              // element are bound by instruction issue, which packed arithmetic
+              // halves (4096 x 4864 x 16384: 290 us against 332 with scalar).
+              uint32_t u[32], v[32];
+              float sb[8][2];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                             : "=f"(sb[j][0]), "=f"(sb[j][1])
+                             : "r"(scale + sc_col + 4 * (c + 8 * j)));
+              tmem_read_16x256(src + c, u, v);
+              release();
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint64_t s2 = pack2(sb[j][0], sb[j][1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t* x = i < 2 ? u + 4 * j + 2 * i : v + 4 * j + 2 * i - 4;
+                  uint64_t& to = sum[(c / 8 + j) * 4 + i];
+                  to = fma2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), s2), pack2(sa[i], sa[i]), to);
+                }
+              }
+            } else {
+              uint32_t v[kChunk];
+              tmem_read(src + c, v);
+              release();
+#pragma unroll
+              for (int i = 0; i < kChunk / 2; ++i)
+                sum[c / 2 + i] = fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                      pack2(sa[0], sa[0]), sum[c / 2 + i]);
+            }
+          }
+          tphase ^= (tfull >> 3) & 1;  // the second of the two is done: the next phase
+          tfull ^= 8;
+          tempty ^= 8;
+          src ^= kBufCols;
         }
-        const uint32_t src = lane_base + (it & 1) * kBufCols;
-        ok = mbar_wait_at(btfull + 8 * (it & 1), (it >> 1) & 1, p.status);
         if (!ok) break;
         __syncwarp();
-        tcgen05_after_sync();
-#pragma unroll
-        for (int c = 0; c < 128; c += kChunk) {
-          // once everything is read, the accumulator may be overwritten
-          auto release = [&]() {
-            if (c != 128 - kChunk) return;
-            tcgen05_before_sync();
-            if (lane == 0) mbar_arrive_cluster(btempty + 8 * (it & 1));
-          };
-          if constexpr (kColScales) {
-            // A column's scale serves the lane's four rows.  Two steps an
-            // element are bound by instruction issue, which packed arithmetic
-            // halves (4096 x 4864 x 16384: 290 us against 332 with scalar).
-            uint32_t u[32], v[32];
-            float sb[8][2];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                           : "=f"(sb[j][0]), "=f"(sb[j][1])
-                           : "r"(sc_col + off + 4 * (c + 8 * j)));
-            tmem_read_16x256(src + c, u, v);
-            release();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint64_t s2 = pack2(sb[j][0], sb[j][1]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t* x = i < 2 ? u + 4 * j + 2 * i : v + 4 * j + 2 * i - 4;
-                uint64_t& to = sum[(c / 8 + j) * 4 + i];
-                to = fma2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), s2), pack2(sa[i], sa[i]), to);
-              }
-            }
-          } else {
-            uint32_t v[kChunk];
-            tmem_read(src + c, v);
-            release();
-#pragma unroll
-            for (int i = 0; i < kChunk / 2; ++i)
-              sum[c / 2 + i] = fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
-                                    pack2(sa[0], sa[0]), sum[c / 2 + i]);
-          }
-        }
-        ++it;
-        off += 4 * kScaleFloats;
-        if (kb + 1 == nkb || (kb & (kScaleBatch - 1)) == kScaleBatch - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(bsempty + 8 * (batch % kScaleStages));
-          ++batch;
-        }
+        if (lane == 0) mbar_arrive(&bar->sempty[stage]);
+        stage ^= 1;
+        sphase ^= stage ^ 1;
       }
       if (!ok) break;
       float acc[128];
@@ -414,6 +416,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           });
       }
     }
+    if (!ok) report_timeout(p.status);
     if (lane == 0) bulk_wait_all();
   }
   tcgen05_before_sync();

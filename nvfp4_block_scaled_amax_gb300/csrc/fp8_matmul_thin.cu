@@ -112,7 +112,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       share(tl, kb, end);
       int32_t x = (tl.kb0 + kb) * kBK;
       for (; kb < end; ++kb, x += kBK) {
-        if (!mbar_wait(&bar->empty[s], phase, p.status)) {
+        if (!mbar_wait(&bar->empty[s], phase)) {
           ok = false;
           break;
         }
@@ -130,9 +130,10 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         }
       }
     }
-    if (!ok)  // given up: let the copies in flight land
+    if (!ok) report_timeout(p.status);
+    if (!ok)  // let the copies in flight land
       for (uint32_t i = sent < (uint32_t)stages ? 0 : sent - stages; i < sent; ++i)
-        mbar_wait(&bar->full[i % stages], (i / stages) & 1, p.status);
+        mbar_wait(&bar->full[i % stages], (i / stages) & 1);
   } else if (w == kSumWarps + 1) {
     constexpr uint32_t kIdesc = idesc_e4m3(kWeights, kBN);
     const uint64_t desc0 = operand_desc(smem_u32(smem));
@@ -143,7 +144,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       int kb, end;
       share(tl, kb, end);
       for (; kb < end; ++kb) {
-        if (!mbar_wait(&bar->full[s], phase, p.status) || !mbar_wait(&bar->tempty[buf], tphase, p.status)) {
+        if (!mbar_wait(&bar->full[s], phase) || !mbar_wait(&bar->tempty[buf], tphase)) {
           ok = false;
           break;
         }
@@ -167,6 +168,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         }
       }
     }
+    if (!ok) report_timeout(p.status);
   } else if (w == kSumWarps + 2) {
     const int64_t kblocks = (p.a_cols + kBK - 1) / kBK, nblocks = (p.b_rows + 127) / 128;
     uint32_t it = 0;
@@ -185,7 +187,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         pb = p.sb + (member * nblocks + tl.n0 / 128) * kblocks + tl.kb0 + kb;
       for (; kb < end; kb += kScaleBatch, ++it) {
         const uint32_t s = it % kScaleStages;
-        if (!mbar_wait(&bar->sempty[s], ((it / kScaleStages) & 1) ^ 1, p.status)) {
+        if (!mbar_wait(&bar->sempty[s], ((it / kScaleStages) & 1) ^ 1)) {
           ok = false;
           break;
         }
@@ -209,6 +211,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         cp_async_arrive(&bar->sfull[s]);
       }
     }
+    if (!ok) report_timeout(p.status);
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
@@ -241,12 +244,12 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         if (in_batch == 0) {
           const uint32_t ss = batch % kScaleStages;
           off = sc + ss * (kScaleBatch * L::kScaleFloats * 4);
-          ok = mbar_wait(&bar->sfull[ss], (batch / kScaleStages) & 1, p.status);
+          ok = mbar_wait(&bar->sfull[ss], (batch / kScaleStages) & 1);
           if (!ok) break;
         }
         float sw;
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sw) : "r"(off + 4 * kBN + (kRowScales ? 4 * n_in_tile : 0)));
-        ok = mbar_wait(&bar->tfull[buf], tphase, p.status);
+        ok = mbar_wait(&bar->tfull[buf], tphase);
         if (!ok) break;
         __syncwarp();
         tcgen05_after_sync();
@@ -315,6 +318,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       if (lane < split) mbar_arrive_cluster_release(map_to_cta(smem_u32(&bar->taken), lane));
       ++round;
     }
+    if (!ok) report_timeout(p.status);
   }
   __syncwarp();
   tcgen05_before_sync();

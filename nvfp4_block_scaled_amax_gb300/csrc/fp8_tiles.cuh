@@ -149,37 +149,28 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
-// The bounded wait of common.cuh without a time hint on the try: a hinted try
-// that does not succeed at once sleeps, and its sleep ends up to half a
-// microsecond late, which the hand-overs below (one every ~0.27 us) cannot
-// afford.  The limit is checked every 1024 tries.
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+// Waits for a phase of an mbarrier, with a limit: false when it has not come
+// after 2^20 tries.  A try that fails lasts up to 2600 cycles (measured), so
+// that is about 1.4 s.  Unlike the wait of common.cuh it gives no time hint (a
+// hinted try sleeps, up to half a microsecond too long for hand-overs every
+// 0.3 us) and is a few instructions, for loops that must stay small.
+__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 1048576;\n"
+      "W:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D;\n"
+      " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra W;\n"
+      "D:\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_at(uint32_t b, uint32_t parity, unsigned* status) {
-  // units of 2^20 cycles, so that a 32-bit clock serves
-  unsigned start = 0;
-#pragma unroll 1
-  for (unsigned i = 0;; ++i) {
-    if (mbar_try(b, parity)) return true;
-    if ((i & 1023) != 1023) continue;
-    const unsigned now = (unsigned)(clock64() >> 20);
-    if (i == 1023) start = now;
-    if (now - start > (unsigned)(kWaitLimitCycles >> 20)) {
-      atomicOr(status, kStatusWaitTimeout);
-      return false;
-    }
-  }
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+  return mbar_wait_at(smem_u32(bar), parity);
 }
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsigned* status) {
-  return mbar_wait_at(smem_u32(bar), parity, status);
-}
+// One warp's role gave up waiting: for nvfp4_device_status.
+__device__ __forceinline__ void report_timeout(unsigned* status) { atomicOr(status, kStatusWaitTimeout); }
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
