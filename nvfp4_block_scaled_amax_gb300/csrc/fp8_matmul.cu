@@ -99,8 +99,22 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   cluster_sync();
   tcgen05_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem, 0);
-  const int tiles = first[member_count(p)];
+  // Tiles are dealt out in turns of one per pair.  Where the last turn would
+  // leave half of the pairs idle or more, its tiles are halved (256 x 128), one
+  // half to a pair: such a turn takes about 0.6 of a whole one.
   const int t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int whole = first[member_count(p)], over = whole % step, uncut = 2 * over <= step ? whole - over : whole;
+  const int tiles = uncut + 2 * (whole - uncut);
+  auto tile_at = [&](int t) {
+    if (t < uncut) return Tiles::at(p, first, t);
+    Tile tl = Tiles::at(p, first, uncut + (t - uncut) / 2);
+    const int right = 128 * ((t - uncut) & 1);
+    tl.n0 += right;
+    tl.b_row += right;
+    tl.cols = max(0, min(128, tl.cols - right));
+    if (tl.cols == 0) tl.nkb = 0;
+    return tl;
+  };
 
   if (w < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -110,8 +124,10 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       uint32_t s = 0, phase = 1;
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += step) {
-        const Tile tl = Tiles::at(p, first, t);
-        const int32_t arow = (int32_t)tl.a_row + 128 * rank, brow = (int32_t)tl.b_row + 128 * rank;
+        const Tile tl = tile_at(t);
+        const int32_t arow = (int32_t)tl.a_row + 128 * rank;
+        // each CTA holds half of B's rows: of a halved tile, 64 (and 64 that no MMA reads)
+        const int32_t brow = (int32_t)tl.b_row + (t < uncut ? 128 : 64) * rank;
         int32_t x = tl.kb0 * kBK;
         for (int kb = 0; kb < tl.nkb; ++kb, x += kBK) {
           if (!mbar_wait(&bar->empty[s], phase)) {
@@ -139,12 +155,12 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         }
       }
     } else if (w == 1 && rank == 0) {
-      constexpr uint32_t kIdesc = idesc_e4m3(256, 256);
       const uint64_t desc0 = operand_desc(smem_u32(smem));
       uint32_t s = 0, phase = 0, buf = 0, tphase = 1;
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += step) {
-        const int nkb = Tiles::at(p, first, t).nkb;
+        const int nkb = tile_at(t).nkb;
+        const uint32_t idesc = t < uncut ? idesc_e4m3(256, 256) : idesc_e4m3(256, 128);
         for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait(&bar->full[s], phase) || !mbar_wait(&bar->tempty[buf], tphase)) {
             ok = false;
@@ -156,7 +172,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
             const uint32_t d = tmem + buf * kBufCols;
 #pragma unroll
             for (int k = 0; k < kBK / 32; ++k)  // 32 bytes further inside the 128-byte swizzled rows
-              umma_e4m3<2>(d, a + 2 * k, b + 2 * k, kIdesc, k > 0);
+              umma_e4m3<2>(d, a + 2 * k, b + 2 * k, idesc, k > 0);
             umma_commit_pair(&bar->tfull[buf]);
             umma_commit_pair(&bar->empty[s]);
           }
@@ -176,7 +192,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       uint32_t it = 0;
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += step) {
-        const Tile tl = Tiles::at(p, first, t);
+        const Tile tl = tile_at(t);
         const int64_t member = p.wgrad || tl.nkb == 0 ? 0 : tl.member;
         const float* pa = p.sa + tl.kb0 * p.a_rows + tl.a_row;
         const float* pb;
@@ -239,13 +255,24 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     uint32_t stage = 0, sphase = 0;
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
-      const Tile tl = Tiles::at(p, first, t);
+      const Tile tl = tile_at(t);
       uint64_t sum[64];  // pairs of columns
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
+      const bool idle = t >= uncut && half;  // a halved tile has the first half's columns only
       for (int kb = 0; kb < tl.nkb; kb += kScaleBatch) {
         ok = mbar_wait_at(smem_u32(&bar->sfull[stage]), sphase);
         if (!ok) break;
+        if (idle) {
+          for (int n = min(kScaleBatch, tl.nkb - kb); n > 0 && ok; --n) {
+            ok = mbar_wait_at(tfull, tphase);
+            if (ok && lane == 0) mbar_arrive_cluster(tempty);
+            tphase ^= (tfull >> 3) & 1;
+            tfull ^= 8;
+            tempty ^= 8;
+            src ^= kBufCols;
+          }
+        } else {
         uint32_t scale = sc_row + stage * (kScaleBatch * kScaleFloats * 4);
         // This loop is kept as small as it can be: it has to fit the scheduler's
         // own instruction store (a few instructions more cost a third of its speed).
@@ -312,6 +339,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           tempty ^= 8;
           src ^= kBufCols;
         }
+        }
         if (!ok) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->sempty[stage]);
@@ -327,7 +355,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       // past a member's end, and rows whose pitch TMA cannot take, are written
       // by the warp itself, a row at a time.
       const int row0 = 128 * (int)rank + 32 * q, c0 = 128 * half;
-      if (row0 >= tl.rows || c0 >= tl.cols) continue;
+      if (idle || row0 >= tl.rows || c0 >= tl.cols) continue;
       const bool by_tma = p.out_map && row0 + 32 <= tl.rows;
       auto put = [&](int c, auto&& fill) {  // 128 bytes of the rows, from column c of the tile
         if (c >= tl.cols) return;
@@ -426,24 +454,26 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   if (w == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-// Which of the two kernels a product runs on.  Up to 64 rows (96 per expert)
-// the thin kernel's tiles fit and it is ahead everywhere (5120 x 4096 weights,
-// 1 / 16 / 64 rows: 7.7 / 8.7 / 13.0 us against 16.6 / 18.2 / 16.3).  Above, the
-// estimated times decide, in us, fitted to both kernels at 65 to 1024 rows, N
-// 512 to 8192, K 512 to 8192: a start, then the blocks that each CTA or pair
-// sums one after another.  For instance, thin against pair at 128 rows and
-// 128 x 128 blocks: N 1024, K 4096 10.8 / 15.7; N 5120, K 4096 18.3 / 15.8; N 8192,
-// K 512 8.0 / 6.6.  Of 86 such products the rule picked the faster kernel,
-// within 10 percent, for all but two.
+// Which of the two kernels a product runs on.  Up to 32 rows (96 per expert)
+// the thin kernel's tiles fit and it is ahead (5120 x 4096 weights, 1 / 16 rows:
+// 8.1 / 8.6 us against 20; 1100 rows to 16 experts of 4096 x 2048: 35.5 against
+// 42.9).  Above, the estimated times decide, in us, fitted to both kernels at
+// 64 to 1024 rows, N 512 to 8192, K 512 to 8192: a start, then the blocks that
+// each CTA or pair sums one after another.  For instance, thin against pair at
+// 128 rows and 128 x 128 blocks: N 1024, K 4096 10.6 / 12.3; N 5120, K 4096 18.2 /
+// 13.7; N 8192, K 512 7.9 / 6.5.  Of 128 such products the rule picks the faster
+// kernel, or one within 10 percent of it, for all but two (14 percent).
 bool thin_is_faster(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   const int64_t members = a.offsets ? a.experts : 1;
   const int64_t rows = a.wgrad ? a.a_rows : (a.a_rows + members - 1) / members;
-  if (rows <= (members > 1 ? 96 : 64)) return true;
+  if (rows <= (members > 1 ? 96 : 32)) return true;
   const int64_t k = a.wgrad ? (a.a_cols + members - 1) / members : a.a_cols;
   const double kb = (double)((k + kBK - 1) / kBK);
   const int64_t pair_tiles = members * ((rows + 255) / 256) * ((a.b_rows + 255) / 256);
-  const int64_t pair_turns = (pair_tiles + ctx.num_sms / 2 - 1) / (ctx.num_sms / 2);
-  const double pair = 4.5 + pair_turns * kb * (a.b_block_rows == 1 ? 0.56 : 0.39);
+  const int64_t pairs = ctx.num_sms / 2, over = pair_tiles % pairs;
+  const double last = over == 0 ? 0.0 : 2 * over <= pairs ? 0.65 : 1.0;  // of a turn: halved tiles
+  const double pair = 4.5 + (pair_tiles / pairs + last) * kb * (a.b_block_rows == 1 ? 0.56 : 0.38) +
+                      (a.b_rows * (a.out_bf16 ? 2 : 4) % 16 ? 2.5 : 0.0);  // rows written by the warps
   const ThinPlan t = thin_plan(a, ctx);
   const int64_t ctas = t.tiles * t.split, turns = (ctas + 2 * ctx.num_sms - 1) / (2 * ctx.num_sms);
   const double block = ctas > ctx.num_sms ? 0.6 : 0.45;  // two CTAs of an SM slow each other
@@ -485,7 +515,7 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   // No more tiles than this, whatever the offsets.
   const int64_t tn = (a.b_rows + 255) / 256, tm = (a.a_rows + 255) / 256;
   const int64_t tiles = tn * (a.wgrad ? tm * a.experts : tm + (a.offsets ? a.experts : 0));
-  const unsigned pairs = (unsigned)(tiles < ctx.num_sms / 2 ? tiles : ctx.num_sms / 2);
+  const unsigned pairs = (unsigned)(2 * tiles < ctx.num_sms / 2 ? 2 * tiles : ctx.num_sms / 2);  // (halves)
   const auto kernel = a.b_block_rows == 1 ? matmul_pair_kernel<true> : matmul_pair_kernel<false>;
   static std::atomic<uint64_t> allowed[2];
   e = allow_smem(reinterpret_cast<const void*>(kernel), kSmemBytes, allowed[a.b_block_rows == 1]);
