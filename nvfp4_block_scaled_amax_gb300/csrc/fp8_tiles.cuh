@@ -150,14 +150,14 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 // Waits for a phase of an mbarrier, with a limit: false when it has not come
-// after 2^20 tries.  A try that fails lasts up to 2600 cycles (measured), so
-// that is about 1.4 s.  Unlike the wait of common.cuh it gives no time hint (a
+// after 2^19 tries.  A try that fails lasts up to 2600 cycles (measured), so
+// that is about 0.7 s.  Unlike the wait of common.cuh it gives no time hint (a
 // hinted try sleeps, up to half a microsecond too long for hand-overs every
 // 0.3 us) and is a few instructions, for loops that must stay small.
 __device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 1048576;\n"
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 524288;\n"
       "W:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D;\n"
       " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra W;\n"
       "D:\n selp.u32 %0, 1, 0, p;\n}"
