@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, in
   grid_begin();
   __syncthreads();
   const int64_t begin = blockIdx.x * chunk, end = min(begin + chunk, a.slots);
+#pragma unroll 4
   for (int64_t s = begin + threadIdx.x; s < end; s += kSortThreads) {
     const int e = a.ids[s];
     if ((unsigned)e < (unsigned)a.experts) atomicAdd(&cnt[e], 1);
@@ -66,14 +67,26 @@ sort_place_kernel(SortArgs a, int64_t chunk, const uint8_t* x, uint8_t* out, int
   const int64_t begin = self * chunk + w * seg;
   const int64_t end = min(begin + seg, a.slots);
   int* mine = wcnt + w * a.experts;
-  for (int64_t s0 = begin; s0 < end; s0 += 32) {
-    const int64_t s = s0 + lane;
-    int e = s < end ? a.ids[s] : -1;
-    if ((unsigned)e >= (unsigned)a.experts) e = -1;
+  // The first ids of the lane are read at once and kept for both walks.
+  constexpr int kHeld = 4;
+  int held[kHeld];
+  auto expert_at = [&](int64_t s) {
+    const int e = s < end ? a.ids[s] : -1;
+    return (unsigned)e < (unsigned)a.experts ? e : -1;
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) held[k] = expert_at(begin + 32 * k + lane);
+  auto walk = [&](auto&& visit) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (begin + 32 * k < end) visit(begin + 32 * k + lane, held[k]);
+    for (int64_t s0 = begin + 32 * kHeld; s0 < end; s0 += 32) visit(s0 + lane, expert_at(s0 + lane));
+  };
+  walk([&](int64_t, int e) {
     const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
     if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
     __syncwarp();
-  }
+  });
   if (nchunks > 1)  // a warp per expert: its rows in the earlier chunks and in all of them
     for (int e = w; e < a.experts; e += kSortWarps) {
       int before = 0, all = 0;
@@ -124,10 +137,7 @@ sort_place_kernel(SortArgs a, int64_t chunk, const uint8_t* x, uint8_t* out, int
     if (lane == 0) first[a.experts] = run;
   }
   __syncthreads();
-  for (int64_t s0 = begin; s0 < end; s0 += 32) {
-    const int64_t s = s0 + lane;
-    int e = s < end ? a.ids[s] : -1;
-    if ((unsigned)e >= (unsigned)a.experts) e = -1;
+  walk([&](int64_t s, int e) {
     const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
     const int row = e >= 0 ? mine[e] + __popc(peers & ((1u << lane) - 1u)) : -1;
     __syncwarp();
@@ -140,7 +150,7 @@ sort_place_kernel(SortArgs a, int64_t chunk, const uint8_t* x, uint8_t* out, int
       }
       if (kCopy && row >= 0) map[row] = (int)s;
     }
-  }
+  });
   if (writes) {
     // rows without a slot: the end of every member and the end of the capacity
     for (int e = self; e < a.experts; e += nchunks)
@@ -174,83 +184,53 @@ sort_place_kernel(SortArgs a, int64_t chunk, const uint8_t* x, uint8_t* out, int
 }
 
 // ---------------------------------------------------------------------------
-// Gather: one pass over the tokens by bulk copies.  Each of a CTA's warps
-// streams pieces of tokens (up to 8 KB) through its own ring in shared memory:
-// one load per piece, then a store per kept slot, no register in between, so
-// a token is read once however many rows it goes to.  Rows without a slot
-// are stored from a zeroed piece.  Memory-bound.
-constexpr int kPiece = 8192;
+// Gather: a warp takes 2 KB of a token into registers and stores them to the
+// rows of its kept slots, so a token is read once however many rows it goes
+// to; then the warps zero the rows without a slot.  Memory-bound, mostly by
+// stores, which is why they are plain ones: bulk copies out of shared memory
+// stop at 4.5 TB/s here (15 bytes a cycle and SM).  A warp per piece: 16384 x
+// 4096 BF16 to 36,800 rows in 104 us, 6.8 TB/s; the same warps in a grid that
+// stays (8 per SM) 121 us, bulk copies 134 us.
 constexpr int kGatherWarps = 4;
-constexpr int kGatherRing = 6;    // pieces per warp
-constexpr int kGatherAhead = 4;   // loads in flight
-constexpr int kGatherSmem = kPiece * (kGatherWarps * kGatherRing + 1);
+constexpr int kPiece = 2048;   // bytes of a token a warp moves at a time
+constexpr int kZeroRows = 8;   // rows a warp looks at in one go
 
-__global__ void __launch_bounds__(32 * kGatherWarps, 1)
-gather_kernel(const uint8_t* x, uint8_t* out, TokenArgs a, int64_t row_bytes, unsigned* status) {
-  extern __shared__ __align__(128) uint8_t pieces[];
-  __shared__ uint64_t loaded[kGatherWarps][kGatherRing];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* zeros = pieces + kPiece * kGatherWarps * kGatherRing;
-  for (int i = threadIdx.x; i < kPiece / 16; i += 32 * kGatherWarps)
-    reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
-  if (lane == 0)
-    for (int i = 0; i < kGatherRing; ++i) mbar_init(&loaded[w][i], 1);
-  fence_proxy_async_shared();
-  __syncthreads();
+__global__ void __launch_bounds__(32 * kGatherWarps)
+gather_kernel(const uint8_t* x, uint8_t* out, TokenArgs a, int64_t row_bytes) {
   grid_begin();
+  const int lane = threadIdx.x & 31;
   const int64_t slots = a.tokens * a.topk;
-  const int parts = (int)((row_bytes + kPiece - 1) / kPiece);
-  const int64_t warp = (int64_t)blockIdx.x * kGatherWarps + w, warps = (int64_t)gridDim.x * kGatherWarps;
-  const int64_t items = a.tokens * parts;
-  const int64_t mine = items > warp ? (items - warp + warps - 1) / warps : 0;  // items warp, warp + warps, ...
-  const uint32_t ring = smem_u32(pieces + w * kGatherRing * kPiece);
-  auto load = [&](int64_t i) {
-    const int64_t item = warp + i * warps, t = item / parts, off = (item - t * parts) * kPiece;
-    const uint32_t n = (uint32_t)min((int64_t)kPiece, row_bytes - off);
-    uint64_t* bar = &loaded[w][i % kGatherRing];
-    mbar_arrive_expect_tx(bar, n);
-    bulk_load(ring + (uint32_t)(i % kGatherRing) * kPiece, x + t * row_bytes + off, n, bar);
-  };
-  // Lane j stores slot j of the token (and j + 32); its row is looked up one
-  // piece ahead.
-  auto row_at = [&](int64_t i, int j) {
-    return i < mine && j < a.topk ? a.row_of_slot[(warp + i * warps) / parts * a.topk + j] : -1;
-  };
-  if (lane == 0)
-    for (int64_t i = 0; i < min((int64_t)kGatherAhead, mine); ++i) load(i);
-  int next = row_at(0, lane);
-  int64_t i = 0;
-  for (; i < mine; ++i) {
-    const int64_t item = warp + i * warps, off = (item % parts) * kPiece;
-    const uint32_t n = (uint32_t)min((int64_t)kPiece, row_bytes - off);
-    const uint32_t src = ring + (uint32_t)(i % kGatherRing) * kPiece;
-    const int row = next, row2 = row_at(i, lane + 32);
-    next = row_at(i + 1, lane);
-    if (!mbar_wait_bounded(&loaded[w][i % kGatherRing], (uint32_t)(i / kGatherRing) & 1, status)) break;
-    if (row >= 0 && row < a.rows) bulk_store(out + row * row_bytes + off, src, n);
-    if (row2 >= 0 && row2 < a.rows) bulk_store(out + row2 * row_bytes + off, src, n);
-    bulk_commit();
-    // The piece that the next load overwrites was stored kGatherRing -
-    // kGatherAhead items ago.
-    if (i + kGatherAhead < mine) {
-      asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kGatherRing - kGatherAhead) : "memory");
-      __syncwarp();
-      if (lane == 0) load(i + kGatherAhead);
+  const int pieces = (int)((row_bytes + kPiece - 1) / kPiece);
+  const int64_t warp = (int64_t)blockIdx.x * kGatherWarps + (threadIdx.x >> 5);
+  const int64_t warps = (int64_t)gridDim.x * kGatherWarps;
+  for (int64_t u = warp; u < a.tokens * pieces; u += warps) {
+    const int64_t t = u / pieces, off = (u - t * pieces) * kPiece;
+    const int n = (int)min((int64_t)kPiece, row_bytes - off);
+    const uint4* src = reinterpret_cast<const uint4*>(x + t * row_bytes + off) + lane;
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if ((lane + 32 * i) * 16 < n) v[i] = __ldcs(src + 32 * i);
+    for (int j0 = 0; j0 < a.topk; j0 += 32) {
+      const int mine = j0 + lane < a.topk ? a.row_of_slot[t * a.topk + j0 + lane] : -1;
+      for (int j = 0; j < min(32, a.topk - j0); ++j) {
+        const int row = __shfl_sync(0xFFFFFFFFu, mine, j);
+        if (row < 0 || row >= a.rows) continue;
+        uint4* dst = reinterpret_cast<uint4*>(out + row * row_bytes + off) + lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((lane + 32 * i) * 16 < n) __stcs(dst + 32 * i, v[i]);
+      }
     }
   }
-  if (i < mine)  // given up: let the copies in flight land
-    for (int64_t k = i + 1; k < min(i + kGatherAhead, mine); ++k)
-      mbar_wait_bounded(&loaded[w][k % kGatherRing], (uint32_t)(k / kGatherRing) & 1, status);
-  __syncwarp();
-  for (int64_t r0 = warp * 32; r0 < a.rows; r0 += warps * 32) {
-    const int64_t r = r0 + lane;
-    const int slot = r < a.rows ? a.slot_of_row[r] : 0;
-    if (r < a.rows && (slot < 0 || slot >= slots))
-      for (int64_t off = 0; off < row_bytes; off += kPiece)
-        bulk_store(out + r * row_bytes + off, smem_u32(zeros), (uint32_t)min((int64_t)kPiece, row_bytes - off));
+  for (int64_t r0 = warp * kZeroRows; r0 < a.rows; r0 += warps * kZeroRows) {
+    const int slot = lane < kZeroRows && r0 + lane < a.rows ? a.slot_of_row[r0 + lane] : 0;
+    unsigned empty = __ballot_sync(0xFFFFFFFFu, slot < 0 || slot >= slots);
+    for (; empty; empty &= empty - 1) {
+      uint4* dst = reinterpret_cast<uint4*>(out + (r0 + __ffs(empty) - 1) * row_bytes);
+      for (int64_t i = lane; i < row_bytes / 16; i += 32) __stcs(dst + i, make_uint4(0, 0, 0, 0));
+    }
   }
-  bulk_commit();
-  bulk_wait_all();
 }
 
 constexpr int kRowThreads = 128;
@@ -472,17 +452,12 @@ cudaError_t launch_gather_tokens(const void* x, void* out, const TokenArgs& args
   int64_t row_bytes = a.width * (a.bf16 ? 2 : 4);
   const uint8_t* xv = static_cast<const uint8_t*>(x);
   uint8_t* ov = static_cast<uint8_t*>(out);
-  unsigned* status = ctx.status;
-  static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&gather_kernel), kGatherSmem, allowed);
-  if (e != cudaSuccess) return e;
   // every warp has a piece to copy, or rows to look at
-  const int64_t items = a.tokens * ((row_bytes + kPiece - 1) / kPiece), looks = (a.rows + 31) / 32;
+  const int64_t items = a.tokens * ((row_bytes + kPiece - 1) / kPiece), looks = (a.rows + kZeroRows - 1) / kZeroRows;
   const int64_t want = ((items > looks ? items : looks) + kGatherWarps - 1) / kGatherWarps;
-  const unsigned grid = (unsigned)(want < ctx.num_sms ? want : ctx.num_sms);
-  void* p[] = {&xv, &ov, &a, &row_bytes, &status};
-  return launch_dependent(reinterpret_cast<const void*>(&gather_kernel), dim3(grid), dim3(32 * kGatherWarps), kGatherSmem,
-                    ctx.stream, p);
+  void* p[] = {&xv, &ov, &a, &row_bytes};
+  return launch_dependent(reinterpret_cast<const void*>(&gather_kernel),
+                          dim3((unsigned)(want < (1 << 30) ? want : (1 << 30))), dim3(32 * kGatherWarps), 0, ctx.stream, p);
 }
 
 cudaError_t launch_combine_tokens(const void* rows, void* y, const TokenArgs& args, const LaunchCtx& ctx) {
