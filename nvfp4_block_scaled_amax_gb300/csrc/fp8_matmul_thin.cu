@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                    const __grid_constant__ MatmulKernelArgs p, int stages, int split) {
   using L = Layout<kBN>;
-  using Tiles = TileList<kBN, kWeights, 1 << 20>;
+  using Tiles = TileList<kBN, kWeights, 0>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* scales = reinterpret_cast<float*>(smem + stages * L::kStageBytes);

@@ -66,7 +66,7 @@ struct Tile {
 // Tiles of kTM rows of A by kTN rows of B, all members in one list: first[i]
 // is the first tile of member i.  Inside a member, bands of kBand row tiles,
 // and in a band all row tiles of a column before the next column, so that the
-// tiles in flight share both operands' rows in L2.
+// tiles in flight share both operands' rows in L2.  kBand 0: one band.
 template <int kTM, int kTN, int kBand>
 struct TileList {
   static __device__ __forceinline__ int64_t rows_of(const MatmulKernelArgs& p, int e) {
@@ -107,8 +107,8 @@ struct TileList {
     member_range(p, lo, begin, end);
     const int64_t M = p.wgrad ? p.a_rows : end - begin;
     const int mt = (int)((M + kTM - 1) / kTM), nt = (int)((p.b_rows + kTN - 1) / kTN);
-    const int band = i / (kBand * nt), in_band = i - band * kBand * nt;
-    const int height = min(kBand, mt - band * kBand);
+    const int band = kBand ? i / (kBand * nt) : 0, in_band = i - band * kBand * nt;
+    const int height = kBand ? min(kBand, mt - band * kBand) : mt;
     const int64_t m0 = (int64_t)(band * kBand + in_band % height) * kTM;
     r.n0 = (int64_t)(in_band / height) * kTN;
     r.rows = (int)min((int64_t)kTM, M - m0);

@@ -76,3 +76,14 @@ def test_rows_of_more_than_two_to_the_31_elements():
     drows, dw = nv.combine_tokens_grad(y, rows, plan)
     assert torch.equal(drows[-64:], y[slot[-64:] // topk])
     assert dw.shape == (T, topk)
+
+
+@pytest.mark.parametrize("M,N", [(1, 524288), (20, 524160)])
+def test_few_rows_through_a_very_wide_matrix(M, N):
+    """4096 (and 4095) tiles of weights: tile indexes times 2^20 would pass 32 bits."""
+    K = 144
+    a, b = nv.FP8Operand(codes(M, K, 1), scales((2, M), 2)), nv.FP8Operand(codes(N, K, 3), scales((2, N), 4))
+    y = nv.matmul_fp8(a, b, out_dtype=torch.float32)
+    av = a.data.double() * a.scale.t().double().repeat_interleave(128, 1)[:, :K]
+    bv = b.data.double() * b.scale.t().double().repeat_interleave(128, 1)[:, :K]
+    check(y, av, bv)
