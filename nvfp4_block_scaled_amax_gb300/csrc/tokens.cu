@@ -120,7 +120,8 @@ sort_place_kernel(SortArgs a, int64_t chunk, const uint8_t* x, uint8_t* out, int
     int run = 0;
     for (int e0 = 0; e0 < a.experts; e0 += 32) {
       const int e = e0 + lane;
-      const int padded = e < a.experts ? (total[e] + a.align - 1) / a.align * a.align : 0;
+      // (unsigned: the sum before the division may pass 2^31, the member's rows do not)
+      const int padded = e < a.experts ? (int)(((unsigned)total[e] + a.align - 1) / a.align * a.align) : 0;
       int incl = padded;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {

@@ -87,3 +87,15 @@ def test_few_rows_through_a_very_wide_matrix(M, N):
     av = a.data.double() * a.scale.t().double().repeat_interleave(128, 1)[:, :K]
     bv = b.data.double() * b.scale.t().double().repeat_interleave(128, 1)[:, :K]
     check(y, av, bv)
+
+
+def test_sort_whose_member_and_alignment_pass_two_to_the_31_together():
+    align = 1000003
+    T = 2147 * align  # already a multiple: a member of T rows, although T + align - 1 > 2^31
+    ids = torch.zeros(T, 1, device="cuda", dtype=torch.int32)
+    plan = nv.sort_tokens(ids, 1, align=align)
+    assert plan.offsets.tolist() == [0, T] and plan.rows == T
+    for s in range(0, T, 1 << 28):
+        e = min(s + (1 << 28), T)
+        want = torch.arange(s, e, device="cuda", dtype=torch.int32)
+        assert torch.equal(plan.row_of_slot[s:e, 0], want) and torch.equal(plan.slot_of_row[s:e], want)
