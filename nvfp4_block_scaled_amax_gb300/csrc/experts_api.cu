@@ -194,6 +194,7 @@ nvfp4_status nvfp4_combine_tokens_grad(const void* dy, const void* rows_in, int 
   nvfp4_status st = check_rows(dtype, tokens, width, topk, rows);
   if (st != NVFP4_OK) return st;
   if ((tokens > 0 && row_of_slot == nullptr) || (rows > 0 && slot_of_row == nullptr)) return NVFP4_ERR_NULL;
+  if (!size_ok(tokens + (rows + 31) / 32)) return NVFP4_ERR_SHAPE;  // one CTA each
   if (width > 0 && ((tokens > 0 && dy == nullptr) || (rows > 0 && (rows_in == nullptr || drows == nullptr))))
     return NVFP4_ERR_NULL;
   if (!aligned(dy, 16) || !aligned(rows_in, 16) || !aligned(drows, 16) || !aligned(row_of_slot, 4) ||

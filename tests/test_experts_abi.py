@@ -96,6 +96,8 @@ def test_combine(lib):
     assert grad(sor=None) == ERR_NULL
     assert grad(drows=D + 8) == ERR_ALIGN
     assert grad(width=68) == ERR_SHAPE
+    most = (1 << 31) - 1
+    assert lib.nvfp4_combine_tokens_grad(X, A, 0, most, 8, 1, B, C, most, None, D, E, None) == ERR_SHAPE  # CTAs of a launch
 
 
 def test_fp8(lib):
