@@ -36,6 +36,8 @@ def expert_layer(x: torch.Tensor, weights: torch.Tensor | FP8Tensor, expert_ids:
     (K, N multiples of 16); otherwise the members are not padded and nothing is saved."""
     if isinstance(weights, torch.Tensor):
         weights = quantize_fp8(weights, block_rows=BLOCK, colwise=training)
+    elif training and weights.col is None:
+        raise ValueError("the gradients need the column-wise cast of the weights: quantize_fp8(..., colwise=True)")
     E = weights.row.data.shape[0]
     rows, plan = dispatch_tokens(x, expert_ids, E, align=BLOCK if training else 1)
     q = quantize_fp8(rows, colwise=training)

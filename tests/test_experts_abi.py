@@ -137,3 +137,13 @@ def test_fp8(lib):
     wg = lib.nvfp4_fp8_matmul_grouped_wgrad
     assert wg(X, A, B, C, 64, 64, 72, 4, E, D, 1, None) == ERR_SHAPE      # rows % 16
     assert wg(X, A, B, C, 64, 64, 64, 4, None, D, 1, None) == ERR_NULL
+
+
+def test_layer_for_training_needs_the_column_wise_weights():
+    import torch
+
+    from nvfp4_block_scaled_amax_gb300.experts import expert_layer
+    from nvfp4_block_scaled_amax_gb300.fp8 import FP8Operand, FP8Tensor
+    w = FP8Tensor(FP8Operand(torch.zeros(2, 128, 128, dtype=torch.float8_e4m3fn), torch.ones(2, 1, 1), 128), None)
+    with pytest.raises(ValueError, match="column-wise"):
+        expert_layer(torch.zeros(4, 128, dtype=torch.bfloat16), w, torch.zeros(4, 1, dtype=torch.int32), torch.ones(4, 1))
