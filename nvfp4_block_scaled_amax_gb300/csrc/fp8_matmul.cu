@@ -47,8 +47,19 @@ constexpr int kOutBoxes = 2;        // per warp: one is written while the other 
 constexpr int kThreads = 32 * (4 + kSumWarps);
 using Tiles = TileList<256, 256, 8>;
 
+constexpr int kTileSlots = 4;       // tiles worked out ahead
+
+// A tile as one warp hands it to the others (see Tile).
+struct __align__(16) TileSlot {
+  int nkb, kb0, half, member;  // half: of a halved tile
+  int a_row, b_row, n0, out_row;
+  int rows, cols, pad[2];
+};
+
 struct __align__(16) Barriers {
   uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], sfull[kScaleStages], sempty[kScaleStages];
+  uint64_t listed[kTileSlots], done[kTileSlots];
+  TileSlot tiles[kTileSlots];
   uint32_t tmem;
   uint32_t pad[3];
 };
@@ -86,6 +97,10 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         mbar_init(&bar->sfull[i], 32);
         mbar_init(&bar->sempty[i], kSumWarps);
       }
+      for (int i = 0; i < kTileSlots; ++i) {
+        mbar_init(&bar->listed[i], 1);
+        mbar_init(&bar->done[i], kSumWarps + (rank == 0 ? 3 : 2));
+      }
       fence_mbar_init();
       tma_prefetch_desc(&amap);
       tma_prefetch_desc(&bmap);
@@ -107,15 +122,13 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   const int t0 = blockIdx.x >> 1, step = gridDim.x >> 1;
   const int whole = first[member_count(p)], over = whole % step, uncut = 2 * over <= step ? whole - over : whole;
   const int tiles = uncut + 2 * (whole - uncut);
-  auto tile_at = [&](int t) {
-    if (t < uncut) return Tiles::at(p, first, t);
-    Tile tl = Tiles::at(p, first, uncut + (t - uncut) / 2);
-    const int right = 128 * ((t - uncut) & 1);
-    tl.n0 += right;
-    tl.b_row += right;
-    tl.cols = max(0, min(128, tl.cols - right));
-    if (tl.cols == 0) tl.nkb = 0;
-    return tl;
+  const int items = t0 < tiles ? (tiles - 1 - t0) / step + 1 : 0;
+  auto slot_of = [&](int i) { return bar->tiles + i % kTileSlots; };
+  // Waits for tile i of this CTA; a warp that is through with it calls leave.
+  auto listed = [&](int i) { return mbar_wait(&bar->listed[i % kTileSlots], (i / kTileSlots) & 1); };
+  auto leave = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar->done[i % kTileSlots]);
   };
 
   if (w < 4) {
@@ -125,13 +138,16 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       // both operands' slices, counted on the first CTA's barrier
       uint32_t s = 0, phase = 1;
       bool ok = true;
-      for (int t = t0; t < tiles && ok; t += step) {
-        const Tile tl = tile_at(t);
-        const int32_t arow = (int32_t)tl.a_row + 128 * rank;
+      for (int i = 0; i < items && ok; ++i) {
+        if (!(ok = listed(i))) break;
+        const TileSlot* tl = slot_of(i);
+        const int32_t arow = tl->a_row + 128 * rank;
         // each CTA holds half of B's rows: of a halved tile, 64 (and 64 that no MMA reads)
-        const int32_t brow = (int32_t)tl.b_row + (t < uncut ? 128 : 64) * rank;
-        int32_t x = tl.kb0 * kBK;
-        for (int kb = 0; kb < tl.nkb; ++kb, x += kBK) {
+        const int32_t brow = tl->b_row + (tl->half ? 64 : 128) * rank;
+        int32_t x = tl->kb0 * kBK;
+        const int nkb = __shfl_sync(0xFFFFFFFFu, tl->nkb, 0);
+        leave(i);
+        for (int kb = 0; kb < nkb; ++kb, x += kBK) {
           if (!mbar_wait(&bar->empty[s], phase)) {
             ok = false;
             break;
@@ -160,9 +176,11 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       const uint64_t desc0 = operand_desc(smem_u32(smem));
       uint32_t s = 0, phase = 0, buf = 0, tphase = 1;
       bool ok = true;
-      for (int t = t0; t < tiles && ok; t += step) {
-        const int nkb = tile_at(t).nkb;
-        const uint32_t idesc = t < uncut ? idesc_e4m3(256, 256) : idesc_e4m3(256, 128);
+      for (int i = 0; i < items && ok; ++i) {
+        if (!(ok = listed(i))) break;
+        const int nkb = __shfl_sync(0xFFFFFFFFu, slot_of(i)->nkb, 0);
+        const uint32_t idesc = __shfl_sync(0xFFFFFFFFu, slot_of(i)->half ? idesc_e4m3(256, 128) : idesc_e4m3(256, 256), 0);
+        leave(i);
         for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait(&bar->full[s], phase) || !mbar_wait(&bar->tempty[buf], tphase)) {
             ok = false;
@@ -193,10 +211,12 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       const int64_t kblocks = (p.a_cols + kBK - 1) / kBK, nblocks = (p.b_rows + 127) / 128;
       uint32_t it = 0;
       bool ok = true;
-      for (int t = t0; t < tiles && ok; t += step) {
-        const Tile tl = tile_at(t);
+      for (int i = 0; i < items && ok; ++i) {
+        if (!(ok = listed(i))) break;
+        const TileSlot tl = *slot_of(i);
+        leave(i);
         const int64_t member = p.wgrad || tl.nkb == 0 ? 0 : tl.member;
-        const float* pa = p.sa + tl.kb0 * p.a_rows + tl.a_row;
+        const float* pa = p.sa + (int64_t)tl.kb0 * p.a_rows + tl.a_row;
         const float* pb;
         int oa[4], ob[8], nb;  // offsets of this lane's scales; how many of B's exist
 #pragma unroll
@@ -238,6 +258,34 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       }
       if (!ok) report_timeout(p.status);
       asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (w == 3) {
+      // The tiles, ahead of the other warps: working one out takes about 1000
+      // cycles, which in every warp's own loop cost 16384 x 4096 x 2048 in eight
+      // members, FP32 out, 165 us against 153.
+      for (int i = 0; i < items; ++i) {
+        const int t = t0 + i * step;
+        Tile tl = Tiles::at(p, first, t < uncut ? t : uncut + (t - uncut) / 2);
+        if (t >= uncut) {
+          const int right = 128 * ((t - uncut) & 1);
+          tl.n0 += right;
+          tl.b_row += right;
+          tl.cols = max(0, min(128, tl.cols - right));
+          if (tl.cols == 0) tl.nkb = 0;
+        }
+        bool free = false;  // within the time of a tile, which may pass the limit of one wait
+        for (int64_t n = 0; n <= p.a_cols >> 26 && !free; ++n)
+          free = mbar_wait(&bar->done[i % kTileSlots], ((i / kTileSlots) & 1) ^ 1);
+        if (!free) {
+          report_timeout(p.status);
+          break;
+        }
+        if (lane == 0) {
+          *slot_of(i) = {tl.nkb, tl.kb0, t >= uncut, tl.member, (int)tl.a_row, (int)tl.b_row, (int)tl.n0,
+                         (int)tl.out_row, tl.rows, tl.cols, {0, 0}};
+          mbar_arrive(&bar->listed[i % kTileSlots]);
+        }
+        __syncwarp();
+      }
     }
     __syncwarp();
   } else {
@@ -256,17 +304,18 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     uint32_t tfull = smem_u32(&bar->tfull[0]), tempty = tempty0, src = lane_base, tphase = 0;
     uint32_t stage = 0, sphase = 0;
     bool ok = true;
-    for (int t = t0; t < tiles && ok; t += step) {
-      const Tile tl = tile_at(t);
+    for (int item = 0; item < items && ok; ++item) {
+      if (!(ok = listed(item))) break;
+      const int nkb = slot_of(item)->nkb;
       uint64_t sum[64];  // pairs of columns
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
-      const bool idle = t >= uncut && half;  // a halved tile has the first half's columns only
-      for (int kb = 0; kb < tl.nkb; kb += kScaleBatch) {
+      const bool idle = slot_of(item)->half && half;  // a halved tile has the first half's columns only
+      for (int kb = 0; kb < nkb; kb += kScaleBatch) {
         ok = mbar_wait_at(smem_u32(&bar->sfull[stage]), sphase);
         if (!ok) break;
         if (idle) {
-          for (int n = min(kScaleBatch, tl.nkb - kb); n > 0 && ok; --n) {
+          for (int n = min(kScaleBatch, nkb - kb); n > 0 && ok; --n) {
             ok = mbar_wait_at(tfull, tphase);
             if (ok && lane == 0) mbar_arrive_cluster(tempty);
             tphase ^= (tfull >> 3) & 1;
@@ -281,7 +330,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           // again, the hand-over of the scales outside and shorter waits 3 to 8
           // percent faster), as if the loop just fitted an instruction store.
 #pragma unroll 1
-          for (int n = min(kScaleBatch, tl.nkb - kb); n > 0; --n, scale += 4 * kScaleFloats) {
+          for (int n = min(kScaleBatch, nkb - kb); n > 0; --n, scale += 4 * kScaleFloats) {
             float sa[kColScales ? 4 : 1];
             if constexpr (kColScales) {
               // four rows of the lane: lane / 4 + 8 i
@@ -351,6 +400,8 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         sphase ^= stage ^ 1;
       }
       if (!ok) break;
+      const TileSlot tl = *slot_of(item);
+      leave(item);
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 64; ++i) unpack2(sum[i], acc[2 * i], acc[2 * i + 1]);
@@ -371,7 +422,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         if (by_tma) {
           fence_proxy_async_shared();
           __syncwarp();
-          if (lane == 0) tma_store(&omap, src, (int32_t)(tl.n0 + c), (int32_t)(tl.out_row + row0));
+          if (lane == 0) tma_store(&omap, src, tl.n0 + c, tl.out_row + row0);
         } else {
           __syncwarp();
           const int rows = min(32, tl.rows - row0);
@@ -381,7 +432,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
                          : "=r"(x)
                          : "r"(src + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4)
                          : "memory");
-            const int64_t at = (tl.out_row + row0 + r) * p.b_rows + tl.n0 + c;
+            const int64_t at = (int64_t)(tl.out_row + row0 + r) * p.b_rows + tl.n0 + c;
             if (p.out_bf16) {
               uint16_t* dst = static_cast<uint16_t*>(p.out) + at + 2 * lane;
               if (c + 2 * lane < tl.cols) dst[0] = (uint16_t)x;
