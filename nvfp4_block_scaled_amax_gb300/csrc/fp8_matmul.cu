@@ -65,7 +65,7 @@ struct __align__(16) Barriers {
 };
 
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kSumWarps * kOutBoxes * kOutBox +
-                           kScaleStages * kScaleBatch * kScaleFloats * 4 + (int)sizeof(Barriers) + 4 * (kMaxExperts + 2);
+                           kScaleStages * kScaleBatch * kScaleFloats * 4 + (int)sizeof(Barriers) + 4 * Tiles::ints(kMaxExperts);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 static_assert(kScaleStages == 2, "the summing warps toggle between two scale stages");
 
@@ -109,11 +109,13 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   } else if (w == 1) {
     tmem_alloc_pair(&bar->tmem, 512);
   }
+  __syncwarp();
+  cluster_arrive();  // (barriers and tensor memory are set up)
   grid_begin();
   if (w == 2) Tiles::fill(p, first);
   tcgen05_before_sync();
   __syncthreads();
-  cluster_sync();
+  cluster_wait();
   tcgen05_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem, 0);
   // Tiles are dealt out in turns of one per pair.  Where the last turn would

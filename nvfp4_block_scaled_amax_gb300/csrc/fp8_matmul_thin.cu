@@ -46,8 +46,9 @@ struct Layout {
   static constexpr int kScaleFloats = kWeights + kBN;
   static constexpr int kScaleBytes = kScaleStages * kScaleBatch * kScaleFloats * 4;
   static constexpr int kShareBytes = kBN * kWeights * 4;
-  static int rest(int members, int split) {
-    return kScaleBytes + (split > 1 ? kShareBytes : 0) + (int)sizeof(Barriers) + 4 * (members + 1);
+  static int rest(int experts, int split) {
+    return kScaleBytes + (split > 1 ? kShareBytes : 0) + (int)sizeof(Barriers) +
+           4 * TileList<kBN, kWeights, 0>::ints(experts);
   }
 };
 
@@ -89,19 +90,22 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   } else if (w == kSumWarps + 1) {
     tmem_alloc(&bar->tmem, L::kTmemCols);
   }
+  __syncwarp();
+  if (split > 1) cluster_arrive();  // (the barriers are set up)
   grid_begin();
   if (w == kSumWarps + 2) Tiles::fill(p, first);
   tcgen05_before_sync();
   __syncthreads();
-  if (split > 1) cluster_sync();
+  if (split > 1) cluster_wait();
   tcgen05_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem, 0);
   const int tiles = first[member_count(p)];
-  const int t0 = blockIdx.x / split, step = gridDim.x / split;
+  const int lg_split = __ffs(split) - 1;  // 1, 4 or 8: shifts, for a division takes as long as the copy of a block
+  const int t0 = blockIdx.x >> lg_split, step = gridDim.x >> lg_split;
   // This CTA's share of a tile's blocks.
   auto share = [&](const Tile& tl, int& begin, int& end) {
-    begin = (int)((int64_t)tl.nkb * rank / split);
-    end = (int)((int64_t)tl.nkb * (rank + 1) / split);
+    begin = (tl.nkb * rank) >> lg_split;
+    end = (tl.nkb * (rank + 1)) >> lg_split;
   };
 
   if (w == kSumWarps) {
@@ -294,7 +298,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       }
       // Column c belongs to rank c / (kBN / split); its partial sums lie in
       // shares[rank of the sender][c % (kBN / split)][lane of the tile].
-      const int own = kBN / split, lg = __ffs(own) - 1;
+      const int own = kBN >> lg_split, lg = __ffs(own) - 1;
       ok = mbar_wait_cluster(&bar->taken, (round & 1) ^ 1, p.status);
       if (!ok) break;
       const uint32_t mine = smem_u32(shares) + 4 * (rank * own * kWeights + n_in_tile);
@@ -309,10 +313,16 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       ok = mbar_wait_cluster(&bar->got, round & 1, p.status);
       if (!ok) break;
       const int held = min(own, tl.rows - rank * own);  // columns of this CTA that exist
-#pragma unroll 4
+#pragma unroll 2
       for (int c = 0; c < held; ++c) {
+        float part[8];  // all read before the first is added
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < split) part[r] = shares[(r * own + c) * kWeights + n_in_tile];
         float sum = 0.0f;
-        for (int r = 0; r < split; ++r) sum = __fadd_rn(sum, shares[(r * own + c) * kWeights + n_in_tile]);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < split) sum = __fadd_rn(sum, part[r]);
         store(tl, rank * own + c, sum);
       }
       __syncwarp();
@@ -338,9 +348,8 @@ cudaError_t launch(const Fp8MatmulArgs& a, const MatmulKernelArgs& p, int64_t ti
   if (e != cudaSuccess) return e;
   e = make_fp8_tensor_map(&bmap, a.b, a.wgrad ? a.b_rows : a.b_rows * a.experts, a.a_cols, kWeights);
   if (e != cudaSuccess) return e;
-  const int members = a.offsets == nullptr ? 1 : a.experts + 1;
   constexpr int kPerCta = 113 * 1024;  // two CTAs share an SM's 228 KB, 1 KB of it reserved for each
-  const int rest = 1024 + L::rest(members, split);
+  const int rest = 1024 + L::rest(a.experts, split);
   int stages = (kPerCta - rest) / L::kStageBytes;
   if (stages > kMaxStages) stages = kMaxStages;
   const int smem = rest + stages * L::kStageBytes;

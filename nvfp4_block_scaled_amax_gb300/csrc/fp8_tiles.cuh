@@ -63,8 +63,9 @@ struct Tile {
   int member;
 };
 
-// Tiles of kTM rows of A by kTN rows of B, all members in one list: first[i]
-// is the first tile of member i.  Inside a member, bands of kBand row tiles,
+// Tiles of kTM rows of A by kTN rows of B, all members in one list, in shared
+// memory: first[i] is the first tile of member i (first[members]: the number of
+// tiles), and kept behind them where each member begins.  Inside a member, bands of kBand row tiles,
 // and in a band all row tiles of a column before the next column, so that the
 // tiles in flight share both operands' rows in L2.  kBand 0: one band.
 template <int kTM, int kTN, int kBand>
@@ -75,9 +76,14 @@ struct TileList {
     member_range(p, e, begin, end);
     return end - begin;
   }
-  // One warp fills first[0 .. members].
+  // Integers for `experts` members.
+  static constexpr __host__ __device__ int ints(int experts) { return 2 * experts + 3; }
+  // One warp fills the list.
   static __device__ __forceinline__ void fill(const MatmulKernelArgs& p, int* first) {
     const int lane = threadIdx.x & 31, members = member_count(p);
+    int* start = first + members + 1;
+    if (p.offsets != nullptr)
+      for (int e = lane; e <= p.experts; e += 32) start[e] = (int)clamp_offset(p, e);
     const int64_t tn = (p.b_rows + kTN - 1) / kTN;
     int run = 0;
     for (int e0 = 0; e0 < members; e0 += 32) {
@@ -103,14 +109,19 @@ struct TileList {
     Tile r;
     r.member = lo;
     const int i = t - first[lo];
-    int64_t begin, end;
-    member_range(p, lo, begin, end);
+    int64_t begin = 0, end = p.wgrad ? p.a_cols : p.a_rows;
+    if (p.offsets != nullptr) {
+      const int* start = first + member_count(p) + 1;
+      begin = start[lo];
+      if (lo < p.experts) end = max((int)begin, start[lo + 1]);
+    }
     const int64_t M = p.wgrad ? p.a_rows : end - begin;
     const int mt = (int)((M + kTM - 1) / kTM), nt = (int)((p.b_rows + kTN - 1) / kTN);
     const int band = kBand ? i / (kBand * nt) : 0, in_band = i - band * kBand * nt;
     const int height = kBand ? min(kBand, mt - band * kBand) : mt;
-    const int64_t m0 = (int64_t)(band * kBand + in_band % height) * kTM;
-    r.n0 = (int64_t)(in_band / height) * kTN;
+    const int column = height == 1 ? in_band : (int)((unsigned)in_band / (unsigned)height);
+    const int64_t m0 = (int64_t)(band * kBand + in_band - column * height) * kTM;
+    r.n0 = (int64_t)column * kTN;
     r.rows = (int)min((int64_t)kTM, M - m0);
     r.cols = (int)min((int64_t)kTN, p.b_rows - r.n0);
     if (p.wgrad) {
@@ -221,8 +232,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 // Four bytes to shared memory, asynchronously; zeros when `there` is false.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool there) {
