@@ -8,8 +8,8 @@
 // 4 or 8 CTAs where there are too few tiles to fill the machine: each CTA
 // sums its share of the blocks, sends every column of its partial sums to
 // the CTA of the cluster that owns the column (through distributed shared
-// memory), and the owner adds the shares in the order of their rank, so the
-// result does not depend on timing.
+// memory, counted on the owner's barrier), and the owner adds the shares in
+// the order of their rank, so the result does not depend on timing.
 //
 // Bound by reading the weights: two CTAs per SM keep up to 200 KB of operand
 // slices per SM in flight.  Warps 0-3 sum, warp 4 issues the copies, warp 5
@@ -32,7 +32,7 @@ constexpr int kMaxStages = 8, kMaxBuffers = 8;
 struct Barriers {
   uint64_t full[kMaxStages], empty[kMaxStages], tfull[kMaxBuffers], tempty[kMaxBuffers];
   uint64_t sfull[kScaleStages], sempty[kScaleStages];
-  uint64_t got, taken;  // the cluster's partial sums: all have arrived / all have been added
+  uint64_t got, taken;  // the cluster's partial sums: all are here / all have been added
   uint32_t tmem;
   uint32_t pad;
 };
@@ -45,9 +45,11 @@ struct Layout {
   static constexpr int kTmemCols = kBN * kBuffers;
   static constexpr int kScaleFloats = kWeights + kBN;
   static constexpr int kScaleBytes = kScaleStages * kScaleBatch * kScaleFloats * 4;
-  static constexpr int kShareBytes = kBN * kWeights * 4;
+  // Columns a CTA of a cluster owns (of few columns and many CTAs, the last CTAs own none).
+  static __host__ __device__ int own(int split) { return split == 1 ? 0 : kBN / split < 4 ? 4 : kBN / split; }
+  static __host__ __device__ int share_floats(int split) { return split * own(split) * kWeights; }
   static int rest(int experts, int split) {
-    return kScaleBytes + (split > 1 ? kShareBytes : 0) + (int)sizeof(Barriers) +
+    return kScaleBytes + 4 * share_floats(split) + (int)sizeof(Barriers) +
            4 * TileList<kBN, kWeights, 0>::ints(experts);
   }
 };
@@ -61,8 +63,9 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* scales = reinterpret_cast<float*>(smem + stages * L::kStageBytes);
-  float* shares = scales + L::kScaleBytes / 4;  // [split][kBN / split][128]
-  Barriers* bar = reinterpret_cast<Barriers*>(shares + (split > 1 ? L::kShareBytes / 4 : 0));
+  float* shares = scales + L::kScaleBytes / 4;  // [rank of the sender][own columns / 4][row of B in the tile][4]
+  const int own = L::own(split);
+  Barriers* bar = reinterpret_cast<Barriers*>(shares + L::share_floats(split));
   int* first = reinterpret_cast<int*>(bar + 1);
   const int w = warp_index(), lane = threadIdx.x & 31;
   const int rank = split > 1 ? (int)cluster_rank() : 0;
@@ -81,7 +84,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         mbar_init(&bar->sfull[i], 32);
         mbar_init(&bar->sempty[i], kSumWarps);
       }
-      mbar_init(&bar->got, kSumWarps * split);
+      mbar_init(&bar->got, 1);
       mbar_init(&bar->taken, kSumWarps * split);
       fence_mbar_init();
       tma_prefetch_desc(&amap);
@@ -102,6 +105,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   const int tiles = first[member_count(p)];
   const int lg_split = __ffs(split) - 1;  // 1, 4 or 8: shifts, for a division takes as long as the copy of a block
   const int t0 = blockIdx.x >> lg_split, step = gridDim.x >> lg_split;
+  bool ok = true;
   // This CTA's share of a tile's blocks.
   auto share = [&](const Tile& tl, int& begin, int& end) {
     begin = (tl.nkb * rank) >> lg_split;
@@ -110,7 +114,6 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 
   if (w == kSumWarps) {
     uint32_t s = 0, phase = 1, sent = 0;
-    bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
       const Tile tl = Tiles::at(p, first, t);
       int kb, end;
@@ -143,7 +146,6 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     constexpr uint32_t kIdesc = idesc_e4m3(kWeights, kBN);
     const uint64_t desc0 = operand_desc(smem_u32(smem));
     uint32_t s = 0, phase = 0, buf = 0, tphase = 1;
-    bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
       const Tile tl = Tiles::at(p, first, t);
       int kb, end;
@@ -177,7 +179,6 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   } else if (w == kSumWarps + 2) {
     const int64_t kblocks = (p.a_cols + kBK - 1) / kBK, nblocks = (p.b_rows + 127) / 128;
     uint32_t it = 0;
-    bool ok = true;
     for (int t = t0; t < tiles && ok; t += step) {
       const Tile tl = Tiles::at(p, first, t);
       int kb, end;
@@ -223,7 +224,6 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     const uint32_t sc = smem_u32(scales);
     const int n_in_tile = 32 * w + lane;
     uint32_t batch = 0, buf = 0, tphase = 0, round = 0;
-    bool ok = true;
     auto store = [&](const Tile& tl, int c, float v) {
       if (c >= tl.rows || n_in_tile >= tl.cols) return;
       const int64_t at = (tl.out_row + c) * p.b_rows + tl.n0 + n_in_tile;
@@ -296,37 +296,43 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         for (int i = 0; i < kBN; ++i) store(tl, i, acc[i]);
         continue;
       }
-      // Column c belongs to rank c / (kBN / split); its partial sums lie in
-      // shares[rank of the sender][c % (kBN / split)][lane of the tile].
-      const int own = kBN >> lg_split, lg = __ffs(own) - 1;
+      // Column c belongs to rank c / own.  Columns travel in fours.
+      const int lg = __ffs(own) - 1;
       ok = mbar_wait_cluster(&bar->taken, (round & 1) ^ 1, p.status);
       if (!ok) break;
-      const uint32_t mine = smem_u32(shares) + 4 * (rank * own * kWeights + n_in_tile);
+      const int held = max(0, min(own, tl.rows - rank * own));  // columns of this CTA that exist
+      if (w == 0 && lane == 0) mbar_arrive_expect_tx(&bar->got, split * kWeights * 4 * ((held + 3) & ~3));
+      const uint32_t mine = smem_u32(shares) + 4 * (rank * own * kWeights + 4 * n_in_tile), got = smem_u32(&bar->got);
 #pragma unroll
-      for (int i = 0; i < kBN; ++i) {
+      for (int i = 0; i < kBN; i += 4) {
         if (i >= tl.rows) break;
-        const uint32_t dst = map_to_cta(mine + 4 * (i & (own - 1)) * kWeights, i >> lg);
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(acc[i]) : "memory");
+        store_async(map_to_cta(mine + 4 * (i & (own - 1)) * kWeights, i >> lg), acc[i], acc[i + 1], acc[i + 2], acc[i + 3],
+                    map_to_cta(got, i >> lg));
       }
-      __syncwarp();
-      if (lane < split) mbar_arrive_cluster_release(map_to_cta(smem_u32(&bar->got), lane));
       ok = mbar_wait_cluster(&bar->got, round & 1, p.status);
       if (!ok) break;
-      const int held = min(own, tl.rows - rank * own);  // columns of this CTA that exist
-#pragma unroll 2
-      for (int c = 0; c < held; ++c) {
-        float part[8];  // all read before the first is added
+#pragma unroll 1
+      for (int c = 0; c < held; c += 4) {
+        float4 part[8];  // all read before the first is added
 #pragma unroll
         for (int r = 0; r < 8; ++r)
-          if (r < split) part[r] = shares[(r * own + c) * kWeights + n_in_tile];
-        float sum = 0.0f;
+          if (r < split) part[r] = *reinterpret_cast<const float4*>(shares + (r * own + c) * kWeights + 4 * n_in_tile);
+        float4 sum = part[0];
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < split) sum = __fadd_rn(sum, part[r]);
-        store(tl, rank * own + c, sum);
+        for (int r = 1; r < 8; ++r)
+          if (r < split)
+            sum = make_float4(__fadd_rn(sum.x, part[r].x), __fadd_rn(sum.y, part[r].y), __fadd_rn(sum.z, part[r].z),
+                              __fadd_rn(sum.w, part[r].w));
+        const int at = rank * own + c;
+        store(tl, at, sum.x);
+        store(tl, at + 1, sum.y);
+        store(tl, at + 2, sum.z);
+        store(tl, at + 3, sum.w);
       }
-      __syncwarp();
-      if (lane < split) mbar_arrive_cluster_release(map_to_cta(smem_u32(&bar->taken), lane));
+      if (t + step < tiles) {
+        __syncwarp();
+        if (lane < split) mbar_arrive_cluster_release(map_to_cta(smem_u32(&bar->taken), lane));
+      }
       ++round;
     }
     if (!ok) report_timeout(p.status);
@@ -334,8 +340,18 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   __syncwarp();
   tcgen05_before_sync();
   __syncthreads();
-  // no CTA leaves while another may still write to its shared memory
-  if (split > 1) cluster_sync();
+  // No CTA leaves before the others are done with its barriers.  What they
+  // send it has arrived by then, as it waited for it; a CTA that gave up waiting
+  // stays until stores in flight have landed.
+  if (split > 1) {
+    cluster_arrive_relaxed();
+    cluster_wait();
+    if (!ok) {
+      const long long c0 = clock64();
+      while (clock64() - c0 < 1000000LL) {
+      }
+    }
+  }
   tcgen05_after_sync();
   if (w == kSumWarps + 1) tmem_dealloc(tmem, L::kTmemCols);
 }

@@ -200,8 +200,16 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, 
                "r"(c0), "r"(c1), "r"(src)
                : "memory");
 }
-// For data written to the cluster's shared memory: the arrival that publishes
-// it and the wait that sees it.
+// Four floats to the shared memory of a CTA of the cluster, their bytes counted
+// on a barrier of that CTA (both addresses from map_to_cta): the owner hears
+// of them without an arrival that would first wait for them.
+__device__ __forceinline__ void store_async(uint32_t dst, float a, float b, float c, float d, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+               "f"(a), "f"(b), "f"(c), "f"(d), "r"(bar)
+               : "memory");
+}
+// For the cluster's shared memory: an arrival after the thread's earlier
+// accesses, and a wait that sees what was written before the phase ended.
 __device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -234,6 +242,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The same without ordering memory (which waits for the thread's stores in flight).
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
   cluster_arrive();
   cluster_wait();
