@@ -513,13 +513,13 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 
 // Which of the two kernels a product runs on.  Up to 32 rows (96 per expert)
 // the thin kernel's tiles fit and it is ahead (5120 x 4096 weights, 1 / 16 rows:
-// 8.1 / 8.6 us against 20; 1100 rows to 16 experts of 4096 x 2048: 35.5 against
-// 42.9).  Above, the estimated times decide, in us, fitted to both kernels at
+// 6.2 / 6.1 us against 20; 1100 rows to 16 experts of 4096 x 2048: 38.3 against
+// 39.6).  Above, the estimated times decide, in us, fitted to both kernels at
 // 64 to 1024 rows, N 512 to 8192, K 512 to 8192: a start, then the blocks that
 // each CTA or pair sums one after another.  For instance, thin against pair at
-// 128 rows and 128 x 128 blocks: N 1024, K 4096 10.6 / 12.3; N 5120, K 4096 18.2 /
-// 13.7; N 8192, K 512 7.9 / 6.5.  Of 128 such products the rule picks the faster
-// kernel, or one within 10 percent of it, for all but two (14 percent).
+// 128 rows and 128 x 128 blocks: N 1024, K 4096 8.4 / 12.0; N 5120, K 4096 16.7 /
+// 12.8; N 8192, K 512 7.8 / 5.9.  Of 128 such products the rule picks the faster
+// kernel, or one within 4 percent of it.
 bool thin_is_faster(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   const int64_t members = a.offsets ? a.experts : 1;
   const int64_t rows = a.wgrad ? a.a_rows : (a.a_rows + members - 1) / members;
@@ -534,7 +534,7 @@ bool thin_is_faster(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   const ThinPlan t = thin_plan(a, ctx);
   const int64_t ctas = t.tiles * t.split, turns = (ctas + 2 * ctx.num_sms - 1) / (2 * ctx.num_sms);
   const double block = ctas > ctx.num_sms ? 0.6 : 0.45;  // two CTAs of an SM slow each other
-  const double thin = 4.5 + (t.split > 1 ? 4.5 : 0.0) + turns * kb / t.split * block;
+  const double thin = 4.5 + (t.split > 1 ? 2.0 : 0.0) + turns * kb / t.split * block;
   return thin < pair;
 }
 

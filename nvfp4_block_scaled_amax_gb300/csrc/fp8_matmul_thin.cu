@@ -14,8 +14,8 @@
 // Bound by reading the weights: two CTAs per SM keep up to 200 KB of operand
 // slices per SM in flight.  Warps 0-3 sum, warp 4 issues the copies, warp 5
 // the MMAs (kBuffers accumulators, so the hand-overs overlap), warp 6 the
-// scales.  64 rows to 16 experts of 4096 x 2048 weights: 23.5 us, 5.4 TB/s (79
-// percent of the copy rate); one row through 5120 x 4096: 7.7 us.
+// scales.  64 rows to 16 experts of 4096 x 2048 weights: 22.2 us, 5.7 TB/s (84
+// percent of the copy rate); one row through 5120 x 4096: 6.8 us.
 #include "fp8_tiles.cuh"
 
 namespace nvfp4 {
@@ -103,7 +103,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   tcgen05_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem, 0);
   const int tiles = first[member_count(p)];
-  const int lg_split = __ffs(split) - 1;  // 1, 4 or 8: shifts, for a division takes as long as the copy of a block
+  const int lg_split = __ffs(split) - 1;  // 1, 2, 4 or 8: shifts, for a division takes as long as the copy of a block
   const int t0 = blockIdx.x >> lg_split, step = gridDim.x >> lg_split;
   bool ok = true;
   // This CTA's share of a tile's blocks.
@@ -303,12 +303,17 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       const int held = max(0, min(own, tl.rows - rank * own));  // columns of this CTA that exist
       if (w == 0 && lane == 0) mbar_arrive_expect_tx(&bar->got, split * kWeights * 4 * ((held + 3) & ~3));
       const uint32_t mine = smem_u32(shares) + 4 * (rank * own * kWeights + 4 * n_in_tile), got = smem_u32(&bar->got);
+      // To the ranks from this one on, then to those before it, so that not all
+      // send to one CTA at a time (200 rows to 1040 x 8192: 12.6 to 11.7 us).
 #pragma unroll
-      for (int i = 0; i < kBN; i += 4) {
-        if (i >= tl.rows) break;
-        store_async(map_to_cta(mine + 4 * (i & (own - 1)) * kWeights, i >> lg), acc[i], acc[i + 1], acc[i + 2], acc[i + 3],
-                    map_to_cta(got, i >> lg));
-      }
+      for (int before = 0; before < 2; ++before)
+#pragma unroll
+        for (int i = 0; i < kBN; i += 4) {
+          if (i >= tl.rows) break;
+          if (((i >> lg) < rank) == before)
+            store_async(map_to_cta(mine + 4 * (i & (own - 1)) * kWeights, i >> lg), acc[i], acc[i + 1], acc[i + 2],
+                        acc[i + 3], map_to_cta(got, i >> lg));
+        }
       ok = mbar_wait_cluster(&bar->got, round & 1, p.status);
       if (!ok) break;
 #pragma unroll 1
@@ -388,15 +393,17 @@ ThinPlan thin_plan(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   ThinPlan t;
   t.bn = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   t.tiles = members * ((rows + t.bn - 1) / t.bn) * ((a.b_rows + kWeights - 1) / kWeights);
-  // Eight CTAs, or four, share a tile's blocks where all of them fit beside
-  // one another (two per SM) and each keeps two blocks or more; joining costs
-  // about 2 us.  5120 x 4096 weights, one row: 10.4 us alone, 7.7 us in fours
-  // (eights: two turns, 11.8 us); 1024 x 4096, 16 rows: 10.8, 7.6 and 6.6 us.
+  // Eight CTAs, four or two share a tile's blocks where all of them fit beside
+  // one another (two per SM) and each keeps two blocks or more.  5120 x 4096
+  // weights, one row: 10.6 us alone, 7.3 us in fours (eights: two turns, 10.7 us);
+  // 1024 x 4096, 16 rows: 8.5, 4.7 and 4.5 us.  Two gain less, so they want more
+  // blocks: 10240 x 8192, 32 rows 19.2 us against 23.8, 12800 x 2048, 16 rows 8.5
+  // against 8.3.
   const int64_t k = a.wgrad ? (a.a_cols + members - 1) / members : a.a_cols;
   const int64_t kb = (k + kBK - 1) / kBK;
   t.split = 1;
-  for (int s = 8; s >= 4 && t.split == 1; s /= 2)
-    if (t.tiles * s <= 2 * ctx.num_sms && kb >= 16) t.split = s;
+  for (int s = 8; s >= 2 && t.split == 1; s /= 2)
+    if (t.tiles * s <= 2 * ctx.num_sms && kb >= (s == 2 ? 32 : 16)) t.split = s;
   return t;
 }
 

@@ -307,3 +307,28 @@ def test_refusals():
             (nv.NVFP4Error, lambda: nv.quantize_fp8(x[:24], colwise=True))]:
         with pytest.raises(err):
             call()
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("M,N,K", [(3, 9900, 4112), (40, 9872, 4224),  # two CTAs share a tile's blocks
+                                   (4700, 4500, 144)])                # more tiles per CTA than are worked out ahead
+def test_product_of_many_tiles(M, N, K, block_rows):
+    a, b = operand(M, K, 1, M + K), operand(N, K, block_rows, N)
+    got = nv.matmul_fp8(a, b)
+    check_product(got, exact(a), exact(b), torch.bfloat16)
+    assert torch.equal(got, nv.matmul_fp8(a, b))
+    assert nv.device_status() == 0
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_clusters_that_join_tile_after_tile(block_rows):
+    """23 members of 65 rows are 46 tiles of 64 rows, more than there are clusters of eight CTAs at a time."""
+    counts = [65] * 23 + [5]
+    offsets, off = member_offsets(counts)
+    a, b = operand(off[-1], 2064, 1, 1), operand(120, 2064, block_rows, 2, lead=(len(counts),))
+    got = nv.matmul_fp8_grouped(a, b, offsets, out_dtype=torch.float32)
+    av, bv = exact(a), exact(b)
+    for e in range(len(counts)):
+        check_product(got[off[e]:off[e + 1]], av[off[e]:off[e + 1]], bv[e], torch.float32)
+    assert torch.equal(got, nv.matmul_fp8_grouped(a, b, offsets, out_dtype=torch.float32))
+    assert nv.device_status() == 0
