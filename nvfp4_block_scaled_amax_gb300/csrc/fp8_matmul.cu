@@ -18,16 +18,16 @@
 // warps of each CTA read the finished accumulator of their 128 rows and add
 // it, scaled, to their registers (128 per thread) while the next block is
 // multiplied.  Output leaves through shared memory by TMA while the next
-// tile is summed.
+// tile is summed; one more warp works the tiles out ahead.
 //
-// Measured at 8192 x 5120 x 8192 (BF16 out, 128 x 128 blocks of B): 220 us,
-// 3.1 PFLOP/s; with a scale per row of B (4096 x 4864 x 16384, FP32 out) 266 us
+// Measured at 8192 x 5120 x 8192 (BF16 out, 128 x 128 blocks of B): 217 us,
+// 3.2 PFLOP/s; with a scale per row of B (4096 x 4864 x 16384, FP32 out) 266 us
 // against 204.  The MMAs alone take 168 us, with their operand copies 185 us
 // (256 x 128 MMAs: 240 us, so the tile is 256 wide although two accumulators
 // then leave no third to run ahead).  What bounds it is the hand-over: an
 // accumulator must be heard of, read, scaled and given back within the time
 // of one block's MMAs (about 520 cycles), of which the scaled sums alone take
-// 290.  The tensor pipe is 76 percent busy (53 with a scale per row of B).
+// 290.  The tensor pipe is 78 percent busy (55 with a scale per row of B).
 #include "fp8_tiles.cuh"
 
 namespace nvfp4 {
