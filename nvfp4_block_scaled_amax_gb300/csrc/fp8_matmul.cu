@@ -134,7 +134,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   };
 
   if (w < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kColScales ? 40 : 24));
     // These loops are the same in all lanes of their warp; one lane issues.
     if (w == 0) {
       // both operands' slices, counted on the first CTA's barrier
@@ -291,7 +291,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kColScales ? 232 : 240));
     const int q = w & 3, half = (w - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + half * 128;
     const uint32_t tempty0 = map_to_cta(smem_u32(&bar->tempty[0]), 0);
