@@ -94,7 +94,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         mbar_init(&bar->tempty[i], 2 * kSumWarps);
       }
       for (int i = 0; i < kScaleStages; ++i) {
-        mbar_init(&bar->sfull[i], 32);
+        mbar_init(&bar->sfull[i], kColScales ? 33 : 32);  // the lanes' own copies (and the bulk copies)
         mbar_init(&bar->sempty[i], kSumWarps);
       }
       for (int i = 0; i < kTileSlots; ++i) {
@@ -213,10 +213,19 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       const int64_t kblocks = (p.a_cols + kBK - 1) / kBK, nblocks = (p.b_rows + 127) / 128;
       uint32_t it = 0;
       bool ok = true;
+      // A scale per row of both: rows of memory, one bulk copy each where 16-byte
+      // boundaries allow, instead of 12 copies of 4 bytes a lane (4096 x 4864 x
+      // 16384: 235 us against 243).
+      const bool a_bulk = p.a_rows % 4 == 0 && (reinterpret_cast<uintptr_t>(p.sa) & 15) == 0;
+      const bool b_bulk = kColScales && p.b_rows % 4 == 0 && (reinterpret_cast<uintptr_t>(p.sb) & 15) == 0;
       for (int i = 0; i < items && ok; ++i) {
         if (!(ok = listed(i))) break;
         const TileSlot tl = *slot_of(i);
         leave(i);
+        const bool bulk = kColScales && a_bulk && b_bulk && tl.a_row % 4 == 0;
+        const uint32_t a_bytes = 4 * (uint32_t)max((int64_t)0, min((int64_t)128, p.a_rows - tl.a_row - 128 * rank));
+        const uint32_t b_bytes = 4 * (uint32_t)tl.cols;
+        if (bulk) fence_proxy_async_shared();  // another tile's may have come by plain copies
         const int64_t member = p.wgrad || tl.nkb == 0 ? 0 : tl.member;
         const float* pa = p.sa + (int64_t)tl.kb0 * p.a_rows + tl.a_row;
         const float* pb;
@@ -242,6 +251,25 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           }
           uint32_t dst = smem_u32(scales + s * kScaleBatch * kScaleFloats) + 4 * lane;
           const int n = min(kScaleBatch, tl.nkb - kb);
+          if (bulk) {
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&bar->sfull[s], n * (a_bytes + b_bytes));
+              const float *qa = pa + 128 * rank, *qb = pb;
+              for (int j = 0; j < n; ++j) {
+                const uint32_t to = dst + 4 * kScaleFloats * j;
+                if (a_bytes) bulk_load(to, qa, a_bytes, &bar->sfull[s]);
+                bulk_load(to + 512, qb, b_bytes, &bar->sfull[s]);
+                qa += p.a_rows;
+                qb += p.b_rows;
+              }
+            }
+            __syncwarp();
+            pa += n * p.a_rows;
+            pb += n * p.b_rows;
+            cp_async_arrive(&bar->sfull[s]);
+            continue;
+          }
+          if (kColScales && lane == 0) mbar_arrive(&bar->sfull[s]);
           for (int j = 0; j < n; ++j, dst += 4 * kScaleFloats) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) cp_async4(dst + 128 * i, pa + oa[i], true);

@@ -332,3 +332,22 @@ def test_clusters_that_join_tile_after_tile(block_rows):
         check_product(got[off[e]:off[e + 1]], av[off[e]:off[e + 1]], bv[e], torch.float32)
     assert torch.equal(got, nv.matmul_fp8_grouped(a, b, offsets, out_dtype=torch.float32))
     assert nv.device_status() == 0
+
+
+def test_scales_that_start_off_a_boundary():
+    """Members that start at any row, and widths that are no multiples of four: scales with a row each, 4-byte aligned."""
+    counts = [301, 258, 0, 515, 130]
+    offsets, off = member_offsets(counts)
+    for N, pad in ((260, 0), (259, 0), (260, 1)):
+        a, b = operand(off[-1] + 4, 528, 1, 1), operand(N, 528, 1, 2, lead=(len(counts),))
+        if pad:  # the same scales, one float further into their storage
+            storage = torch.cat([torch.zeros(1, device="cuda"), b.scale.flatten()])
+            b = nv.FP8Operand(b.data, storage[1:].view(b.scale.shape), 1)
+        got = nv.matmul_fp8_grouped(a, b, offsets, out_dtype=torch.float32)
+        av, bv = exact(a), exact(b)
+        for e in range(len(counts)):
+            check_product(got[off[e]:off[e + 1]], av[off[e]:off[e + 1]], bv[e], torch.float32)
+        assert nv.device_status() == 0
+    a, b = operand(2503, 400, 1, 3), operand(2301, 400, 1, 4)
+    check_product(nv.matmul_fp8(a, b, out_dtype=torch.float32), exact(a), exact(b), torch.float32)
+    assert nv.device_status() == 0
