@@ -20,14 +20,14 @@
 // multiplied.  Output leaves through shared memory by TMA while the next
 // tile is summed; one more warp works the tiles out ahead.
 //
-// Measured at 8192 x 5120 x 8192 (BF16 out, 128 x 128 blocks of B): 217 us,
-// 3.2 PFLOP/s; with a scale per row of B (4096 x 4864 x 16384, FP32 out) 266 us
-// against 204.  The MMAs alone take 168 us, with their operand copies 185 us
+// Measured at 8192 x 5120 x 8192 (BF16 out, 128 x 128 blocks of B): 214 us,
+// 3.2 PFLOP/s; with a scale per row of B (4096 x 4864 x 16384, FP32 out) 236 us
+// against 199.  The MMAs alone take 168 us, with their operand copies 185 us
 // (256 x 128 MMAs: 240 us, so the tile is 256 wide although two accumulators
 // then leave no third to run ahead).  What bounds it is the hand-over: an
 // accumulator must be heard of, read, scaled and given back within the time
 // of one block's MMAs (about 520 cycles), of which the scaled sums alone take
-// 290.  The tensor pipe is 78 percent busy (55 with a scale per row of B).
+// 290.  The tensor pipe is 79 percent busy (60 with a scale per row of B).
 #include "fp8_tiles.cuh"
 
 namespace nvfp4 {
@@ -134,6 +134,10 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   };
 
   if (w < 4) {
+    // 128 threads here, 256 that sum, 168 registers each at launch.  Every
+    // register that these warps can spare helps the sums (72 / 216: weight gradient
+    // 153 us against 147, the product above 215.5 against 213.7); with a scale
+    // per row of B they need more than 24.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kColScales ? 40 : 24));
     // These loops are the same in all lanes of their warp; one lane issues.
     if (w == 0) {
