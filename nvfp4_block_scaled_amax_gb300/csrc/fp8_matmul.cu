@@ -551,7 +551,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 // each CTA or pair sums one after another.  For instance, thin against pair at
 // 128 rows and 128 x 128 blocks: N 1024, K 4096 8.4 / 12.0; N 5120, K 4096 16.7 /
 // 12.8; N 8192, K 512 7.8 / 5.9.  Of 128 such products the rule picks the faster
-// kernel, or one within 4 percent of it.
+// kernel, or one within 5 percent of it.
 bool thin_is_faster(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   const int64_t members = a.offsets ? a.experts : 1;
   const int64_t rows = a.wgrad ? a.a_rows : (a.a_rows + members - 1) / members;
@@ -561,7 +561,7 @@ bool thin_is_faster(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   const int64_t pair_tiles = members * ((rows + 255) / 256) * ((a.b_rows + 255) / 256);
   const int64_t pairs = ctx.num_sms / 2, over = pair_tiles % pairs;
   const double last = over == 0 ? 0.0 : 2 * over <= pairs ? 0.65 : 1.0;  // of a turn: halved tiles
-  const double pair = 4.5 + (pair_tiles / pairs + last) * kb * (a.b_block_rows == 1 ? 0.56 : 0.38) +
+  const double pair = 4.5 + (pair_tiles / pairs + last) * kb * (a.b_block_rows == 1 ? 0.50 : 0.38) +
                       (a.b_rows * (a.out_bf16 ? 2 : 4) % 16 ? 2.5 : 0.0);  // rows written by the warps
   const ThinPlan t = thin_plan(a, ctx);
   const int64_t ctas = t.tiles * t.split, turns = (ctas + 2 * ctx.num_sms - 1) / (2 * ctx.num_sms);
