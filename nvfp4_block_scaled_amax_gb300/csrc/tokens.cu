@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, in
 // first one writes the maps, and each copies its share of the rows, a warp
 // per piece of 2 KB.
 constexpr int kCopyPiece = 2048;
+constexpr int kCopyRows = 6144;  // at most, one integer of shared memory each
 
 template <bool kCopy>
 __global__ void __launch_bounds__(kSortThreads)
@@ -425,16 +426,17 @@ cudaError_t launch_sort_tokens(const SortArgs& args, const LaunchCtx& ctx) {
 
 cudaError_t launch_dispatch_tokens(const SortArgs& s, const void* x, void* out, const TokenArgs& t,
                                    const LaunchCtx& ctx) {
-  // Few slots and rows: one launch (8 tokens of 1024 BF16, top 2: 3.3 us; the sort
-  // of 1024 slots alone takes 3.4 us, the gather by itself 4.0).
+  // Few slots and rows: one launch (1024 tokens of 4096 BF16, top 2, 8 experts: 6.6
+  // us against 7.9 in two; of 1024, 32 experts, members of 128: 7.6 against 10.2;
+  // 8 tokens: 3.3 us).  The warps hold the ids of 2048 slots between the two walks.
   const int64_t row_bytes = t.width * (t.bf16 ? 2 : 4);
-  if (s.slots > 1024 || s.rows > 4096 || row_bytes == 0) {
+  if (s.slots > kSortChunk || s.rows > kCopyRows || row_bytes == 0) {
     const cudaError_t e = launch_sort_tokens(s, ctx);
     return e != cudaSuccess ? e : launch_gather_tokens(x, out, t, ctx);
   }
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e =
-      allow_smem(reinterpret_cast<const void*>(&sort_place_kernel<true>), sort_smem(kMaxExperts, 4096), allowed);
+      allow_smem(reinterpret_cast<const void*>(&sort_place_kernel<true>), sort_smem(kMaxExperts, kCopyRows), allowed);
   if (e != cudaSuccess) return e;
   const int64_t units = s.rows * ((row_bytes + kCopyPiece - 1) / kCopyPiece);
   const int64_t want = (units + kSortWarps - 1) / kSortWarps;

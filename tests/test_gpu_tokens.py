@@ -208,3 +208,18 @@ def test_refusals():
             (TypeError, lambda: nv.combine_tokens_grad(x.float(), rows, plan, w))]:
         with pytest.raises(err):
             call()
+
+
+@pytest.mark.parametrize("T,topk,E,align", [(1024, 2, 32, 128), (1024, 2, 33, 128), (683, 3, 32, 100), (512, 4, 700, 1),
+                                            (2048, 1, 1, 600), (300, 2, 3, 1000), (2049, 1, 40, 16)])
+def test_dispatch_at_the_limits_of_one_launch(T, topk, E, align):
+    """2048 slots, 6144 rows; members padded by more rows than a CTA has threads; more experts than threads."""
+    ids = make_ids(T, topk, E, seed=T + align)
+    x = torch.randn(T, 72, generator=torch.Generator().manual_seed(1)).bfloat16()
+    rows, plan = nv.dispatch_tokens(x.cuda(), ids.cuda(), E, align=align)
+    offsets, row_of_slot, slots = plan_by_loop(ids, E, align)
+    s = torch.tensor(slots)
+    want = torch.where((s >= 0)[:, None], x[s.clamp(min=0) // topk], torch.zeros((), dtype=torch.bfloat16))
+    assert torch.equal(rows.cpu(), want)
+    assert plan.offsets.tolist() == offsets and plan.slot_of_row.tolist() == slots
+    assert plan.row_of_slot.flatten().tolist() == row_of_slot
