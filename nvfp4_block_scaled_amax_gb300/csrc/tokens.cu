@@ -228,8 +228,10 @@ gather_kernel(const uint8_t* x, uint8_t* out, TokenArgs a, int64_t row_bytes) {
     }
   }
   for (int64_t r0 = warp * kZeroRows; r0 < a.rows; r0 += warps * kZeroRows) {
-    const int slot = lane < kZeroRows && r0 + lane < a.rows ? a.slot_of_row[r0 + lane] : 0;
-    unsigned empty = __ballot_sync(0xFFFFFFFFu, slot < 0 || slot >= slots);
+    // (a lane without a row of its own counts as none, whatever the number of slots: 0 is no valid slot of 0 tokens)
+    const bool there = lane < kZeroRows && r0 + lane < a.rows;
+    const int slot = there ? a.slot_of_row[r0 + lane] : 0;
+    unsigned empty = __ballot_sync(0xFFFFFFFFu, there && (slot < 0 || slot >= slots));
     for (; empty; empty &= empty - 1) {
       uint4* dst = reinterpret_cast<uint4*>(out + (r0 + __ffs(empty) - 1) * row_bytes);
       for (int64_t i = lane; i < row_bytes / 16; i += 32) __stcs(dst + i, make_uint4(0, 0, 0, 0));
