@@ -328,8 +328,9 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const uint4* 
   grid_begin();
   if (blockIdx.x >= a.tokens) {
     const int64_t r0 = (blockIdx.x - a.tokens) * 32;
-    const int mine = r0 + (threadIdx.x & 31) < a.rows ? a.slot_of_row[r0 + (threadIdx.x & 31)] : 0;
-    unsigned empty = __ballot_sync(0xFFFFFFFFu, mine < 0 || mine >= a.tokens * a.topk);
+    const bool there = r0 + (threadIdx.x & 31) < a.rows;  // (a lane past the rows has none to zero)
+    const int mine = there ? a.slot_of_row[r0 + (threadIdx.x & 31)] : 0;
+    unsigned empty = __ballot_sync(0xFFFFFFFFu, there && (mine < 0 || mine >= a.tokens * a.topk));
     for (; empty; empty &= empty - 1) {
       uint4* dst = drows + (r0 + __ffs(empty) - 1) * vecs;
       for (int i = threadIdx.x; i < vecs; i += kRowThreads) __stcs(dst + i, make_uint4(0, 0, 0, 0));
