@@ -159,7 +159,9 @@ sort_place_kernel(SortArgs a, int64_t chunk, const uint8_t* x, uint8_t* out, int
     // (a warp per member where that is a few rows, or the CTA)
     const int group = a.align <= kSortThreads ? 32 : kSortThreads, groups = kSortThreads / group;
     for (int e = self * groups + threadIdx.x / group; e < a.experts; e += nchunks * groups)
-      for (int r = first[e] + total[e] + threadIdx.x % group; r < first[e + 1]; r += group) a.slot_of_row[r] = -1;
+      // (64 bits: a member may end just below 2^31, a lane's first row and its next one past it)
+      for (int64_t r = (int64_t)first[e] + total[e] + threadIdx.x % group; r < first[e + 1]; r += group)
+        a.slot_of_row[r] = -1;
     for (int64_t r = first[a.experts] + (int64_t)self * kSortThreads + threadIdx.x; r < a.rows;
          r += (int64_t)nchunks * kSortThreads)
       a.slot_of_row[r] = -1;
