@@ -449,6 +449,10 @@ nvfp4_status nvfp4_fp8_quantize(const void* x, int dtype, int64_t batch, int64_t
  * 1 or 128.  The sum over a block of 128 is accumulated in FP32 by the tensor
  * cores, scaled and added in FP32; out is rounded once (BF16) or kept (FP32).
  * K % 16 == 0; any M, N >= 0; K = 0 gives zero.
+ * Scales of 2^-109 (the cast's smallest) to 2^100, and 0: no step leaves
+ * FP32's range then unless a block's scaled sum does, whatever the product of
+ * the two scales is.  Beyond 2^100 (blocks with values of 5e32) a block's sum
+ * times one scale may become infinite before the other brings it back.
  */
 nvfp4_status nvfp4_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_t* b, const float* b_scale,
                               int b_block_rows, int64_t M, int64_t N, int64_t K, void* out, int out_dtype,

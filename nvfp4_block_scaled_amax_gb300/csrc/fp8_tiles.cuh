@@ -386,6 +386,17 @@ __device__ __forceinline__ void tmem_read_16x256(uint32_t taddr, uint32_t (&u)[3
       : "memory");
 }
 
+// Whole warp: 16 consecutive columns of the lane from registers, complete on return.
+__device__ __forceinline__ void tmem_write(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15};\n"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
+
 // Two FP32 values in a 64-bit register pair, and arithmetic on both.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
