@@ -463,6 +463,9 @@ nvfp4_status nvfp4_fp8_matmul(const uint8_t* a, const float* a_scale, const uint
  * offsets[e] .. offsets[e+1], device int32, ascending from 0, any alignment),
  * b [num_experts][N][K] one matrix per expert; out [rows][N], zero for rows
  * from offsets[num_experts] on.
+ * Offsets that do not ascend from 0 to at most `rows` set bit 2 of the status
+ * word; an offset below an earlier one counts as that one, one outside 0..rows
+ * as the nearer end, and rows before the first member are not written.
  */
 nvfp4_status nvfp4_fp8_matmul_grouped(const uint8_t* a, const float* a_scale, const uint8_t* b, const float* b_scale,
                                       int b_block_rows, int64_t rows, int64_t N, int64_t K, int num_experts,
@@ -474,6 +477,8 @@ nvfp4_status nvfp4_fp8_matmul_grouped(const uint8_t* a, const float* a_scale, co
  *     out[e][m][n] = sum over rows r of member e of a[m][r] b[n][r],
  * zero for an empty member.  rows % 16 == 0, and every offset a multiple of
  * 128 (nvfp4_sort_tokens with align 128), so that no block spans two members.
+ * (The last may be `rows` instead.)  Other offsets set bit 2 of the status word:
+ * two members that share a block of 128 both count all of it.
  */
 nvfp4_status nvfp4_fp8_matmul_grouped_wgrad(const uint8_t* a, const float* a_scale, const uint8_t* b,
                                             const float* b_scale, int64_t M, int64_t N, int64_t rows,
@@ -481,11 +486,13 @@ nvfp4_status nvfp4_fp8_matmul_grouped_wgrad(const uint8_t* a, const float* a_sca
                                             void* stream);
 
 /*
- * Per-device status word of bounded device-side waits: bit 0 = a wait for a
- * tile copy ran out; bit 1 = a grid-wide barrier of a single-pass call ran
- * out.  Synchronizes the current device, copies the word into
- * *status and, when clear != 0, resets it.  Returns NVFP4_ERR_TIMEOUT when a
- * bit was set, NVFP4_OK otherwise, NVFP4_ERR_CUDA if the copy failed.
+ * Per-device status word of what kernels find out: bit 0 = a wait for a tile
+ * copy ran out; bit 1 = a grid-wide barrier of a single-pass call ran out;
+ * bit 2 = a product by expert met member offsets that it does not take.
+ * Synchronizes the current device, copies the word into *status and, when
+ * clear != 0, resets it.  Returns NVFP4_ERR_TIMEOUT when bit 0 or 1 was set,
+ * NVFP4_ERR_SHAPE when only bit 2 was, NVFP4_OK for 0, NVFP4_ERR_CUDA if the
+ * copy failed.
  */
 nvfp4_status nvfp4_device_status(uint32_t* status, int clear);
 

@@ -458,11 +458,12 @@ def swizzle_scales(compact: torch.Tensor, rows: int, scale_cols: int, out: torch
 
 
 def device_status(clear: bool = True) -> int:
-    """Synchronizes the current device and returns its status word (0 = no
-    device-side wait ran out)."""
+    """Synchronizes the current device and returns its status word: 0, or the
+    sum of 1 (a wait for a tile copy ran out), 2 (a grid-wide barrier ran out)
+    and 4 (a product by expert met member offsets that it does not take)."""
     v = ctypes.c_uint32(0)
     rc = _lib.load().nvfp4_device_status(ctypes.byref(v), int(clear))
-    if rc not in (0, 7):
+    if rc not in (0, 2, 7):
         _lib.check(rc, "nvfp4_device_status")
     return v.value
 

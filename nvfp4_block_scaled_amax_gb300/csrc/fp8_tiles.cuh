@@ -27,28 +27,9 @@ struct MatmulKernelArgs {
 // ---------------------------------------------------------------------------
 // Members and tiles
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ int64_t clamp_offset(const MatmulKernelArgs& p, int e) {
-  const int64_t limit = p.wgrad ? p.a_cols : p.a_rows;
-  const int64_t v = p.offsets[e];
-  return v < 0 ? 0 : v > limit ? limit : v;
-}
-// Rows (wgrad: columns) of A that member e holds.  Member `experts` of a
-// forward product is the rows past the last member: nothing to sum, zeros to
-// write.
-__device__ __forceinline__ void member_range(const MatmulKernelArgs& p, int e, int64_t& begin, int64_t& end) {
-  const int64_t limit = p.wgrad ? p.a_cols : p.a_rows;
-  if (p.offsets == nullptr) {
-    begin = 0;
-    end = limit;
-  } else if (e == p.experts) {
-    begin = clamp_offset(p, e);
-    end = limit;
-  } else {
-    begin = clamp_offset(p, e);
-    end = clamp_offset(p, e + 1);
-    if (end < begin) end = begin;
-  }
-}
+// Member e holds the rows (wgrad: columns) offsets[e] .. offsets[e + 1] of A.
+// Member `experts` of a forward product is the rows past the last member:
+// nothing to sum, zeros to write.
 __device__ __forceinline__ int member_count(const MatmulKernelArgs& p) {
   return p.offsets == nullptr ? 1 : p.experts + (p.wgrad ? 0 : 1);
 }
@@ -70,25 +51,41 @@ struct Tile {
 // tiles in flight share both operands' rows in L2.  kBand 0: one band.
 template <int kTM, int kTN, int kBand>
 struct TileList {
-  static __device__ __forceinline__ int64_t rows_of(const MatmulKernelArgs& p, int e) {
-    if (p.wgrad) return p.a_rows;
-    int64_t begin, end;
-    member_range(p, e, begin, end);
-    return end - begin;
-  }
   // Integers for `experts` members.
   static constexpr __host__ __device__ int ints(int experts) { return 2 * experts + 3; }
-  // One warp fills the list.
+  // One warp fills the list.  Offsets that are no valid ones are reported, and
+  // made to cut A into members all the same (each at least the one before, none
+  // outside A), so that whatever they are the tiles are counted, read and written
+  // inside the tensors and no two members share a row of the output.
   static __device__ __forceinline__ void fill(const MatmulKernelArgs& p, int* first) {
     const int lane = threadIdx.x & 31, members = member_count(p);
+    const int limit = (int)(p.wgrad ? p.a_cols : p.a_rows);
     int* start = first + members + 1;
-    if (p.offsets != nullptr)
-      for (int e = lane; e <= p.experts; e += 32) start[e] = (int)clamp_offset(p, e);
+    if (p.offsets != nullptr) {
+      bool bad = false;
+      for (int e = lane; e <= p.experts; e += 32) {
+        const int v = p.offsets[e], before = e > 0 ? p.offsets[e - 1] : 0;
+        bad |= v < before || v > limit;
+        // rows before the first member would stay unwritten; a block of two members has one scale
+        bad |= p.wgrad ? v % kBK != 0 && v != limit : e == 0 && v != 0;
+        start[e] = max(0, min(v, limit));
+      }
+      __syncwarp();
+      if (__any_sync(0xFFFFFFFFu, bad)) {
+        if (lane == 0) {
+          atomicOr(p.status, kStatusOffsets);
+          for (int e = 1; e <= p.experts; ++e) start[e] = max(start[e], start[e - 1]);
+        }
+        __syncwarp();
+      }
+    }
     const int64_t tn = (p.b_rows + kTN - 1) / kTN;
     int run = 0;
     for (int e0 = 0; e0 < members; e0 += 32) {
       const int e = e0 + lane;
-      const int tiles = e < members ? (int)((rows_of(p, e) + kTM - 1) / kTM * tn) : 0;
+      int64_t rows = p.wgrad ? p.a_rows : limit;
+      if (p.offsets != nullptr && !p.wgrad && e < members) rows = (e < p.experts ? start[e + 1] : limit) - start[e];
+      const int tiles = e < members ? (int)((rows + kTM - 1) / kTM * tn) : 0;
       int incl = tiles;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -113,7 +110,7 @@ struct TileList {
     if (p.offsets != nullptr) {
       const int* start = first + member_count(p) + 1;
       begin = start[lo];
-      if (lo < p.experts) end = max((int)begin, start[lo + 1]);
+      if (lo < p.experts) end = start[lo + 1];
     }
     const int64_t M = p.wgrad ? p.a_rows : end - begin;
     const int mt = (int)((M + kTM - 1) / kTM), nt = (int)((p.b_rows + kTN - 1) / kTN);

@@ -661,7 +661,8 @@ nvfp4_status nvfp4_device_status(uint32_t* status, int clear) {
     if (cudaMemcpyToSymbol(g_nvfp4_status_word, &zero, sizeof zero) != cudaSuccess) return NVFP4_ERR_CUDA;
   }
   *status = v;
-  return v ? NVFP4_ERR_TIMEOUT : NVFP4_OK;
+  if (v & (kStatusWaitTimeout | kStatusGridTimeout)) return NVFP4_ERR_TIMEOUT;
+  return v ? NVFP4_ERR_SHAPE : NVFP4_OK;  // (kStatusOffsets)
 }
 
 }  // extern "C"
