@@ -359,6 +359,7 @@ nvfp4_status nvfp4_swizzle_scales(const uint8_t* compact, uint8_t* swizzled, int
  */
 #define NVFP4_MAX_EXPERTS 1024
 #define NVFP4_MAX_TOPK 64
+#define NVFP4_MAX_ALIGN (1 << 20)
 
 /*
  * Rows of the sorted tensor (its capacity) and bytes of sort scratch for
@@ -381,8 +382,9 @@ nvfp4_status nvfp4_token_rows(int64_t tokens, int topk, int num_experts, int ali
  *   offsets [num_experts + 1]; rows: as nvfp4_token_rows gives;
  *   scratch: scratch_bytes of device memory (NULL where that is 0), contents
  *   irrelevant, not shared by calls that can run at the same time.
- * 1 <= num_experts <= NVFP4_MAX_EXPERTS, 1 <= topk <= NVFP4_MAX_TOPK, align
- * >= 1, tokens >= 0, rows < 2^31.  One launch up to 2048 slots, two above.
+ * 1 <= num_experts <= NVFP4_MAX_EXPERTS, 1 <= topk <= NVFP4_MAX_TOPK, 1 <=
+ * align <= NVFP4_MAX_ALIGN, tokens >= 0, slots and rows < 2^31.  One launch up
+ * to 2048 slots, two above.
  */
 nvfp4_status nvfp4_sort_tokens(const int32_t* expert_ids, int64_t tokens, int topk, int num_experts, int align,
                                int32_t* offsets, int32_t* row_of_slot, int32_t* slot_of_row, int64_t rows,

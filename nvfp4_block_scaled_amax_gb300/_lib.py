@@ -32,6 +32,7 @@ SINGLE_PASS_WORKSPACE_BYTES = 4096
 MAX_GROUPS = 64
 MAX_EXPERTS = 1024
 MAX_TOPK = 64
+MAX_ALIGN = 1 << 20
 
 
 class Output(ctypes.Structure):

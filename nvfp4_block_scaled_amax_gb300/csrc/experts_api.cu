@@ -23,7 +23,7 @@ int64_t capacity(int64_t slots, int experts, int align) {
 
 nvfp4_status check_sort(int64_t tokens, int topk, int experts, int align) {
   if (!size_ok(tokens) || topk < 1 || topk > NVFP4_MAX_TOPK || experts < 1 || experts > kMaxExperts || align < 1 ||
-      align > (1 << 20))
+      align > NVFP4_MAX_ALIGN)
     return NVFP4_ERR_SHAPE;
   if (!size_ok(tokens * topk) || !size_ok(capacity(tokens * topk, experts, align))) return NVFP4_ERR_SHAPE;
   return NVFP4_OK;

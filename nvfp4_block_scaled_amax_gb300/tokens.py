@@ -66,10 +66,14 @@ def _empty_plan(ids: torch.Tensor, num_experts: int, align: int) -> tuple:
     dev, shape = ids.device, ids.shape
     if ids.dtype is not torch.int32:
         raise TypeError(f"expert_ids must be int32, got {ids.dtype}")
-    if num_experts < 1 or num_experts > _lib.MAX_EXPERTS or align < 1:
-        raise ValueError(f"1 to {_lib.MAX_EXPERTS} experts and align >= 1")
+    if num_experts < 1 or num_experts > _lib.MAX_EXPERTS or align < 1 or align > _lib.MAX_ALIGN:
+        raise ValueError(f"1 to {_lib.MAX_EXPERTS} experts and align 1 to {_lib.MAX_ALIGN}, got {num_experts} and {align}")
+    if not 1 <= shape[1] <= _lib.MAX_TOPK:
+        raise ValueError(f"expert_ids with 1 to {_lib.MAX_TOPK} choices a token, got {shape[1]}")
     slots = shape[0] * shape[1]
     rows = (slots + num_experts * (align - 1)) // align * align
+    if slots >= 1 << 31 or rows >= 1 << 31:
+        raise ValueError(f"choices and rows below 2^31, got {slots} and {rows}")
     plan = TokenPlan(torch.empty(num_experts + 1, dtype=torch.int32, device=dev),
                      torch.empty(shape, dtype=torch.int32, device=dev),
                      torch.empty(rows, dtype=torch.int32, device=dev))
