@@ -609,7 +609,6 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   p.a_rows = a.a_rows;
   p.a_cols = a.a_cols;
   p.b_rows = a.b_rows;
-  p.b_block_rows = a.b_block_rows;
   p.experts = a.experts;
   p.wgrad = a.wgrad;
   p.offsets = a.offsets;

@@ -17,7 +17,7 @@ struct MatmulKernelArgs {
   const float* sa;
   const float* sb;
   int64_t a_rows, a_cols, b_rows;
-  int b_block_rows, experts, wgrad;
+  int experts, wgrad;
   const int32_t* offsets;
   void* out;
   int out_bf16, out_map;
