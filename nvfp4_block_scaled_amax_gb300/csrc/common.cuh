@@ -14,7 +14,6 @@ namespace nvfp4 {
 // Bits of the per-device status word (see nvfp4_device_status).
 constexpr unsigned kStatusWaitTimeout = 1u;  // a wait for a tile copy ran out
 constexpr unsigned kStatusGridTimeout = 2u;  // a grid-wide barrier ran out
-constexpr unsigned kStatusOffsets = 4u;      // member offsets that the call does not take
 // A wait that has not completed after this many SM cycles (about 2 s at the
 // GB300 boost clock) is abandoned.
 constexpr long long kWaitLimitCycles = 4000000000LL;

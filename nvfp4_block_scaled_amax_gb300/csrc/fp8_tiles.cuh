@@ -13,6 +13,9 @@ namespace fp8 {
 
 constexpr int kBK = 128;  // elements (bytes) of a block along the contracted dimension
 
+// Beside the bits of common.cuh in the status word: member offsets that the call does not take.
+constexpr unsigned kStatusOffsets = 4u;
+
 struct MatmulKernelArgs {
   const float* sa;
   const float* sb;

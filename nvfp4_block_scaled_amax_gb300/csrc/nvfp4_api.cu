@@ -662,7 +662,7 @@ nvfp4_status nvfp4_device_status(uint32_t* status, int clear) {
   }
   *status = v;
   if (v & (kStatusWaitTimeout | kStatusGridTimeout)) return NVFP4_ERR_TIMEOUT;
-  return v ? NVFP4_ERR_SHAPE : NVFP4_OK;  // (kStatusOffsets)
+  return v ? NVFP4_ERR_SHAPE : NVFP4_OK;  // (member offsets)
 }
 
 }  // extern "C"
