@@ -20,14 +20,16 @@
 // multiplied.  Output leaves through shared memory by TMA while the next
 // tile is summed; one more warp works the tiles out ahead.
 //
-// Measured at 8192 x 5120 x 8192 (BF16 out, 128 x 128 blocks of B): 214 us,
-// 3.2 PFLOP/s; with a scale per row of B (4096 x 4864 x 16384, FP32 out) 236 us
-// against 199.  The MMAs alone take 168 us, with their operand copies 185 us
+// Measured at 8192 x 5120 x 8192 (BF16 out, 128 x 128 blocks of B): 210 us, 3.3
+// PFLOP/s, in bursts of some milliseconds; back to back for seconds 245 us, 2.8
+// PFLOP/s, for the power limit lowers the clock.  At 4096 x 4864 x 16384 (FP32
+// out) a scale per row of B takes 236 us, 128 x 128 blocks 200 (bursts, as every
+// figure below).  The MMAs alone take 168 us, with their operand copies 185 us
 // (256 x 128 MMAs: 240 us, so the tile is 256 wide although two accumulators
 // then leave no third to run ahead).  What bounds it is the hand-over: an
 // accumulator must be heard of, read, scaled and given back within the time
 // of one block's MMAs (about 520 cycles), of which the scaled sums alone take
-// 290.  The tensor pipe is 79 percent busy (60 with a scale per row of B).
+// 290.  The tensor pipe is 78 percent busy (60 with a scale per row of B).
 #include "fp8_tiles.cuh"
 
 namespace nvfp4 {
@@ -569,13 +571,14 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 
 // Which of the two kernels a product runs on.  Up to 32 rows (96 per expert)
 // the thin kernel's tiles fit and it is ahead (5120 x 4096 weights, 1 / 16 rows:
-// 6.2 / 6.1 us against 20; 1100 rows to 16 experts of 4096 x 2048: 38.3 against
-// 39.6).  Above, the estimated times decide, in us, fitted to both kernels at
-// 64 to 1024 rows, N 512 to 8192, K 512 to 8192: a start, then the blocks that
+// 6.9 / 7.1 us against 22.7 / 19.2; 1100 rows to 16 experts of 4096 x 2048: 38.1
+// against 39.0).  Above, the estimated times decide, in us, fitted to both kernels
+// at 64 to 1024 rows, N 512 to 8192, K 512 to 8192: a start, then the blocks that
 // each CTA or pair sums one after another.  For instance, thin against pair at
-// 128 rows and 128 x 128 blocks: N 1024, K 4096 8.4 / 12.0; N 5120, K 4096 16.7 /
-// 12.8; N 8192, K 512 7.8 / 5.9.  Of 128 such products the rule picks the faster
-// kernel, or one within 5 percent of it.
+// 128 rows and 128 x 128 blocks: N 1024, K 4096 8.2 / 12.1; N 5120, K 4096 17.2 /
+// 13.8; N 8192, K 512 7.5 / 5.6.  Of 128 such products (64 to 1024 rows, both
+// forms of scales) the rule picks the faster kernel every time.  (All in CUDA
+// graphs, several inputs in turn.)
 bool thin_is_faster(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   const int64_t members = a.offsets ? a.experts : 1;
   const int64_t rows = a.wgrad ? a.a_rows : (a.a_rows + members - 1) / members;

@@ -14,8 +14,10 @@
 // Bound by reading the weights: two CTAs per SM keep up to 200 KB of operand
 // slices per SM in flight.  Warps 0-3 sum, warp 4 issues the copies, warp 5
 // the MMAs (kBuffers accumulators, so the hand-overs overlap), warp 6 the
-// scales.  64 rows to 16 experts of 4096 x 2048 weights: 22.2 us, 5.7 TB/s (84
-// percent of the copy rate); one row through 5120 x 4096: 6.8 us.
+// scales.  64 rows to 16 experts of 4096 x 2048 weights: 22.6 us, 5.6 TB/s (82
+// percent of the copy rate); one row through 5120 x 4096: 6.9 us.  (Kernel times
+// here and below are of calls in a CUDA graph, on inputs that take turns and
+// are larger than L2 together where the weights are.)
 #include "fp8_tiles.cuh"
 
 namespace nvfp4 {
@@ -395,10 +397,10 @@ ThinPlan thin_plan(const Fp8MatmulArgs& a, const LaunchCtx& ctx) {
   t.tiles = members * ((rows + t.bn - 1) / t.bn) * ((a.b_rows + kWeights - 1) / kWeights);
   // Eight CTAs, four or two share a tile's blocks where all of them fit beside
   // one another (two per SM) and each keeps two blocks or more.  5120 x 4096
-  // weights, one row: 10.6 us alone, 7.3 us in fours (eights: two turns, 10.7 us);
-  // 1024 x 4096, 16 rows: 8.5, 4.7 and 4.5 us.  Two gain less, so they want more
-  // blocks: 10240 x 8192, 32 rows 19.2 us against 23.8, 12800 x 2048, 16 rows 8.5
-  // against 8.3.
+  // weights, one row: 10.5 us alone, 6.8 us in fours (eights: two turns, 10.1 us);
+  // 1024 x 4096, 16 rows: 8.4, 4.6 and 4.2 us.  Two gain less, so they want more
+  // blocks: 10240 x 8192, 32 rows 19.2 us against 22.8, 12800 x 2048, 16 rows 8.2
+  // either way.
   const int64_t k = a.wgrad ? (a.a_cols + members - 1) / members : a.a_cols;
   const int64_t kb = (k + kBK - 1) / kBK;
   t.split = 1;

@@ -7,7 +7,8 @@ computes y[t] = sum_j gates[t, j] * weights[expert_ids[t, j]] @ x[t] and its gra
 (``dispatch_tokens``), cast to E4M3 rows and columns in one pass (``quantize_fp8``), multiplied by expert
 (``matmul_fp8_grouped``) and joined (``combine_tokens``); backwards, the rows' gradient is cast the same way and gives the
 input gradient (the column-wise weights) and the weight gradient (the column-wise activations).  Nothing waits for the
-host: every size depends on the shapes alone.
+host: every size depends on the shapes alone.  As everywhere in this package autograd records nothing: the gradient is the
+function beside the call.
 """
 from __future__ import annotations
 

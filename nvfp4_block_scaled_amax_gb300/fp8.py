@@ -172,7 +172,8 @@ def matmul_fp8_grouped(a: FP8Operand, b: FP8Operand, offsets: torch.Tensor,
                        out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
     """The product by expert: rows offsets[e] .. offsets[e+1] of a [R, K] times
     b[e] transposed, b [E, N, K]; [R, N], zero past offsets[E].  offsets: device
-    int32, as ``TokenPlan.offsets`` (any alignment of the members)."""
+    int32, as ``TokenPlan.offsets`` (any alignment of the members); offsets that
+    do not ascend from 0 to at most R give the value 4 from ``device_status``."""
     (R, K), (E, N, _), dev = _check_pair(a, b, 3)
     _check_offsets(offsets, dev)
     if offsets.numel() != E + 1:
@@ -188,7 +189,8 @@ def matmul_fp8_grouped_wgrad(a: FP8Operand, b: FP8Operand, offsets: torch.Tensor
     """The experts' weight gradients: out[e] = a[:, member e] times b[:, member
     e] transposed, a [N, R] and b [K, R] the column-wise casts of the output
     gradient and the input; [E, N, K], zero for an empty member.  Every offset
-    a multiple of 128 (``dispatch_tokens`` with align=128)."""
+    a multiple of 128 (``dispatch_tokens`` with align=128), or the last one R:
+    others give a wrong result and the value 4 from ``device_status``."""
     (N, R), (K, _), dev = _check_pair(a, b, 2)
     if b.block_rows != 1:
         raise ValueError("b needs block_rows 1")
