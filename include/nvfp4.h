@@ -488,6 +488,62 @@ nvfp4_status nvfp4_fp8_matmul_grouped_wgrad(const uint8_t* a, const float* a_sca
                                             void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * 4-bit operands: the MXFP4 cast and its reading back, and the product of
+ * NVFP4 or MXFP4 operands.  These entry points have no counterpart on the
+ * pages this library follows.  The conventions above hold, except that compact
+ * scales need no alignment, amaxes that of a float, and that there is no noop
+ * flag.
+ *
+ * MXFP4: E2M1 codes as above and, for each block of 32 elements with a =
+ * max|x|, a power of two 2^(floor(log2 a) - 2), at least 2^-127, stored as one
+ * byte, its exponent + 127 (a = 0: 0):  q = E2M1_rn_satfinite(x / scale), the
+ * quotient being exact.  A block with an infinity or a NaN has the byte 255
+ * (NaN) and codes 0.  Layouts as for NVFP4 with 32 in the place of 16: scales
+ * [M][N/32] compact, or swizzled where M and N are multiples of 128.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * The MXFP4 cast of x (M x N, BF16 or FP32), row-wise and / or column-wise, in
+ * one pass.  flags: ROWWISE | COLWISE (at least one) | SWIZZLED.  N % 32 == 0;
+ * COLWISE also M % 32 == 0.
+ */
+nvfp4_status nvfp4_mxfp4_quantize(const void* x, int dtype, int64_t M, int64_t N, uint8_t* data_row,
+                                  uint8_t* scale_row, uint8_t* data_col, uint8_t* scale_col, unsigned flags,
+                                  void* stream);
+
+/*
+ * Reads one direction back: out[y][j] = E2M1(q[y][j]) * scale, exact in FP32,
+ * rounded to BF16 (which is exact too, down to its smallest number) or kept.
+ * flags: SWIZZLED or 0.  cols % 32 == 0.
+ */
+nvfp4_status nvfp4_mxfp4_dequantize(const uint8_t* data, const uint8_t* scale, int64_t rows, int64_t cols,
+                                    unsigned flags, void* out, int out_dtype, void* stream);
+
+/*
+ * One operand of a product.  amax: NULL for MXFP4; NVFP4: one float, or one for
+ * each row with ROW_SCALED.  flags: SWIZZLED | ROW_SCALED.
+ */
+typedef struct {
+  const uint8_t* data;  /* [rows][K/2]                      */
+  const uint8_t* scale; /* [rows][K/block], or swizzled     */
+  const float* amax;
+  unsigned flags;
+} nvfp4_operand;
+
+/*
+ * out[m][n] = sum_k a[m][k] b[n][k] of the values of two operands of one format,
+ * block 16 (NVFP4: E2M1 * scale * (amax / 2688)) or 32 (MXFP4).  Codes and
+ * scales are multiplied and summed by the tensor cores in FP32; the amax factors
+ * are multiplied into the sum, which is rounded once (BF16) or kept (FP32).
+ * K % 32 == 0; any M, N >= 0; K = 0 gives zero.  A swizzled operand needs its
+ * rows and K to be multiples of 128; the two operands may differ in that.
+ */
+nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, int block, int64_t M, int64_t N,
+                              int64_t K, void* out, int out_dtype, void* stream);
+
+/*
  * Per-device status word of what kernels find out: bit 0 = a wait for a tile
  * copy ran out; bit 1 = a grid-wide barrier of a single-pass call ran out;
  * bit 2 = a product by expert met member offsets that it does not take.

@@ -21,6 +21,9 @@ each block of 128, and ``matmul_fp8`` / ``matmul_fp8_grouped`` /
 ``matmul_fp8_grouped_wgrad`` multiply such operands (``fp8``); ``experts``
 runs them together.
 
+4-bit products: ``matmul_fp4`` multiplies what the casts make, ``quantize(...).row`` and ``.col`` or those of
+``quantize_mxfp4`` (MXFP4: a power of two for each block of 32); ``dequantize_fp4`` reads either back (``fp4``).
+
 Paths for "1d" / "2d" / "rht": "single_pass" (one persistent kernel: amax,
 grid barrier, cast; x read from HBM once; needs a small workspace, which
 this module keeps per device and stream) and "two_pass" (an amax kernel,
@@ -52,7 +55,7 @@ __all__ = ["NVFP4Tensor", "NVFP4Error", "empty", "compute_amax", "compute_amax_r
            "swizzle_scales", "scale_bytes", "device_status",
            "TokenPlan", "sort_tokens", "gather_tokens", "gather_tokens_grad", "dispatch_tokens", "combine_tokens",
            "combine_tokens_grad", "FP8Operand", "FP8Tensor", "quantize_fp8", "matmul_fp8", "matmul_fp8_grouped",
-           "matmul_fp8_grouped_wgrad"]
+           "matmul_fp8_grouped_wgrad", "FP4Operand", "FP4Tensor", "quantize_mxfp4", "dequantize_fp4", "matmul_fp4"]
 
 
 @dataclass
@@ -73,6 +76,18 @@ class NVFP4Tensor:
     amax_col: torch.Tensor | None = None
     swizzled: bool = False
     row_scaled: bool = False
+
+    @property
+    def row(self) -> FP4Operand | None:
+        """The row-wise cast as an operand of ``matmul_fp4``."""
+        return None if self.data_row is None else FP4Operand(self.data_row, self.scale_row, self.amax_row, 16,
+                                                             self.swizzled)
+
+    @property
+    def col(self) -> FP4Operand | None:
+        """The column-wise cast (of the tensor transposed) as an operand of ``matmul_fp4``."""
+        return None if self.data_col is None else FP4Operand(self.data_col, self.scale_col, self.amax_col, 16,
+                                                             self.swizzled)
 
     def c_struct(self) -> _lib.Output:
         p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
@@ -468,7 +483,8 @@ def device_status(clear: bool = True) -> int:
     return v.value
 
 
-# The operators of expert layers build on the helpers above.
+# The operators of expert layers and of 4-bit operands build on the helpers above.
+from .fp4 import FP4Operand, FP4Tensor, dequantize_fp4, matmul_fp4, quantize_mxfp4  # noqa: E402
 from .fp8 import (FP8Operand, FP8Tensor, matmul_fp8, matmul_fp8_grouped, matmul_fp8_grouped_wgrad,  # noqa: E402
                   quantize_fp8)
 from .tokens import (TokenPlan, combine_tokens, combine_tokens_grad, dispatch_tokens, gather_tokens,  # noqa: E402

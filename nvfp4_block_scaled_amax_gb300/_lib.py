@@ -27,7 +27,8 @@ EXPORTS = ("nvfp4_status_string", "nvfp4_scale_bytes", "nvfp4_compute_amax", "nv
            "nvfp4_dequantize", "nvfp4_swizzle_scales", "nvfp4_device_status",
            "nvfp4_token_rows", "nvfp4_sort_tokens", "nvfp4_gather_tokens", "nvfp4_dispatch_tokens",
            "nvfp4_combine_tokens", "nvfp4_combine_tokens_grad", "nvfp4_fp8_quantize", "nvfp4_fp8_matmul",
-           "nvfp4_fp8_matmul_grouped", "nvfp4_fp8_matmul_grouped_wgrad")
+           "nvfp4_fp8_matmul_grouped", "nvfp4_fp8_matmul_grouped_wgrad", "nvfp4_mxfp4_quantize",
+           "nvfp4_mxfp4_dequantize", "nvfp4_fp4_matmul")
 SINGLE_PASS_WORKSPACE_BYTES = 4096
 MAX_GROUPS = 64
 MAX_EXPERTS = 1024
@@ -39,6 +40,12 @@ class Output(ctypes.Structure):
     """nvfp4_output."""
     _fields_ = [("data_row", ctypes.c_void_p), ("scale_row", ctypes.c_void_p), ("amax_row", ctypes.c_void_p),
                 ("data_col", ctypes.c_void_p), ("scale_col", ctypes.c_void_p), ("amax_col", ctypes.c_void_p)]
+
+
+class Operand(ctypes.Structure):
+    """nvfp4_operand."""
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("amax", ctypes.c_void_p),
+                ("flags", ctypes.c_uint)]
 
 
 _lock = threading.Lock()
@@ -94,6 +101,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.nvfp4_fp8_matmul.argtypes = [vp, vp, vp, vp, c_int, i64, i64, i64, vp, c_int, vp]
         L.nvfp4_fp8_matmul_grouped.argtypes = [vp, vp, vp, vp, c_int, i64, i64, i64, c_int, vp, vp, c_int, vp]
         L.nvfp4_fp8_matmul_grouped_wgrad.argtypes = [vp, vp, vp, vp, i64, i64, i64, c_int, vp, vp, c_int, vp]
+        L.nvfp4_mxfp4_quantize.argtypes = [vp, c_int, i64, i64, vp, vp, vp, vp, uint, vp]
+        L.nvfp4_mxfp4_dequantize.argtypes = [vp, vp, i64, i64, uint, vp, c_int, vp]
+        L.nvfp4_fp4_matmul.argtypes = [ctypes.POINTER(Operand), ctypes.POINTER(Operand), c_int, i64, i64, i64, vp,
+                                       c_int, vp]
         for name in EXPORTS[1:]:
             getattr(L, name).restype = c_int
         if path is None:

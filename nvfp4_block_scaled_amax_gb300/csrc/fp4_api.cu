@@ -1,0 +1,108 @@
+// fp4_api.cu -- the C ABI of the 4-bit operators (include/nvfp4.h): host-side
+// validation before anything is enqueued, then the launches.
+#include "fp4.h"
+#include "nvfp4.h"
+
+namespace nvfp4 {
+
+nvfp4_status make_launch_ctx(void* stream, LaunchCtx* ctx);
+
+namespace {
+
+nvfp4_status status_of(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
+bool aligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+constexpr int64_t kLimit = (int64_t)1 << 31;  // rows, columns, tiles
+bool size_ok(int64_t v) { return v >= 0 && v < kLimit; }
+int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+
+nvfp4_status check_operand(const nvfp4_operand* o, int block, int64_t rows, int64_t K) {
+  if (o->flags & ~(NVFP4_SWIZZLED | NVFP4_ROW_SCALED)) return NVFP4_ERR_FLAGS;
+  if (block == 32 && (o->amax != nullptr || (o->flags & NVFP4_ROW_SCALED))) return NVFP4_ERR_FLAGS;
+  const bool swizzled = o->flags & NVFP4_SWIZZLED;
+  if (swizzled && (rows % 128 != 0 || K % 128 != 0)) return NVFP4_ERR_ALIGN;
+  if (rows > 0 && K > 0 && (o->data == nullptr || o->scale == nullptr || (block == 16 && o->amax == nullptr)))
+    return NVFP4_ERR_NULL;
+  if (!aligned(o->data, 16) || (swizzled && !aligned(o->scale, 16)) || !aligned(o->amax, 4)) return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
+}
+
+Fp4Side side(const nvfp4_operand* o, int64_t rows) {
+  return {o->data, o->scale, o->amax, rows, (o->flags & NVFP4_ROW_SCALED) != 0, (o->flags & NVFP4_SWIZZLED) != 0};
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" {
+
+nvfp4_status nvfp4_mxfp4_quantize(const void* x, int dtype, int64_t M, int64_t N, uint8_t* data_row,
+                                  uint8_t* scale_row, uint8_t* data_col, uint8_t* scale_col, unsigned flags,
+                                  void* stream) {
+  if (flags & ~(NVFP4_ROWWISE | NVFP4_COLWISE | NVFP4_SWIZZLED)) return NVFP4_ERR_FLAGS;
+  const bool row = flags & NVFP4_ROWWISE, col = flags & NVFP4_COLWISE, swizzled = flags & NVFP4_SWIZZLED;
+  if (!row && !col) return NVFP4_ERR_FLAGS;
+  if (dtype != NVFP4_BF16 && dtype != NVFP4_FP32) return NVFP4_ERR_DTYPE;
+  if (!size_ok(M) || !size_ok(N) || N % 32 != 0 || (col && M % 32 != 0)) return NVFP4_ERR_SHAPE;
+  if (swizzled && (M % 128 != 0 || N % 128 != 0)) return NVFP4_ERR_ALIGN;
+  if (M > 0 && N > 0 && (x == nullptr || (row && (data_row == nullptr || scale_row == nullptr)) ||
+                         (col && (data_col == nullptr || scale_col == nullptr))))
+    return NVFP4_ERR_NULL;
+  if (!aligned(x, 16) || (row && !aligned(data_row, 16)) || (col && !aligned(data_col, 16))) return NVFP4_ERR_ALIGN;
+  if (swizzled && ((row && !aligned(scale_row, 16)) || (col && !aligned(scale_col, 16)))) return NVFP4_ERR_ALIGN;
+  LaunchCtx ctx;
+  const nvfp4_status st = make_launch_ctx(stream, &ctx);
+  if (st != NVFP4_OK) return st;
+  MxCastArgs a = {};
+  a.M = M;
+  a.N = N;
+  a.bf16 = dtype == NVFP4_BF16;
+  a.swizzled = swizzled;
+  a.data_row = row ? data_row : nullptr;
+  a.scale_row = row ? scale_row : nullptr;
+  a.data_col = col ? data_col : nullptr;
+  a.scale_col = col ? scale_col : nullptr;
+  return status_of(launch_mxfp4_cast(x, a, ctx));
+}
+
+nvfp4_status nvfp4_mxfp4_dequantize(const uint8_t* data, const uint8_t* scale, int64_t rows, int64_t cols,
+                                    unsigned flags, void* out, int out_dtype, void* stream) {
+  if (flags & ~NVFP4_SWIZZLED) return NVFP4_ERR_FLAGS;
+  if (out_dtype != NVFP4_BF16 && out_dtype != NVFP4_FP32) return NVFP4_ERR_DTYPE;
+  if (!size_ok(rows) || !size_ok(cols) || cols % 32 != 0) return NVFP4_ERR_SHAPE;
+  if ((flags & NVFP4_SWIZZLED) && (rows % 128 != 0 || cols % 128 != 0)) return NVFP4_ERR_ALIGN;
+  if (rows > 0 && cols > 0 && (data == nullptr || scale == nullptr || out == nullptr)) return NVFP4_ERR_NULL;
+  if (!aligned(data, 16) || !aligned(out, 32)) return NVFP4_ERR_ALIGN;
+  LaunchCtx ctx;
+  const nvfp4_status st = make_launch_ctx(stream, &ctx);
+  if (st != NVFP4_OK) return st;
+  return status_of(launch_mxfp4_dequantize(data, scale, rows, cols, (flags & NVFP4_SWIZZLED) != 0, out,
+                                           out_dtype == NVFP4_BF16, ctx));
+}
+
+nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, int block, int64_t M, int64_t N,
+                              int64_t K, void* out, int out_dtype, void* stream) {
+  if (a == nullptr || b == nullptr) return NVFP4_ERR_NULL;
+  if (out_dtype != NVFP4_BF16 && out_dtype != NVFP4_FP32) return NVFP4_ERR_DTYPE;
+  if (block != 16 && block != 32) return NVFP4_ERR_SHAPE;
+  if (!size_ok(M) || !size_ok(N) || !size_ok(K) || K % 32 != 0) return NVFP4_ERR_SHAPE;
+  if (!size_ok(blocks128(M) * blocks128(N))) return NVFP4_ERR_SHAPE;  // one tile index
+  nvfp4_status st = check_operand(a, block, M, K);
+  if (st != NVFP4_OK) return st;
+  if ((st = check_operand(b, block, N, K)) != NVFP4_OK) return st;
+  if (M > 0 && N > 0 && out == nullptr) return NVFP4_ERR_NULL;
+  if (!aligned(out, 16)) return NVFP4_ERR_ALIGN;
+  LaunchCtx ctx;
+  if ((st = make_launch_ctx(stream, &ctx)) != NVFP4_OK) return st;
+  Fp4MatmulArgs m = {};
+  m.a = side(a, M);
+  m.b = side(b, N);
+  m.K = K;
+  m.block = block;
+  m.out = out;
+  m.out_bf16 = out_dtype == NVFP4_BF16;
+  return status_of(launch_fp4_matmul(m, ctx));
+}
+
+}  // extern "C"

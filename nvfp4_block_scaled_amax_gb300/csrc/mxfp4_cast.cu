@@ -1,0 +1,431 @@
+// mxfp4_cast.cu -- the MXFP4 cast, rows and transposed columns in one pass, and
+// its reading back.
+//
+// For a block of 32 elements with a = max|x|:  the scale is the power of two
+// 2^(floor(log2 a) - 2), not below 2^-127, stored as its exponent + 127 (for a = 0:
+// 0), and q = E2M1_rn_satfinite(x / scale); the quotient is exact, so a code
+// is rounded once.  With a's FP32 exponent field E the stored byte is max(E - 2,
+// 0) and the factor 1 / scale is the FP32 number with exponent field 254 - byte:
+// 2 .. 254, always a normal number.  A block with an infinity or a NaN gets the
+// byte 255 (NaN) and codes 0.  The column-wise output is the same cast of x
+// transposed.
+//
+// A 128 x 128 tile holds whole blocks of both directions, so one CTA casts it
+// from registers with one read of x: TMA brings the tile, a thread takes 8
+// rows x 8 columns, a row's maxima meet over the four lanes of its block, a
+// column's through shared memory, and the codes leave through shared memory by
+// TMA, which also cuts off what lies past the edges.  The four scales of a row
+// are one word of a 512-byte tile of the swizzled layout.  Memory-bound: 2 or
+// 4 bytes in and 17/32 of a byte per direction out for every element.
+#include "common.cuh"
+#include "dependent.h"
+#include "fp4.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 128;
+constexpr int kCodeBytes = kTile * kTile / 2;
+
+struct CastKernelArgs {
+  int64_t M, N;
+  int tiles_n;
+  int64_t tiles;
+  uint8_t* scale_row;
+  uint8_t* scale_col;
+  int swizzled;
+  unsigned* status;
+};
+
+// CTAs of an SM: by registers (4 of 64 spill with both directions), or by shared memory.
+template <bool kBf16, bool kBoth>
+constexpr int kPerSm = kBf16 ? (kBoth ? 3 : 4) : 2;
+
+template <bool kBf16>
+struct Smem {
+  static constexpr int kInBytes = kTile * kTile * (kBf16 ? 2 : 4);
+  static constexpr int kBytes = 1024 + kInBytes + 2 * kCodeBytes;
+};
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+// Per BF16 half, the larger magnitude (its sign is of no use), or NaN.
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The stored byte of a block's scale, from the bits of its maximum.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+  const uint32_t e = (amax_bits >> 23) & 255u;
+  return e == 255u ? 255u : e < 2u ? 0u : e - 2u;
+}
+// 1 / scale (of a block that is not finite: any number; its codes are masked).
+__device__ __forceinline__ float encode_of(uint32_t byte) { return __uint_as_float((254u - min(byte, 252u)) << 23); }
+
+// Four scales of line r (a row, or a column), blocks 4 t .. of C.
+__device__ __forceinline__ void put_scales(uint8_t* base, int64_t r, int t, int64_t C, bool swizzled, uint32_t word) {
+  const int64_t c = 4 * (int64_t)t;
+  if (swizzled) {  // (whole tiles)
+    *reinterpret_cast<uint32_t*>(base + swizzled_scale_offset(r, c, C)) = word;
+    return;
+  }
+  uint8_t* p = base + r * C + c;
+  const int n = (int)min((int64_t)4, C - c);
+  if (n == 4 && (reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+    *reinterpret_cast<uint32_t*>(p) = word;
+  } else {
+    for (int i = 0; i < n; ++i) p[i] = (uint8_t)(word >> (8 * i));
+  }
+}
+
+template <bool kBf16, bool kRow, bool kCol>
+__global__ void __launch_bounds__(kThreads, (kPerSm<kBf16, kRow && kCol>))
+mxfp4_cast_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap rmap,
+                  const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CastKernelArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full;
+  __shared__ __align__(16) float col_max[kThreads / 32][kTile];
+  __shared__ __align__(16) uint8_t row_sc[kTile][4], col_sc[kTile][4];
+  const uint32_t in = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t out_row = in + Smem<kBf16>::kInBytes, out_col = out_row + kCodeBytes;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int g = lane & 15;             // columns 8 g .. 8 g + 7
+  const int rg = 2 * w + (lane >> 4);  // rows 8 rg .. 8 rg + 7
+  if (tid == 0) {
+    mbar_init(&full, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&xmap);
+    if (kRow) tma_prefetch_desc(&rmap);
+    if (kCol) tma_prefetch_desc(&cmap);
+  }
+  grid_begin();
+  __syncthreads();
+  constexpr int kBox = kBf16 ? 64 : 32;  // columns of an input box (128 bytes)
+  const uint64_t policy = l2_policy_evict_first();
+  auto load = [&](int64_t t) {
+    const int32_t m = (int32_t)(t / a.tiles_n) * kTile, n = (int32_t)(t % a.tiles_n) * kTile;
+    mbar_arrive_expect_tx(&full, Smem<kBf16>::kInBytes);
+#pragma unroll
+    for (int k = 0; k < kTile / kBox; ++k)
+      tma_load_2d(smem_raw + (in - smem_u32(smem_raw)) + k * kTile * 128, &xmap, n + k * kBox, m, &full, policy);
+  };
+  if (tid == 0 && blockIdx.x < a.tiles) load(blockIdx.x);
+  uint32_t phase = 0;
+  for (int64_t t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+    const bool ok = mbar_wait_bounded(&full, phase, a.status);
+    phase ^= 1;
+    // 8 x 8 elements: BF16 in four words a row, FP32 in eight
+    constexpr int kW = kBf16 ? 4 : 8;
+    uint32_t x[8][kW];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 8 * rg + i;  // r & 7 == i
+      if constexpr (kBf16) {
+        const uint4 v = lds128(in + (g >> 3) * (kTile * 128) + r * 128 + (((g & 7) ^ i) * 16));
+        x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+      } else {
+        // the two halves in either order, so that eight lanes touch eight different 16-byte places
+        const uint32_t row = in + (g >> 2) * (kTile * 128) + r * 128;
+        const int odd = (g >> 2) & 1;
+        const uint4 p = lds128(row + (((2 * (g & 3) + odd) ^ i) * 16));
+        const uint4 q = lds128(row + (((2 * (g & 3) + 1 - odd) ^ i) * 16));
+        x[i][0] = odd ? q.x : p.x; x[i][1] = odd ? q.y : p.y; x[i][2] = odd ? q.z : p.z; x[i][3] = odd ? q.w : p.w;
+        x[i][4] = odd ? p.x : q.x; x[i][5] = odd ? p.y : q.y; x[i][6] = odd ? p.z : q.z; x[i][7] = odd ? p.w : q.w;
+      }
+    }
+    // everyone has its elements, and (below) the previous codes are stored
+    if (tid == 0) bulk_wait_read_all();
+    if (!__syncthreads_and(ok)) break;
+    if (tid == 0 && t + gridDim.x < a.tiles) load(t + gridDim.x);
+    const int tm = (int)(t / a.tiles_n), tn = (int)(t % a.tiles_n);
+    const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
+
+    // The scale bytes of the thread's rows (their block: lanes g & ~3 .. g | 3),
+    // four to a word, and the maxima of its columns over 16 rows.
+    uint32_t rs[2] = {0, 0};
+    if constexpr (kBf16) {
+      uint32_t rm[4], cm[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (kRow) m = larger(m, x[i][k]);
+          if (kCol) cm[k] = larger(cm[k], x[i][k]);
+        }
+        // the larger half of rows i and i + 1 side by side in one word
+        m = larger(m, __byte_perm(m, m, 0x1032));
+        if (i & 1) rm[i >> 1] = __byte_perm(rm[i >> 1], m, 0x5410); else rm[i >> 1] = m;
+      }
+      if constexpr (kRow) {
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) rm[k] = larger(rm[k], __shfl_xor_sync(0xFFFFFFFFu, rm[k], d));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          rs[k >> 2] |= scale_byte(k & 1 ? rm[k >> 1] & 0xFFFF0000u : rm[k >> 1] << 16) << (8 * (k & 3));
+      }
+      if constexpr (kCol) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cm[k] = larger(cm[k], __shfl_xor_sync(0xFFFFFFFFu, cm[k], 16));
+        if (lane < 16) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float4*>(&col_max[w][8 * g + 4 * k]) =
+                make_float4(bf16_lo(cm[2 * k]), bf16_hi(cm[2 * k]), bf16_lo(cm[2 * k + 1]), bf16_hi(cm[2 * k + 1]));
+        }
+      }
+    } else {
+      float rm[8], cm[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) cm[k] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        rm[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float v = __uint_as_float(x[i][k]);
+          if (kRow) rm[i] = larger(rm[i], v);
+          if (kCol) cm[k] = larger(cm[k], v);
+        }
+      }
+      if constexpr (kRow) {
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) rm[i] = larger(rm[i], __shfl_xor_sync(0xFFFFFFFFu, rm[i], d));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) rs[k >> 2] |= scale_byte(__float_as_uint(rm[k])) << (8 * (k & 3));
+      }
+      if constexpr (kCol) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) cm[k] = larger(cm[k], __shfl_xor_sync(0xFFFFFFFFu, cm[k], 16));
+        if (lane < 16) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float4*>(&col_max[w][8 * g + 4 * k]) =
+                make_float4(cm[4 * k], cm[4 * k + 1], cm[4 * k + 2], cm[4 * k + 3]);
+        }
+      }
+    }
+    if constexpr (kRow) {
+      if ((g & 3) == 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) row_sc[8 * rg + i][g >> 2] = (uint8_t)(rs[i >> 2] >> (8 * (i & 3)));
+    }
+    __syncthreads();
+    // the column scales: the maxima of two warps make a block of 32 rows
+    uint32_t cs[2] = {0, 0};
+    if constexpr (kCol) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 u = *reinterpret_cast<const float4*>(&col_max[w & ~1][8 * g + 4 * k]);
+        const float4 v = *reinterpret_cast<const float4*>(&col_max[w | 1][8 * g + 4 * k]);
+        cs[k] = scale_byte(__float_as_uint(larger(u.x, v.x))) | scale_byte(__float_as_uint(larger(u.y, v.y))) << 8 |
+                scale_byte(__float_as_uint(larger(u.z, v.z))) << 16 | scale_byte(__float_as_uint(larger(u.w, v.w))) << 24;
+      }
+      if (lane < 16 && (w & 1) == 0)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) col_sc[8 * g + k][w >> 1] = (uint8_t)(cs[k >> 2] >> (8 * (k & 3)));
+    }
+    auto value = [&](int i, int k) {  // element of row i, column k
+      if constexpr (kBf16) return k & 1 ? bf16_hi(x[i][k >> 1]) : bf16_lo(x[i][k >> 1]);
+      else return __uint_as_float(x[i][k]);
+    };
+    // Rows of 64 bytes; 16-byte places swizzled by bits 1 and 2 of the row, as TMA expects them.
+    if constexpr (kRow) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t s = (rs[i >> 2] >> (8 * (i & 3))) & 255u;
+        const float f = encode_of(s);
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(value(i, k), f);
+        const uint32_t q = e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+        sts_u32(out_row + (8 * rg + i) * 64 + (((g >> 2) ^ (i >> 1)) & 3) * 16 + (g & 3) * 4, s == 255u ? 0u : q);
+      }
+    }
+    if constexpr (kCol) {
+      uint32_t c[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t s = (cs[k >> 2] >> (8 * (k & 3))) & 255u;
+        const float f = encode_of(s);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(value(i, k), f);
+        const uint32_t q = e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+        c[k] = s == 255u ? 0u : q;
+      }
+      // Lane g stores its column k ^ (g & 7) in turn k (three rounds of swaps
+      // arrange them), so that a turn's stores fall into different banks.
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) {
+        const bool swap = g & d;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (!(k & d)) {
+            const uint32_t p = c[k], q = c[k | d];
+            c[k] = swap ? q : p;
+            c[k | d] = swap ? p : q;
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int kk = k ^ (g & 7);  // column 8 g + kk, a row of the output
+        sts_u32(out_col + (8 * g + kk) * 64 + (((rg >> 2) ^ (kk >> 1)) & 3) * 16 + (rg & 3) * 4, c[k]);
+      }
+    }
+    fence_proxy_async_shared();
+    __syncthreads();
+    if (tid == 0) {
+      if (kRow) tma_store_2d(&rmap, out_row, (int32_t)(n0 / 2), (int32_t)m0);
+      if (kCol) tma_store_2d(&cmap, out_col, (int32_t)(m0 / 2), (int32_t)n0);
+      bulk_commit();
+    }
+    if (tid < kTile) {
+      if (kRow && m0 + tid < a.M)
+        put_scales(a.scale_row, m0 + tid, tn, a.N / 32, a.swizzled, *reinterpret_cast<const uint32_t*>(row_sc[tid]));
+    } else {
+      const int c = tid - kTile;
+      if (kCol && n0 + c < a.N)
+        put_scales(a.scale_col, n0 + c, tm, a.M / 32, a.swizzled, *reinterpret_cast<const uint32_t*>(col_sc[c]));
+    }
+  }
+  if (tid == 0) bulk_wait_all();
+}
+
+template <bool kBf16, bool kRow, bool kCol>
+cudaError_t launch(const CUtensorMap& x, const CUtensorMap& r, const CUtensorMap& c, const CastKernelArgs& k,
+                   const LaunchCtx& ctx) {
+  const auto kernel = mxfp4_cast_kernel<kBf16, kRow, kCol>;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Smem<kBf16>::kBytes, allowed);
+  if (e != cudaSuccess) return e;
+  const int64_t room = (int64_t)ctx.num_sms * kPerSm<kBf16, kRow && kCol>;
+  CUtensorMap maps[3] = {x, r, c};
+  CastKernelArgs args = k;
+  void* p[] = {&maps[0], &maps[1], &maps[2], &args};
+  return launch_dependent(reinterpret_cast<const void*>(kernel), dim3((unsigned)(k.tiles < room ? k.tiles : room)),
+                          dim3(kThreads), Smem<kBf16>::kBytes, ctx.stream, p);
+}
+
+template <bool kBf16>
+cudaError_t launch_directions(const CUtensorMap& x, const CUtensorMap& r, const CUtensorMap& c, bool row, bool col,
+                              const CastKernelArgs& k, const LaunchCtx& ctx) {
+  if (row && col) return launch<kBf16, true, true>(x, r, c, k, ctx);
+  if (row) return launch<kBf16, true, false>(x, r, c, k, ctx);
+  return launch<kBf16, false, true>(x, r, c, k, ctx);
+}
+
+// The value of a scale byte: 2^(byte - 127), 255 NaN.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+}
+// Eight codes -> their values times s.
+__device__ __forceinline__ void decode8(uint32_t q, float s, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{\n .reg .b8 q0, q1, q2, q3;\n mov.b32 {q0, q1, q2, q3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, q0;\n cvt.rn.f16x2.e2m1x2 %1, q1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, q2;\n cvt.rn.f16x2.e2m1x2 %3, q3;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(q));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h[i]));
+    v[2 * i] = __fmul_rn(lo, s);
+    v[2 * i + 1] = __fmul_rn(hi, s);
+  }
+}
+
+// A thread reads half a block, 8 bytes, and writes its 16 values.
+template <bool kOutBf16>
+__global__ void __launch_bounds__(kThreads) mxfp4_dequantize_kernel(const uint8_t* __restrict__ data,
+                                                                    const uint8_t* __restrict__ scale, int64_t halves,
+                                                                    int64_t cols, int swizzled, void* out) {
+  grid_begin();
+  const int64_t per_row = cols / 16;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < halves; i += (int64_t)gridDim.x * kThreads) {
+    const uint2 q = *reinterpret_cast<const uint2*>(data + 8 * i);
+    int64_t at = i >> 1;
+    if (swizzled) {
+      const int64_t r = halves >> 32 ? i / per_row : (int64_t)((uint32_t)i / (uint32_t)per_row);
+      at = swizzled_scale_offset(r, (i - r * per_row) >> 1, per_row >> 1);
+    }
+    const float s = scale_value(scale[at]);
+    float v[16];
+    decode8(q.x, s, *reinterpret_cast<float(*)[8]>(v));
+    decode8(q.y, s, *reinterpret_cast<float(*)[8]>(v + 8));
+    if constexpr (kOutBf16) {
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[k]) : "f"(v[2 * k + 1]), "f"(v[2 * k]));
+      st_cs_v8(static_cast<uint8_t*>(out) + 32 * i, o);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(v[8 * h + k]);
+        st_cs_v8(static_cast<uint8_t*>(out) + 64 * i + 32 * h, o);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_mxfp4_cast(const void* x, const MxCastArgs& a, const LaunchCtx& ctx) {
+  if (a.M == 0 || a.N == 0) return cudaSuccess;
+  CUtensorMap xm, rm = {}, cm = {};
+  cudaError_t e = make_x_tensor_map(&xm, x, a.bf16, a.M, a.N);
+  if (e == cudaSuccess && a.data_row) e = make_fp4_tensor_map(&rm, a.data_row, a.M, a.N / 2);
+  if (e == cudaSuccess && a.data_col) e = make_fp4_tensor_map(&cm, a.data_col, a.N, a.M / 2);
+  if (e != cudaSuccess) return e;
+  CastKernelArgs k = {};
+  k.M = a.M;
+  k.N = a.N;
+  k.tiles_n = (int)((a.N + kTile - 1) / kTile);
+  k.tiles = (a.M + kTile - 1) / kTile * k.tiles_n;
+  k.scale_row = a.scale_row;
+  k.scale_col = a.scale_col;
+  k.swizzled = a.swizzled;
+  k.status = ctx.status;
+  const bool row = a.data_row != nullptr, col = a.data_col != nullptr;
+  return a.bf16 ? launch_directions<true>(xm, rm, cm, row, col, k, ctx)
+                : launch_directions<false>(xm, rm, cm, row, col, k, ctx);
+}
+
+cudaError_t launch_mxfp4_dequantize(const uint8_t* data, const uint8_t* scale, int64_t rows, int64_t cols, bool swizzled,
+                                    void* out, bool out_bf16, const LaunchCtx& ctx) {
+  int64_t halves = rows * (cols / 16);
+  if (halves == 0) return cudaSuccess;
+  const int64_t want = (halves + kThreads - 1) / kThreads, most = (int64_t)ctx.num_sms * 16;
+  const auto kernel = out_bf16 ? mxfp4_dequantize_kernel<true> : mxfp4_dequantize_kernel<false>;
+  int sw = swizzled;
+  void* args[] = {&data, &scale, &halves, &cols, &sw, &out};
+  return launch_dependent(reinterpret_cast<const void*>(kernel), dim3((unsigned)(want < most ? want : most)),
+                          dim3(kThreads), 0, ctx.stream, args);
+}
+
+}  // namespace nvfp4
