@@ -544,6 +544,33 @@ nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, in
                               int64_t K, void* out, int out_dtype, void* stream);
 
 /*
+ * A layer of gated experts for a few tokens, over 4-bit weights:
+ *   y[t] = sum_j gates[t][j] down[e] h,  h = silu(g) * u,  g = gate[e] x[t],
+ *   u = up[e] x[t],  e = expert_ids[t][j]      (silu(v) = v / (1 + exp(-v)))
+ * for x [tokens][hidden] BF16, y the same.  up: [experts][2 * inner][hidden]
+ * operands, an expert's gate rows before its up rows; down:
+ * [experts][hidden][inner]; both of one format (block 16 or 32), compact scales,
+ * rowwise amax: one float, or with ROW_SCALED one for each expert.  NVFP4
+ * scales need 2-byte alignment.  A choice outside 0..num_experts - 1 (-1, say)
+ * adds nothing; a token with none left gives zero.
+ * Sums are FP32; activations enter a product as FP16 scaled by a power of two
+ * for each row and share of the contracted dimension: x exactly down to 2^-31 of
+ * the largest value beside it, h rounded to 11 bits; y is rounded once.
+ * tokens * topk <= NVFP4_MAX_MLP_SLOTS, hidden and inner multiples of 32 up to
+ * NVFP4_MAX_MLP_WIDTH.  workspace: nvfp4_expert_mlp_workspace bytes of device
+ * memory, contents irrelevant, not shared by calls that can run at the same
+ * time.  Two launches.
+ */
+#define NVFP4_MAX_MLP_SLOTS 1024
+#define NVFP4_MAX_MLP_WIDTH 10240
+nvfp4_status nvfp4_expert_mlp_workspace(int64_t tokens, int topk, int num_experts, int64_t hidden, int64_t inner,
+                                        size_t* bytes);
+nvfp4_status nvfp4_expert_mlp(const void* x, int64_t tokens, int64_t hidden, int64_t inner, const nvfp4_operand* up,
+                              const nvfp4_operand* down, int block, const int32_t* expert_ids, const float* gates,
+                              int topk, int num_experts, void* workspace, size_t workspace_bytes, void* y,
+                              void* stream);
+
+/*
  * Per-device status word of what kernels find out: bit 0 = a wait for a tile
  * copy ran out; bit 1 = a grid-wide barrier of a single-pass call ran out;
  * bit 2 = a product by expert met member offsets that it does not take.

@@ -55,7 +55,8 @@ __all__ = ["NVFP4Tensor", "NVFP4Error", "empty", "compute_amax", "compute_amax_r
            "swizzle_scales", "scale_bytes", "device_status",
            "TokenPlan", "sort_tokens", "gather_tokens", "gather_tokens_grad", "dispatch_tokens", "combine_tokens",
            "combine_tokens_grad", "FP8Operand", "FP8Tensor", "quantize_fp8", "matmul_fp8", "matmul_fp8_grouped",
-           "matmul_fp8_grouped_wgrad", "FP4Operand", "FP4Tensor", "quantize_mxfp4", "dequantize_fp4", "matmul_fp4"]
+           "matmul_fp8_grouped_wgrad", "FP4Operand", "FP4Tensor", "quantize_mxfp4", "dequantize_fp4", "matmul_fp4",
+           "quantize_experts", "expert_mlp"]
 
 
 @dataclass
@@ -489,3 +490,4 @@ from .fp8 import (FP8Operand, FP8Tensor, matmul_fp8, matmul_fp8_grouped, matmul_
                   quantize_fp8)
 from .tokens import (TokenPlan, combine_tokens, combine_tokens_grad, dispatch_tokens, gather_tokens,  # noqa: E402
                      gather_tokens_grad, sort_tokens)
+from .experts import expert_mlp, quantize_experts  # noqa: E402

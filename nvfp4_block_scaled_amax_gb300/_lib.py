@@ -28,12 +28,14 @@ EXPORTS = ("nvfp4_status_string", "nvfp4_scale_bytes", "nvfp4_compute_amax", "nv
            "nvfp4_token_rows", "nvfp4_sort_tokens", "nvfp4_gather_tokens", "nvfp4_dispatch_tokens",
            "nvfp4_combine_tokens", "nvfp4_combine_tokens_grad", "nvfp4_fp8_quantize", "nvfp4_fp8_matmul",
            "nvfp4_fp8_matmul_grouped", "nvfp4_fp8_matmul_grouped_wgrad", "nvfp4_mxfp4_quantize",
-           "nvfp4_mxfp4_dequantize", "nvfp4_fp4_matmul")
+           "nvfp4_mxfp4_dequantize", "nvfp4_fp4_matmul", "nvfp4_expert_mlp_workspace", "nvfp4_expert_mlp")
 SINGLE_PASS_WORKSPACE_BYTES = 4096
 MAX_GROUPS = 64
 MAX_EXPERTS = 1024
 MAX_TOPK = 64
 MAX_ALIGN = 1 << 20
+MAX_MLP_SLOTS = 1024
+MAX_MLP_WIDTH = 10240
 
 
 class Output(ctypes.Structure):
@@ -105,6 +107,9 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.nvfp4_mxfp4_dequantize.argtypes = [vp, vp, i64, i64, uint, vp, c_int, vp]
         L.nvfp4_fp4_matmul.argtypes = [ctypes.POINTER(Operand), ctypes.POINTER(Operand), c_int, i64, i64, i64, vp,
                                        c_int, vp]
+        L.nvfp4_expert_mlp_workspace.argtypes = [i64, c_int, c_int, i64, i64, ctypes.POINTER(size)]
+        L.nvfp4_expert_mlp.argtypes = [vp, i64, i64, i64, ctypes.POINTER(Operand), ctypes.POINTER(Operand), c_int, vp,
+                                       vp, c_int, c_int, vp, size, vp, vp]
         for name in EXPORTS[1:]:
             getattr(L, name).restype = c_int
         if path is None:

@@ -39,6 +39,26 @@ struct Fp4MatmulArgs {
 };
 cudaError_t launch_fp4_matmul(const Fp4MatmulArgs& a, const LaunchCtx& ctx);
 
+constexpr int kMaxMlpSlots = 1024;
+constexpr int kMaxMlpWidth = 10240;  // hidden and inner sizes
+
+// The gated expert layer for a few tokens (Fp4Side: of all experts; rows and
+// swizzled unused, amax_per_row: one amax an expert).
+struct ExpertMlpArgs {
+  const void* x;   // [tokens][hidden] BF16
+  Fp4Side up;      // [experts][2 inner][hidden / 2]: gate rows, then up rows
+  Fp4Side down;    // [experts][hidden][inner / 2]
+  int block;
+  const int32_t* ids;   // [tokens][topk]
+  const float* gates;
+  int64_t tokens, hidden, inner;
+  int topk, experts;
+  void* workspace;
+  void* y;         // [tokens][hidden] BF16
+};
+size_t expert_mlp_workspace(const ExpertMlpArgs& a);
+cudaError_t launch_expert_mlp(const ExpertMlpArgs& a, const LaunchCtx& ctx);
+
 // Tensor map of a row-major byte matrix, box 128 bytes x `box_rows` rows,
 // 128-byte swizzle, zero fill outside (fp8.h).
 cudaError_t make_fp8_tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int box_rows);

@@ -26,6 +26,25 @@ nvfp4_status check_operand(const nvfp4_operand* o, int block, int64_t rows, int6
   return NVFP4_OK;
 }
 
+static_assert(NVFP4_MAX_MLP_SLOTS == kMaxMlpSlots && NVFP4_MAX_MLP_WIDTH == kMaxMlpWidth, "limits of the header");
+
+nvfp4_status check_mlp(int64_t tokens, int topk, int experts, int64_t hidden, int64_t inner) {
+  if (tokens < 0 || tokens > kMaxMlpSlots || topk < 1 || topk > NVFP4_MAX_TOPK || tokens * topk > kMaxMlpSlots)
+    return NVFP4_ERR_SHAPE;
+  if (experts < 1 || experts > NVFP4_MAX_EXPERTS) return NVFP4_ERR_SHAPE;
+  for (int64_t v : {hidden, inner})
+    if (v < 0 || v > kMaxMlpWidth || v % 32 != 0) return NVFP4_ERR_SHAPE;
+  return NVFP4_OK;
+}
+
+// A stack of weight matrices.
+nvfp4_status check_experts(const nvfp4_operand* o, int block, bool any) {
+  if (o->flags & NVFP4_SWIZZLED) return NVFP4_ERR_FLAGS;
+  const nvfp4_status st = check_operand(o, block, any, any);
+  if (st != NVFP4_OK) return st;
+  return aligned(o->scale, block == 16 ? 2 : 1) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
+
 Fp4Side side(const nvfp4_operand* o, int64_t rows) {
   return {o->data, o->scale, o->amax, rows, (o->flags & NVFP4_ROW_SCALED) != 0, (o->flags & NVFP4_SWIZZLED) != 0};
 }
@@ -103,6 +122,55 @@ nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, in
   m.out = out;
   m.out_bf16 = out_dtype == NVFP4_BF16;
   return status_of(launch_fp4_matmul(m, ctx));
+}
+
+nvfp4_status nvfp4_expert_mlp_workspace(int64_t tokens, int topk, int num_experts, int64_t hidden, int64_t inner,
+                                        size_t* bytes) {
+  if (bytes == nullptr) return NVFP4_ERR_NULL;
+  const nvfp4_status st = check_mlp(tokens, topk, num_experts, hidden, inner);
+  if (st != NVFP4_OK) return st;
+  ExpertMlpArgs a = {};
+  a.tokens = tokens;
+  a.topk = topk;
+  a.hidden = hidden;
+  a.inner = inner;
+  *bytes = expert_mlp_workspace(a);
+  return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_expert_mlp(const void* x, int64_t tokens, int64_t hidden, int64_t inner, const nvfp4_operand* up,
+                              const nvfp4_operand* down, int block, const int32_t* expert_ids, const float* gates,
+                              int topk, int num_experts, void* workspace, size_t workspace_bytes, void* y,
+                              void* stream) {
+  if (up == nullptr || down == nullptr) return NVFP4_ERR_NULL;
+  if (block != 16 && block != 32) return NVFP4_ERR_SHAPE;
+  nvfp4_status st = check_mlp(tokens, topk, num_experts, hidden, inner);
+  if (st != NVFP4_OK) return st;
+  const bool any = tokens > 0 && hidden > 0 && inner > 0;
+  if ((st = check_experts(up, block, any)) != NVFP4_OK) return st;
+  if ((st = check_experts(down, block, any)) != NVFP4_OK) return st;
+  if (tokens > 0 && hidden > 0 && y == nullptr) return NVFP4_ERR_NULL;
+  if (any && (x == nullptr || expert_ids == nullptr || gates == nullptr || workspace == nullptr)) return NVFP4_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(workspace, 16) || !aligned(expert_ids, 4) || !aligned(gates, 4))
+    return NVFP4_ERR_ALIGN;
+  ExpertMlpArgs a = {};
+  a.x = x;
+  a.up = side(up, 0);
+  a.down = side(down, 0);
+  a.block = block;
+  a.ids = expert_ids;
+  a.gates = gates;
+  a.tokens = tokens;
+  a.hidden = hidden;
+  a.inner = inner;
+  a.topk = topk;
+  a.experts = num_experts;
+  a.workspace = workspace;
+  a.y = y;
+  if (any && workspace_bytes < expert_mlp_workspace(a)) return NVFP4_ERR_SHAPE;
+  LaunchCtx ctx;
+  if ((st = make_launch_ctx(stream, &ctx)) != NVFP4_OK) return st;
+  return status_of(launch_expert_mlp(a, ctx));
 }
 
 }  // extern "C"

@@ -9,13 +9,22 @@ computes y[t] = sum_j gates[t, j] * weights[expert_ids[t, j]] @ x[t] and its gra
 input gradient (the column-wise weights) and the weight gradient (the column-wise activations).  Nothing waits for the
 host: every size depends on the shapes alone.  As everywhere in this package autograd records nothing: the gradient is the
 function beside the call.
+
+For decoding, a whole layer of gated experts over 4-bit weights:
+
+    up, down = quantize_experts(gate_up), quantize_experts(down)      # [E, 2 F, H], [E, H, F], once
+    y = expert_mlp(x, up, down, expert_ids, gates)                    # two launches
 """
 from __future__ import annotations
 
+import ctypes
 from dataclasses import dataclass
 
 import torch
 
+from . import FP4Operand, _lib, quantize_grouped, quantize_mxfp4
+from ._call import call
+from .fp4 import _check_operand, _struct
 from .fp8 import BLOCK, FP8Tensor, matmul_fp8_grouped, matmul_fp8_grouped_wgrad, quantize_fp8
 from .tokens import TokenPlan, combine_tokens, combine_tokens_grad, dispatch_tokens, gather_tokens_grad
 
@@ -55,3 +64,74 @@ def expert_layer_grad(dy: torch.Tensor, saved: ExpertSaved) -> tuple[torch.Tenso
     drows = matmul_fp8_grouped(q.row, saved.weights.col, plan.offsets, out_dtype=dy.dtype)
     dweights = matmul_fp8_grouped_wgrad(q.col, saved.rows.col, plan.offsets)
     return gather_tokens_grad(drows, plan), dweights, dgates
+
+
+def quantize_experts(weights: torch.Tensor, block: int = 16) -> FP4Operand:
+    """Casts a stack of weight matrices [E, N, K] (bfloat16 or float32) to 4 bits along K for ``expert_mlp``: NVFP4 with
+    an amax for each matrix (block 16, N % 8 == 0) or MXFP4 (block 32).  K % 32 == 0.  For weights, ahead of use: it
+    makes several calls."""
+    if weights.dim() != 3:
+        raise ValueError("weights must be [E, N, K]")
+    E, N, K = weights.shape
+    if K % 32:
+        raise ValueError("the contracted dimension must be a multiple of 32")
+    if not weights.is_contiguous():
+        raise ValueError("tensors passed to libnvfp4 must be contiguous CUDA tensors")
+    if block == 32:
+        q = quantize_mxfp4(weights.view(E * N, K)).row
+        return FP4Operand(q.data.view(E, N, K // 2), q.scale.view(E, N, K // 32), None, 32)
+    if block != 16:
+        raise ValueError(f"block 16 (NVFP4) or 32 (MXFP4), got {block}")
+    if N % 8:
+        raise ValueError("NVFP4 experts need a multiple of 8 rows")
+    dev = weights.device
+    data = torch.empty((E, N, K // 2), dtype=torch.uint8, device=dev)
+    scale = torch.empty((E, N, K // 16), dtype=torch.uint8, device=dev)
+    amax = torch.zeros((E, 4), dtype=torch.float32, device=dev)  # (each at a 16-byte boundary, as the cast writes them)
+    from . import NVFP4Tensor
+    for e0 in range(0, E, _lib.MAX_GROUPS):
+        members = range(e0, min(E, e0 + _lib.MAX_GROUPS))
+        outs = [NVFP4Tensor(N, K, data[e], scale[e].view(-1), amax[e, :1]) for e in members]
+        quantize_grouped(weights[e0:members.stop].view(-1, K), [N] * len(members), "1d", colwise=False, out=outs)
+    return FP4Operand(data, scale, amax[:, 0].contiguous(), 16)
+
+
+def expert_mlp(x: torch.Tensor, up: FP4Operand, down: FP4Operand, expert_ids: torch.Tensor, gates: torch.Tensor,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """y[t] = sum_j gates[t, j] * down[e] @ (silu(gate[e] @ x[t]) * (up[e] @ x[t])), e = expert_ids[t, j], for a few
+    tokens: x [T, H] bfloat16, expert_ids int32 and gates float32 [T, topk], up [E, 2 F, H] (an expert's gate rows, then
+    its up rows) and down [E, H, F] 4-bit operands of one format with compact scales (``quantize_experts``).  Ids outside
+    0 .. E - 1 are dropped.  T * topk <= 1024; H and F multiples of 32, at most 10240.  More tokens than a few dozen per
+    expert are faster through ``expert_layer``'s operators."""
+    E, F2, H = _check_operand("up", up, 3)
+    Ed, Hd, F = _check_operand("down", down, 3)
+    dev = x.device
+    if x.dtype is not torch.bfloat16 or gates.dtype is not torch.float32 or expert_ids.dtype is not torch.int32:
+        raise TypeError(f"bfloat16 x, float32 gates and int32 expert_ids, got {x.dtype}, {gates.dtype} and "
+                        f"{expert_ids.dtype}")
+    if x.dim() != 2 or expert_ids.dim() != 2 or gates.shape != expert_ids.shape or expert_ids.shape[0] != x.shape[0]:
+        raise ValueError("x [T, H], expert_ids and gates [T, topk]")
+    T, topk = expert_ids.shape
+    if Ed != E or Hd != H or F2 != 2 * F or x.shape[1] != H or up.block != down.block:
+        raise ValueError(f"up [E, 2 F, H] and down [E, H, F] of one format for x [T, H], got {(E, F2, H)} (block "
+                         f"{up.block}), {(Ed, Hd, F)} (block {down.block}) and {tuple(x.shape)}")
+    if up.swizzled or down.swizzled:
+        raise ValueError("expert_mlp takes compact scales")
+    if not 1 <= T * topk <= _lib.MAX_MLP_SLOTS and T:
+        raise ValueError(f"expert_mlp takes up to {_lib.MAX_MLP_SLOTS} choices, got {T} x {topk}")
+    if max(H, F) > _lib.MAX_MLP_WIDTH:
+        raise ValueError(f"expert_mlp takes sizes up to {_lib.MAX_MLP_WIDTH}")
+    for v in (x, expert_ids, gates):
+        if not (v.is_cuda and v.is_contiguous()) or v.device != dev:
+            raise ValueError("tensors passed to libnvfp4 must be contiguous CUDA tensors, on one device")
+    if up.data.device != dev or down.data.device != dev:
+        raise ValueError("weights and x on one device")
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous bfloat16 {tuple(x.shape)} tensor on {dev}")
+    need = 4 * (T * topk * (H + F) + H // 16)
+    work = torch.empty(need, dtype=torch.uint8, device=dev)
+    call("nvfp4_expert_mlp", dev, x.data_ptr(), T, H, F, ctypes.byref(_struct(up, E)), ctypes.byref(_struct(down, E)),
+         up.block, expert_ids.data_ptr(), gates.data_ptr(), topk, E, work.data_ptr(), need, out.data_ptr())
+    return out
