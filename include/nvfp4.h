@@ -559,7 +559,7 @@ nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, in
  * tokens * topk <= NVFP4_MAX_MLP_SLOTS, hidden and inner multiples of 32 up to
  * NVFP4_MAX_MLP_WIDTH.  workspace: nvfp4_expert_mlp_workspace bytes of device
  * memory, contents irrelevant, not shared by calls that can run at the same
- * time.  Two launches.
+ * time.  Three launches.
  */
 #define NVFP4_MAX_MLP_SLOTS 1024
 #define NVFP4_MAX_MLP_WIDTH 10240

@@ -13,7 +13,7 @@ function beside the call.
 For decoding, a whole layer of gated experts over 4-bit weights:
 
     up, down = quantize_experts(gate_up), quantize_experts(down)      # [E, 2 F, H], [E, H, F], once
-    y = expert_mlp(x, up, down, expert_ids, gates)                    # two launches
+    y = expert_mlp(x, up, down, expert_ids, gates)                    # three launches
 """
 from __future__ import annotations
 
@@ -130,7 +130,7 @@ def expert_mlp(x: torch.Tensor, up: FP4Operand, down: FP4Operand, expert_ids: to
         out = torch.empty_like(x)
     elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bfloat16 {tuple(x.shape)} tensor on {dev}")
-    need = 4 * (T * topk * (H + F) + H // 16)
+    need = 4 * T * topk * (H + F)
     work = torch.empty(need, dtype=torch.uint8, device=dev)
     call("nvfp4_expert_mlp", dev, x.data_ptr(), T, H, F, ctypes.byref(_struct(up, E)), ctypes.byref(_struct(down, E)),
          up.block, expert_ids.data_ptr(), gates.data_ptr(), topk, E, work.data_ptr(), need, out.data_ptr())
