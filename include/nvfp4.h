@@ -553,18 +553,19 @@ nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, in
  * rowwise amax: one float, or with ROW_SCALED one for each expert.  NVFP4
  * scales need 2-byte alignment.  A choice outside 0..num_experts - 1 (-1, say)
  * adds nothing; a token with none left gives zero.
- * Sums are FP32; activations enter a product as FP16 scaled by a power of two
- * for each row and share of the contracted dimension: x exactly down to 2^-31 of
- * the largest value beside it, h rounded to 11 bits; y is rounded once.
+ * Sums are FP32; x and h enter a product as sums of eight 4-bit operands, which
+ * leave at most 2^-19 (NVFP4) or 2^-16 (MXFP4) of the largest value of each block,
+ * or of an NVFP4 row's h 2^-31 of (amax sum|x|)^2; y is rounded once.  A token with
+ * an infinity or a NaN, in x or in h, gives NaN.
  * tokens * topk <= NVFP4_MAX_MLP_SLOTS, hidden and inner multiples of 32 up to
  * NVFP4_MAX_MLP_WIDTH.  workspace: nvfp4_expert_mlp_workspace bytes of device
- * memory, contents irrelevant, not shared by calls that can run at the same
- * time.  Three launches.
+ * memory, 128-byte aligned, contents irrelevant, not shared by calls that can run
+ * at the same time.  Four launches.
  */
 #define NVFP4_MAX_MLP_SLOTS 1024
 #define NVFP4_MAX_MLP_WIDTH 10240
 nvfp4_status nvfp4_expert_mlp_workspace(int64_t tokens, int topk, int num_experts, int64_t hidden, int64_t inner,
-                                        size_t* bytes);
+                                        int block, size_t* bytes);
 nvfp4_status nvfp4_expert_mlp(const void* x, int64_t tokens, int64_t hidden, int64_t inner, const nvfp4_operand* up,
                               const nvfp4_operand* down, int block, const int32_t* expert_ids, const float* gates,
                               int topk, int num_experts, void* workspace, size_t workspace_bytes, void* y,

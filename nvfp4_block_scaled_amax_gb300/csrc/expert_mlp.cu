@@ -1,507 +1,627 @@
 // expert_mlp.cu -- a layer of gated experts over 4-bit weights for a few
 // tokens:
-//     y[t] = sum_j gates[t][j] Wd[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])),   e = ids[t][j],
-// in two kernels of one body and a third that adds: the first gives the hidden values of every slot
-// (t, j), the second multiplies them by Wd and adds a token's slots.
+//     y[t] = sum_j gates[t][j] Wd[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])),   e = ids[t][j].
 //
-// With a few rows an expert the time is that of reading its weights once, so
-// the weights stay 4 bits until they are in registers: each lane streams 16
-// bytes (32 weights) of two weight rows at a time, four such loads ahead, and
-// makes FP16 operands of them for mma.sync (16 weight rows x 8 tokens x 16):
-// an E2M1 code times an E4M3 scale has six significant bits, so the NVFP4
-// product is exact in FP16; MXFP4 codes are multiplied as they are, and the sum
-// over a block is scaled in FP32, since powers of two may leave FP16's range.
-// (tcgen05 has no product of 4-bit weights and 16-bit activations; the tensor
-// cores are not what bounds this.)
+// With a few rows an expert the time is that of reading its weights once, and
+// unpacking them to multiply in 16 bits costs more instructions than the SMs can
+// issue meanwhile (about two a weight; measured at the largest listed sizes 135
+// us where reading takes 51).  So the tensor cores take the weights as they are
+// (tcgen05 block_scale), and the activations become 4 bits too: as the sum of
+// kTerms 4-bit operands, each the cast of what the earlier ones left over.
 //
-// Activations are held in shared memory as FP16 scaled by a power of two for
-// each row and each warp's share of the contracted dimension, so that their
-// largest is in [2^14, 2^15): BF16 activations keep every bit down to 2^-31 of
-// the largest, hidden values (FP32 between the kernels) are rounded to 11 bits,
-// eight times finer than BF16's 8.  Sums, SiLU and the sum over slots are FP32.
+// Terms.  A term of a block (16 or 32 elements, as the weights') is its
+// E2M1 codes with a scale at which the block's largest remainder is at most 6
+// (NVFP4: the next E4M3 number above a sixth of it) or below 8 (MXFP4: a power
+// of two); a code is off by at most 1, or 2 above 6, so the remainder falls to
+// 3/16 (NVFP4) or 1/4 (MXFP4), and eight terms leave 2^-19 or 2^-16 of the
+// block's largest element, far below the 2^-9 of the BF16 output.  The
+// subtraction is exact in FP32.  Each term is a row of the product beside the
+// others: N = 8 tokens, where few rows leave an MMA's columns empty anyway.
+// E4M3 scales span 17 powers of two; they count in units of their row and term
+// (4^-i for term i), so that a row's small blocks lose nothing until 2^-29 of its
+// largest.  The unit of a row of x comes from its largest element; that of
+// the hidden row, which is cut into terms tile by tile, from a bound:
+// |g|, |u| <= amax sum|x|.  (The sums' own rounding in FP32 is of that order.)
 //
-// A CTA of 12 warps serves an even share of the items, an item being 32 weight
-// rows of one expert for up to 8 kNT of its rows ("segment": an expert and
-// such a group of rows).  ks warps share an item's contracted dimension and
-// join their sums through shared memory in the order of the warps.  The second
-// kernel writes each slot's weighted result, and a last one adds the tokens'
-// slots in order, so that nothing depends on timing.
-#include "common.cuh"
-#include "dependent.h"
-#include "fp4.h"
+// Four launches: slots sorted by expert and x into terms; gate and up products
+// with SiLU and the hidden rows' terms; down product, weighted by the gates;
+// the slots of a token added in order.  The products are fp4_matmul_thin.cu's:
+// 128 weight rows on the tensor-memory lanes (64 gate and 64 up rows) by kTok
+// tokens' terms, the contracted dimension of a tile split over a cluster where
+// there are few tiles; partial results travel with their terms already added.
+#include "fp4_tiles.cuh"
 #include "tokens.h"
 
 namespace nvfp4 {
+namespace fp4 {
 namespace {
 
-constexpr int kWarps = 12, kThreads = 32 * kWarps;
-constexpr int kChunk = 128;   // weights of a row that four lanes take at a time
-constexpr int kItemRows = 32;  // weight rows of an item: two MMA tiles (first kernel: 16 gate rows and their up rows)
-constexpr int kRedPitch = 36;  // floats of 32 rows in the joining buffer: the four lanes of a row meet other banks
+constexpr int kTerms = 8;
 
-struct KernelArgs {
-  const uint16_t* x;      // first kernel: [tokens][width], BF16
-  float* hidden;          // [slots][inner]: out of the first kernel, into the second
+// What the launches hand to each other, in the workspace.
+struct Rows {
+  uint8_t* codes;   // [slots * kTerms][width / 2]: sorted slot, term
+  uint8_t* scales;  // [segments][scale tiles of the width][512]: rows of a segment as in Format's tiles
+  float* unit;      // [slots] NVFP4: what a scale of 1 stands for in term 0
+};
+struct Plan {
+  int32_t* segments;     // how many
+  int4* table;           // [segments] expert, first sorted slot, slots
+  int32_t* slot_of_row;  // [slots] slot of a sorted one
+};
+
+// ---------------------------------------------------------------------------
+// Terms
+// ---------------------------------------------------------------------------
+// Four elements of a block into terms: v is left with the remainders.  The
+// block lies in 4 (NVFP4) or 8 (MXFP4) neighbouring lanes.  codes[i]: four codes
+// of term i; scales: byte i the scale of term i.
+template <int kBlock>
+__device__ __forceinline__ void to_terms(float (&v)[4], float unit, uint32_t (&codes)[kTerms], uint32_t (&scales)[2]) {
+  scales[0] = scales[1] = 0;
+  float inv_unit6 = __fdiv_rn(1.0f / 6.0f, unit);
+#pragma unroll
+  for (int i = 0; i < kTerms; ++i) {
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = fabsf(v[j]);
+      m = a >= m ? a : a != a ? __int_as_float(0x7F800000) : m;  // (a NaN counts as an infinity)
+    }
+#pragma unroll
+    for (int d = 1; d < kBlock / 4; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    uint32_t byte;
+    float value, inv;  // the scale, and its reciprocal (any rounding: what it leaves goes to the next term)
+    if constexpr (kBlock == 16) {
+      const float q = __fmul_rn(m, inv_unit6);
+      byte = e4m3_rn_satfinite(q);
+      if (byte < 126u && e4m3_decode(byte) < q) ++byte;
+      value = __fmul_rn(e4m3_decode(byte), unit);
+      inv = byte == 0 ? 0.0f : __fdividef(1.0f, value);
+      unit = __fmul_rn(unit, 0.25f);
+      inv_unit6 = __fmul_rn(inv_unit6, 4.0f);
+      if (!(q <= 449.0f)) byte = 127u;  // not finite: the whole row becomes NaN
+    } else {
+      const uint32_t e = __float_as_uint(m) >> 23;
+      byte = e < 2u ? 0u : e - 2u;
+      value = __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+      inv = __uint_as_float((254u - byte) << 23);
+      if (!(m <= kFltMax)) byte = 255u;
+    }
+    if (!(m <= kFltMax)) inv = 0.0f;
+    uint16_t h;
+    asm("{\n .reg .b8 lo, hi;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 hi, %4, %3;\n"
+        " mov.b16 %0, {lo, hi};\n}"
+        : "=h"(h)
+        : "f"(__fmul_rn(v[0], inv)), "f"(__fmul_rn(v[1], inv)), "f"(__fmul_rn(v[2], inv)), "f"(__fmul_rn(v[3], inv)));
+    if (inv == 0.0f) h = 0;  // (an infinity times 0)
+    codes[i] = h;
+    scales[i >> 2] |= byte << (8 * (i & 3));
+    uint32_t f01, f23;
+    asm("{\n .reg .b8 lo, hi;\n mov.b16 {lo, hi}, %2;\n cvt.rn.f16x2.e2m1x2 %0, lo;\n cvt.rn.f16x2.e2m1x2 %1, hi;\n}"
+        : "=r"(f01), "=r"(f23)
+        : "h"(h));
+    float c[4];
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}"
+        : "=f"(c[0]), "=f"(c[1])
+        : "r"(f01));
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}"
+        : "=f"(c[2]), "=f"(c[3])
+        : "r"(f23));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __fmaf_rn(-c[j], value, v[j]);
+  }
+}
+
+// Their places: four codes of each term in rows of `pitch` bytes, and the
+// lane's share of the block's scales (row n0 + i of a segment is term i).
+template <int kBlock>
+__device__ __forceinline__ void store_codes(uint8_t* row, int64_t pitch, int64_t element, const uint32_t (&codes)[kTerms]) {
+#pragma unroll
+  for (int i = 0; i < kTerms; ++i)
+    *reinterpret_cast<uint16_t*>(row + i * pitch + element / 2) = (uint16_t)codes[i];
+}
+template <int kBlock>
+__device__ __forceinline__ void store_scales(uint8_t* segment, int n0, int64_t element, int lane,
+                                             const uint32_t (&scales)[2]) {
+  constexpr int kLanes = kBlock / 4, kEach = kTerms / kLanes;
+  uint8_t* tile = segment + element / (4 * kBlock) * kScaleTile + element % (4 * kBlock) / kBlock;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int term = (lane % kLanes) * kEach + i, n = n0 + term;
+    tile[n % 32 * 16 + n / 32 * 4] = (uint8_t)(scales[term >> 2] >> (8 * (term & 3)));
+  }
+}
+// Power of two at which scales up to 448 reach a sixth of `largest`.
+__device__ __forceinline__ float unit_of(float largest) {
+  const int e = (int)(__float_as_uint(largest) >> 23) - 127;  // floor(log2)
+  return __uint_as_float((uint32_t)(max(-100, e - 10) + 127) << 23);
+}
+
+// ---------------------------------------------------------------------------
+// Slots by expert, and x into terms
+// ---------------------------------------------------------------------------
+constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32;
+constexpr int kPrepPart = 128 * kPrepWarps;  // elements of a CTA
+
+struct PrepArgs {
+  const uint16_t* x;
   const int32_t* ids;
-  const float* gates;
-  const uint8_t* data;    // [experts][rows][width / 2]
-  const uint8_t* scale;
-  const float* amax;
+  const float* amax;  // of the gate and up weights; NULL: MXFP4
   int amax_per_expert;
-  int slots, topk, experts;
-  int width;              // contracted dimension
-  int rows;               // weight rows of an expert
-  int ks;                 // warps that share an item
-  float* parts;           // second kernel: [slots][rows], weighted
+  int slots, topk, experts, width, tok;
+  Rows x_rows;
+  float* h_unit;
+  Plan plan;
 };
 
-__device__ __forceinline__ uint4 load_weights(const uint8_t* p, bool there) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (there)
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-  return v;
-}
-// Eight E2M1 codes -> four pairs in FP16.
-__device__ __forceinline__ void to_f16(uint32_t q, uint32_t (&h)[4]) {
-  asm("{\n .reg .b8 q0, q1, q2, q3;\n mov.b32 {q0, q1, q2, q3}, %4;\n"
-      " cvt.rn.f16x2.e2m1x2 %0, q0;\n cvt.rn.f16x2.e2m1x2 %1, q1;\n"
-      " cvt.rn.f16x2.e2m1x2 %2, q2;\n cvt.rn.f16x2.e2m1x2 %3, q3;\n}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(q));
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ float power_of_two(uint32_t byte) {  // 2^(byte - 127), 255: NaN
-  return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
-}
-// Four words of four neighbouring lanes transposed: lane t's word i becomes word t of lane i.
-__device__ __forceinline__ void transpose4(uint4& v, int t) {
-  uint32_t a = t & 1 ? v.x : v.y, b = t & 1 ? v.z : v.w;  // to the neighbour
-  a = __shfl_xor_sync(0xFFFFFFFFu, a, 1);
-  b = __shfl_xor_sync(0xFFFFFFFFu, b, 1);
-  if (t & 1) v.x = a, v.z = b; else v.y = a, v.w = b;
-  a = t & 2 ? v.x : v.z, b = t & 2 ? v.y : v.w;
-  a = __shfl_xor_sync(0xFFFFFFFFu, a, 2);
-  b = __shfl_xor_sync(0xFFFFFFFFu, b, 2);
-  if (t & 2) v.x = a, v.y = b; else v.z = a, v.w = b;
-}
-
-template <int kN>
-struct Count {
-  static constexpr int value = kN;
-};
-
-// Shared memory: activations [chunk][row][256 bytes], the joining buffer, and
-// the slots sorted by expert.
-template <int kNT>
-struct Layout {
-  static constexpr int kRows = 8 * kNT;  // rows of a segment
-  static constexpr int kRedFloats = kRows * kRedPitch;  // of a warp
-  static constexpr __host__ __device__ int chunks(int width) { return (width + kChunk - 1) / kChunk; }
-  static constexpr __host__ __device__ int x_bytes(int width) { return chunks(width) * kRows * 2 * kChunk; }
-  static constexpr int kRedBytes = kWarps * kRedFloats * 4;
-  static constexpr int kScaleBytes = kWarps * kRows * 4;
-  static constexpr __host__ __device__ int list_bytes(int slots, int experts) {
-    return 4 * (2 * (experts + 1) + experts) + 4 * slots + 2 * ((slots + 1) & ~1) * 2;
-  }
-  static constexpr int bytes(int width, int slots, int experts) {
-    return 256 + x_bytes(width) + kRedBytes + kScaleBytes + list_bytes(slots, experts);
-  }
-};
-
-template <bool kDown, int kBlock, int kNT>
-__global__ void __launch_bounds__(kThreads, 1) expert_mlp_kernel(const __grid_constant__ KernelArgs p) {
-  using L = Layout<kNT>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((256u - (smem_u32(smem_raw) & 255u)) & 255u);
-  const int C = L::chunks(p.width);
-  float* red = reinterpret_cast<float*>(smem + L::x_bytes(p.width));
-  float* xinv = red + L::kRedBytes / 4;                 // [ks][rows of the segment]
-  int* row0 = reinterpret_cast<int*>(xinv + kWarps * L::kRows);  // [experts + 1] first sorted slot
-  int* seg0 = row0 + p.experts + 1;                     // [experts + 1] first segment
-  int* count = seg0 + p.experts + 1;                    // [experts]
-  int* ids = count + p.experts;                         // [slots]
-  uint16_t* sorted = reinterpret_cast<uint16_t*>(ids + p.slots);  // [slots]
-  uint16_t* place = sorted + ((p.slots + 1) & ~1);      // [slots] place within the expert
-  const int tid = threadIdx.x, w = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t xs = smem_u32(smem);
-
-  // The second kernel starts when all CTAs of the first are past this point, and
-  // those are past everything before the first: what neither kernel writes may
-  // be read ahead of its own wait.
-  if (!kDown) {
-    grid_dependency_wait();
-    grid_launch_dependents();
-  }
-
-  // Slots by expert, in ascending order.
-  for (int s = tid; s < p.slots; s += kThreads) {
+template <int kBlock>
+__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_constant__ PrepArgs p) {
+  extern __shared__ int lists[];
+  int* ids = lists;                      // [slots]
+  int* row0 = ids + p.slots;             // [experts] first sorted slot
+  int* seg0 = row0 + p.experts;          // [experts] first segment
+  int* count = seg0 + p.experts;         // [experts]
+  __shared__ float largest[kPrepWarps], sums[kPrepWarps];
+  __shared__ int place[kMaxTopk];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int parts = (p.width + kPrepPart - 1) / kPrepPart;
+  const int token = blockIdx.x / parts, part = blockIdx.x % parts;
+  grid_begin();
+  for (int s = tid; s < p.slots; s += kPrepThreads) {
     const int e = p.ids[s];
     ids[s] = e >= 0 && e < p.experts ? e : -1;
   }
-  for (int e = tid; e < p.experts; e += kThreads) count[e] = 0;
+  for (int e = tid; e < p.experts; e += kPrepThreads) count[e] = 0;
+  // The row's largest finite element and the sum of magnitudes.
+  const uint16_t* row = p.x + (int64_t)token * p.width;
+  float m = 0.0f, sum = 0.0f;
+#pragma unroll 2
+  for (int k = 8 * tid; k < p.width; k += 8 * kPrepThreads) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + k));
+    const float v[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
+                        bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(v[i]);
+      if (a <= kFltMax) {
+        m = fmaxf(m, a);
+        sum = __fadd_rn(sum, a);
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, d));
+  }
+  if (lane == 0) largest[w] = m, sums[w] = sum;
+  __syncthreads();
+  m = largest[0], sum = sums[0];
+#pragma unroll
+  for (int i = 1; i < kPrepWarps; ++i) m = fmaxf(m, largest[i]), sum = __fadd_rn(sum, sums[i]);
+  for (int s = tid; s < p.slots; s += kPrepThreads)
+    if (ids[s] >= 0) atomicAdd(&count[ids[s]], 1);
   __syncthreads();
   if (w == 0) {
-    for (int base = 0; base < p.slots; base += 32) {
-      const int s = base + lane, e = s < p.slots ? ids[s] : -1;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-      const int before = __popc(same & ((1u << lane) - 1));
-      const int at = e >= 0 ? count[e] : 0;
-      __syncwarp();
-      if (e >= 0) {
-        place[s] = (uint16_t)(at + before);
-        if (before == 0) count[e] = at + __popc(same);
-      }
-      __syncwarp();
-    }
     int rows = 0, segs = 0;
     for (int base = 0; base < p.experts; base += 32) {
-      const int e = base + lane, n = e < p.experts ? count[e] : 0, m = (n + L::kRows - 1) / L::kRows;
-      int rn = n, rm = m;
+      const int e = base + lane, n = e < p.experts ? count[e] : 0, s = (n + p.tok - 1) / p.tok;
+      int rn = n, rs = s;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int un = __shfl_up_sync(0xFFFFFFFFu, rn, d), um = __shfl_up_sync(0xFFFFFFFFu, rm, d);
-        if (lane >= d) rn += un, rm += um;
+        const int un = __shfl_up_sync(0xFFFFFFFFu, rn, d), us = __shfl_up_sync(0xFFFFFFFFu, rs, d);
+        if (lane >= d) rn += un, rs += us;
       }
-      if (e < p.experts) row0[e] = rows + rn - n, seg0[e] = segs + rm - m;
+      if (e < p.experts) row0[e] = rows + rn - n, seg0[e] = segs + rs - s;
       rows += __shfl_sync(0xFFFFFFFFu, rn, 31);
-      segs += __shfl_sync(0xFFFFFFFFu, rm, 31);
+      segs += __shfl_sync(0xFFFFFFFFu, rs, 31);
     }
-    if (lane == 0) row0[p.experts] = rows, seg0[p.experts] = segs;
+    if (lane == 0 && blockIdx.x == 0) *p.plan.segments = segs;
+  }
+  // The token's slots: how many earlier ones chose the same expert.
+  for (int j = w; j < p.topk; j += kPrepWarps) {
+    const int s = token * p.topk + j, e = ids[s];
+    int before = 0;
+    for (int i = lane; i < s; i += 32) before += ids[i] == e;
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    if (lane == 0) place[j] = before;
   }
   __syncthreads();
-  for (int s = tid; s < p.slots; s += kThreads)
-    if (ids[s] >= 0) sorted[row0[ids[s]] + place[s]] = (uint16_t)s;
-  const int segs = seg0[p.experts];
-  const int tiles = p.rows / kItemRows;  // items of a segment
-  const int64_t total = (int64_t)segs * tiles;
-  const int i0 = (int)(total * blockIdx.x / gridDim.x), i1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
-  if (i0 == i1) {
-    grid_dependency_wait();
-    grid_launch_dependents();
-    return;
-  }
-
-  // Expert of a segment.
-  auto expert_of = [&](int seg) {
-    int lo = 0, hi = p.experts;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (seg0[mid] <= seg) lo = mid; else hi = mid;
-    }
-    return lo;  // (the last of several with this first segment is the one that has it)
-  };
-  const int workers = kWarps / p.ks, worker = w / p.ks, k = w % p.ks;
-  const int c0 = C * k / p.ks, c1 = C * (k + 1) / p.ks;
-  const int first_seg = i0 / tiles;
-
-  // Loads run two chunks ahead.  The lane's rows of an item: g, and 8, 16, 24
-  // further (first kernel: gate row g, its up row, and both 8 further).
-  const int64_t pitch = p.width / 2, spitch = p.width / kBlock;
-  const int64_t row1 = kDown ? 8 : p.rows / 2, row2 = kDown ? 16 : 8;
-  const int item_rows = kDown ? kItemRows : kItemRows / 2;  // that the base row moves by
-  int a_item = i0 + worker, a_seg = first_seg, a_end = min(i1, (first_seg + 1) * tiles), ac = c0;
-  bool more = true;
-  const uint8_t *wp = nullptr, *sp = nullptr;
-  auto aim = [&]() {  // to the next segment while the share of this one is used up
-    while (a_item >= a_end) {
-      if (a_end >= i1) {
-        more = false;
-        return;
-      }
-      a_item = a_end + worker;
-      ++a_seg;
-      a_end = min(i1, (a_seg + 1) * tiles);
-    }
-    const int64_t r = (int64_t)expert_of(a_seg) * p.rows + (a_item - a_seg * tiles) * item_rows + g;
-    wp = p.data + r * pitch + 16 * t + 64 * c0;
-    sp = p.scale + r * spitch + (kBlock == 16 ? 2 : 1) * (t + 4 * c0);
-  };
-  const int64_t wstep = (int64_t)workers * item_rows * pitch - 64 * (c1 - c0);
-  const int64_t sstep = (int64_t)workers * item_rows * spitch - (kBlock == 16 ? 8 : 4) * (c1 - c0);
-  struct Chunk {
-    uint4 q[4];
-    uint32_t s[4];
-  };
-  auto load = [&](Chunk& d) {
-    if (!more) return;
-    const bool there = ac * kChunk + 32 * t < p.width;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = (i & 1 ? row1 : 0) + (i & 2 ? row2 : 0);
-      d.q[i] = load_weights(wp + r * pitch, there);
-      if constexpr (kBlock == 16)
-        d.s[i] = there ? __ldg(reinterpret_cast<const uint16_t*>(sp + r * spitch)) : 0u;
-      else
-        d.s[i] = there ? __ldg(sp + r * spitch) : 0u;
-    }
-    wp += 64;
-    sp += kBlock == 16 ? 8 : 4;
-    if (++ac == c1) {
-      ac = c0;
-      a_item += workers;
-      if (a_item < a_end) {
-        wp += wstep;
-        sp += sstep;
+  if (blockIdx.x == 0)
+    for (int e = tid; e < p.experts; e += kPrepThreads)
+      for (int i = 0; i * p.tok < count[e]; ++i)
+        p.plan.table[seg0[e] + i] = make_int4(e, row0[e] + i * p.tok, min(p.tok, count[e] - i * p.tok), 0);
+  const float unit = kBlock == 16 ? unit_of(m) : 1.0f;
+  if (part == 0)
+    for (int j = tid; j < p.topk; j += kPrepThreads) {
+      const int s = token * p.topk + j, e = ids[s];
+      if (e < 0) continue;
+      const int r = row0[e] + place[j];
+      p.plan.slot_of_row[r] = s;
+      p.x_rows.unit[r] = unit;
+      if constexpr (kBlock == 16) {
+        const float bound = __fmul_rn(p.amax[p.amax_per_expert ? e : 0], sum);
+        p.h_unit[r] = unit_of(fminf(__fmul_rn(2.0f * bound, bound), kFltMax));
       } else {
-        aim();
+        p.h_unit[r] = 1.0f;
       }
     }
-  };
-  Chunk ring[2];
-  aim();
-  load(ring[0]);
-  load(ring[1]);
-
-  if (kDown) {
-    grid_dependency_wait();
-    grid_launch_dependents();
+  // Terms of 128 elements a warp, the last ones padded to a step of 64 with zeros.
+  const int64_t k = (int64_t)part * kPrepPart + 128 * w + 4 * lane;
+  if (k - 4 * lane >= p.width) return;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (k < p.width) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + k));
+    v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
   }
+  uint32_t codes[kTerms], scales[2];
+  to_terms<kBlock>(v, unit, codes, scales);
+  if (k >= (p.width + 63) / 64 * 64) return;
+  const int64_t tiles = (p.width + 4 * kBlock - 1) / (4 * kBlock);
+  for (int j = 0; j < p.topk; ++j) {
+    const int e = ids[token * p.topk + j];
+    if (e < 0) continue;
+    const int r = row0[e] + place[j], seg = seg0[e] + place[j] / p.tok;
+    if (k < p.width)
+      store_codes<kBlock>(p.x_rows.codes + (int64_t)r * kTerms * (p.width / 2), p.width / 2, k, codes);
+    store_scales<kBlock>(p.x_rows.scales + seg * tiles * kScaleTile, place[j] % p.tok * kTerms, k, lane, scales);
+  }
+}
 
-  int item = i1, end = i0, seg = first_seg - 1;  // "before" the first segment
-  int c = c1, ntok = 0, nt = 0, first_row = 0;
-  float factor = 1.0f;
-  float acc[2][kNT][4];
+// ---------------------------------------------------------------------------
+// The products
+// ---------------------------------------------------------------------------
+constexpr int kOutWarps = 4, kScaleWarps = 4;
+constexpr int kThreads = 32 * (kOutWarps + 2 + kScaleWarps);
+constexpr int kWeights = 128;  // weight rows of a tile
+constexpr int kMaxStages = 8;
+static_assert(kScaleWarps == 4, "stages are dealt out to 4, 2 or 1 of them");
 
-  // The segment's activations into shared memory: a warp's share of a row at a
-  // time, kBatch pieces of 8 elements of a lane read at once.
-  auto load_x = [&]() {
-    constexpr int kBatch = kDown ? 2 : 4;
-    for (int q = w; q < ntok * p.ks; q += kWarps) {
-      const int n = q / p.ks, part = q % p.ks;
-      const int b0 = C * part / p.ks * (kChunk / 8), b1 = C * (part + 1) / p.ks * (kChunk / 8);
-      const int slot = sorted[first_row + n];
-      uint4 u[kBatch][kDown ? 2 : 1];
-      auto fetch = [&](int b) {
+struct MlpKernelArgs {
+  const uint8_t* scale;  // of the weights, compact
+  const float* amax;
+  int amax_per_expert;
+  int experts, rows, width;  // weight rows of an expert, contracted dimension
+  int inner;                 // up: gate rows of an expert
+  Plan plan;
+  Rows in;                   // the activations' terms
+  Rows out;                  // up: the hidden rows'
+  const float* gates;        // down
+  float* parts;              // down: [slots][rows]
+  int tiles;                 // of an expert's weights
+  unsigned* status;
+};
+
+struct Barriers {
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+  uint64_t got, taken;  // the cluster's partial results: all are here / all have been added
+  uint32_t tmem;
+  uint32_t pad;
+};
+
+template <int kTok, int kBlock>
+struct Layout {
+  using F = Format<kBlock>;
+  static constexpr int kBN = kTok * kTerms;
+  static constexpr int kCodes = (kWeights + kBN) * kStageRow;
+  static constexpr int kStageBytes = kCodes + 2 * F::kScaleBytes;
+  static constexpr int kBuffers = kBN > 64 ? 1 : 2;
+  static constexpr int kCols = kBuffers * kBN + 2 * F::kCols;
+  static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
+  static_assert(kCols <= 256, "two CTAs share an SM's tensor memory");
+  static constexpr int kResultBytes = kTok * kWeights * 4;  // a tile's results
+  static __host__ __device__ int own(int split) { return (kTok + split - 1) / split; }  // tokens a CTA of a cluster joins
+  static __host__ __device__ int share_bytes(int split) {
+    return split == 1 ? 0 : split * own(split) * kWeights * 4;
+  }
+  static int rest(int split) { return kResultBytes + share_bytes(split) + (int)sizeof(Barriers); }
+};
+
+__device__ __forceinline__ void store_async(uint32_t dst, float v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst),
+               "r"(__float_as_uint(v)), "r"(bar)
+               : "memory");
+}
+
+// The four writing warps meet, and stop together if one of them gave up waiting.
+__device__ __forceinline__ bool together(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+
+template <bool kDown, int kTok, int kBlock>
+__global__ void __launch_bounds__(kThreads, 2)
+expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                      const __grid_constant__ MlpKernelArgs p, int stages, int split) {
+  using L = Layout<kTok, kBlock>;
+  using F = Format<kBlock>;
+  constexpr int kBN = L::kBN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* results = reinterpret_cast<float*>(smem + stages * L::kStageBytes);  // [token][row]
+  float* shares = results + L::kResultBytes / 4;                              // [rank][own token][row]
+  Barriers* bar = reinterpret_cast<Barriers*>(shares + L::share_bytes(split) / 4);
+  const int own = L::own(split);
+  const int w = warp_index(), lane = threadIdx.x & 31;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
+
+  if (w == kOutWarps) {
+    if (lane == 0) {
+      for (int i = 0; i < stages; ++i) {
+        mbar_init(&bar->full[i], 2);
+        mbar_init(&bar->empty[i], 1);
+      }
+      for (int i = 0; i < L::kBuffers; ++i) {
+        mbar_init(&bar->tfull[i], 1);
+        mbar_init(&bar->tempty[i], kOutWarps);
+      }
+      mbar_init(&bar->got, 1);
+      mbar_init(&bar->taken, kOutWarps * split);
+      fence_mbar_init();
+      tma_prefetch_desc(&wmap);
+      tma_prefetch_desc(&xmap);
+    }
+  } else if (w == kOutWarps + 1) {
+    tmem_alloc(&bar->tmem, L::kTmemCols);
+  }
+  __syncwarp();
+  if (split > 1) cluster_arrive();  // (the barriers are set up)
+  grid_begin();
+  tcgen05_before_sync();
+  __syncthreads();
+  if (split > 1) cluster_wait();
+  tcgen05_after_sync();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem, 0);
+  const int lg_split = __ffs(split) - 1;
+  const int t0 = blockIdx.x >> lg_split, step = gridDim.x >> lg_split;
+  const int tiles = __shfl_sync(0xFFFFFFFFu, *p.plan.segments, 0) * p.tiles;
+  const int nkb = (p.width + kStageK - 1) / kStageK;
+  const int kb0 = (nkb * rank) >> lg_split, kb1 = (nkb * (rank + 1)) >> lg_split;
+  bool ok = true;
+  // Row r of a tile's 128: of the stack of all experts' weights.
+  constexpr int kTileRows = kDown ? kWeights : kWeights / 2;
+  auto first_row = [&](const int4& seg, int tile) { return seg.x * p.rows + tile * kTileRows; };
+
+  if (w == kOutWarps) {
+    uint32_t s = 0, phase = 1, sent = 0;
+    for (int t = t0; t < tiles && ok; t += step) {
+      const int4 seg = p.plan.table[t / p.tiles];
+      const int r0 = first_row(seg, t % p.tiles);
+      const int64_t scale_tiles = (p.width + 4 * kBlock - 1) / (4 * kBlock);
+      const uint8_t* xs = p.in.scales + (t / p.tiles) * scale_tiles * kScaleTile;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&bar->empty[s], phase)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t bytes = (uint32_t)min((int64_t)F::kTiles, scale_tiles - kb * F::kTiles) * kScaleTile;
+          const uint32_t dst = smem_u32(smem + s * L::kStageBytes), full = smem_u32(&bar->full[s]);
+          mbar_arrive_expect_tx(&bar->full[s], L::kCodes + bytes);
+          tma_load(dst, &wmap, kb * kStageRow, r0, full);
+          if (!kDown) tma_load(dst + kWeights / 2 * kStageRow, &wmap, kb * kStageRow, r0 + p.inner, full);
+          tma_load(dst + kWeights * kStageRow, &xmap, kb * kStageRow, seg.y * kTerms, full);
+          bulk_load(dst + L::kCodes + F::kScaleBytes, xs + (int64_t)kb * F::kScaleBytes, bytes, &bar->full[s]);
+        }
+        __syncwarp();
+        ++sent;
+        if (++s == (uint32_t)stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok) {
+      report_timeout(p.status);
+      // let the copies in flight land
+      for (uint32_t i = sent < (uint32_t)stages ? 0 : sent - stages; i < sent; ++i)
+        mbar_wait(&bar->full[i % stages], (i / stages) & 1);
+    }
+  } else if (w == kOutWarps + 1) {
+    constexpr uint32_t kIdesc = F::idesc(kWeights, kBN);
+    const uint64_t desc0 = operand_desc(smem_u32(smem));
+    const uint64_t sdesc0 = scale_desc(smem_u32(smem) + L::kCodes);
+    const uint32_t sw = tmem + L::kBuffers * kBN, sx = sw + F::kCols;
+    uint32_t s = 0, phase = 0, buf = 0, tphase = 1;
+    for (int t = t0; t < tiles && ok; t += step) {
+      if (!mbar_wait(&bar->tempty[buf], tphase)) {
+        ok = false;
+        break;
+      }
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&bar->full[s], phase)) {
+          ok = false;
+          break;
+        }
+        tcgen05_after_sync();
+        if (elect_one()) {
+          const uint64_t a = desc0 + s * (L::kStageBytes / 16), b = a + kWeights * kStageRow / 16;
+          const uint64_t ds = sdesc0 + s * (L::kStageBytes / 16);
+          const int left = p.width - kb * kStageK, steps = left >= kStageK ? 4 : (left + 63) / 64;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int at = b + 32 * i;
-          const bool there = at < b1 && 8 * at < p.width;
+          for (int j = 0; j < F::kTiles; ++j)
+            if (j * 4 * kBlock < steps * 64) {
+              scales_to_tmem<1>(sw + 4 * j, ds + j * (kScaleTile / 16));
+              scales_to_tmem<1>(sx + 4 * j, ds + (F::kScaleBytes + j * kScaleTile) / 16);
+            }
 #pragma unroll
-          for (int h = 0; h < (kDown ? 2 : 1); ++h) u[i][h] = make_uint4(0, 0, 0, 0);
-          if (there) {
-            if constexpr (kDown) {
-              const uint4* src = reinterpret_cast<const uint4*>(p.hidden + (int64_t)slot * p.width + 8 * at);
-              u[i][0] = __ldcg(src), u[i][1] = __ldcg(src + 1);
-            } else {
-              u[i][0] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(slot / p.topk) * p.width + 8 * at));
+          for (int k = 0; k < 4; ++k)
+            if (k < steps)
+              umma_fp4<1, kBlock>(tmem + buf * kBN, a + 2 * k, b + 2 * k, kIdesc | F::half(k), sw + F::col(k),
+                                  sx + F::col(k), kb > kb0 || k > 0);
+          umma_commit(&bar->empty[s]);
+          if (kb + 1 == kb1) umma_commit(&bar->tfull[buf]);
+        }
+        __syncwarp();
+        if (++s == (uint32_t)stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+      if (++buf == L::kBuffers) {
+        buf = 0;
+        tphase ^= 1;
+      }
+    }
+    if (!ok) report_timeout(p.status);
+  } else if (w > kOutWarps + 1) {
+    uint32_t s = 0, phase = 1, it = 0;
+    // No more warps than stages: a warp's stage may then not be two uses of its slot
+    // ahead, where the barrier's parity would be that of a phase long over.
+    const int mine = w - kOutWarps - 2, active = stages >= kScaleWarps ? kScaleWarps : stages >= 2 ? 2 : 1;
+    const int64_t pitch = p.width / kBlock;
+    const int last = p.experts * p.rows;
+    for (int t = t0; t < tiles && ok; t += step) {
+      const int r0 = first_row(p.plan.table[t / p.tiles], t % p.tiles);
+      for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+        if ((it & (active - 1)) == (uint32_t)mine) {
+          const int64_t at = (int64_t)kb * F::kRowBytes;
+          const int n = (int)min((int64_t)F::kRowBytes, pitch - at);
+          constexpr int kW = F::kTiles;
+          uint32_t v[4][kW];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int r = r0 + (kDown || g < 2 ? 32 * g : p.inner + 32 * (g - 2)) + lane;
+            compact_scales<kW>(p.scale + r * pitch + at, r < last ? n : 0, v[g]);
+          }
+          ok = mbar_wait(&bar->empty[s], phase);
+          if (ok) {
+            const uint32_t dst = smem_u32(smem + s * L::kStageBytes) + L::kCodes + 16 * lane;
+#pragma unroll
+            for (int j = 0; j < kW; ++j) sts_v4(dst + j * kScaleTile, v[0][j], v[1][j], v[2][j], v[3][j]);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->full[s]);
+          }
+        }
+        if (++s == (uint32_t)stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok) report_timeout(p.status);
+  } else {
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
+    const int r = 32 * w + lane;
+    uint32_t buf = 0, tphase = 0, round = 0;
+    for (int t = t0; t < tiles && ok; t += step) {
+      const int tile = t % p.tiles, segment = t / p.tiles;
+      const int4 seg = p.plan.table[segment];
+      const float factor = kBlock == 16 ? __fdiv_rn(p.amax[p.amax_per_expert ? seg.x : 0], 2688.0f) : 1.0f;
+      // this CTA's tokens of the segment, all or its share
+      const int first = split == 1 ? 0 : rank * own, mine = max(0, min(split == 1 ? kTok : own, seg.z - first));
+      ok = mbar_wait(&bar->tfull[buf], tphase);
+      if (ok && split > 1) ok = mbar_wait_cluster(&bar->taken, (round & 1) ^ 1, p.status);
+      if (!(ok = together(ok))) break;
+      tcgen05_after_sync();
+      if (split > 1 && w == 0 && lane == 0) mbar_arrive_expect_tx(&bar->got, split * kWeights * 4 * mine);
+      // A token's terms added, the smallest first.
+#pragma unroll 1
+      for (int n = 0; n < seg.z; n += 2) {
+        uint32_t v[16];
+        tmem_read(lane_base + buf * kBN + n * kTerms, v);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float sum = __uint_as_float(v[8 * h + kTerms - 1]);
+#pragma unroll
+          for (int i = kTerms - 2; i >= 0; --i)
+            sum = __fmaf_rn(sum, kBlock == 16 ? 0.25f : 1.0f, __uint_as_float(v[8 * h + i]));
+          const int token = n + h;
+          if (token >= seg.z) break;
+          if (split == 1) {
+            results[token * kWeights + r] = sum;
+          } else {
+            const int to = token / own;
+            store_async(map_to_cta(smem_u32(shares + (rank * own + token - to * own) * kWeights + r), to), sum,
+                        map_to_cta(smem_u32(&bar->got), to));
+          }
+        }
+      }
+      tcgen05_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->tempty[buf]);
+      if (++buf == L::kBuffers) {
+        buf = 0;
+        tphase ^= 1;
+      }
+      if (split > 1) {
+        ok = mbar_wait_cluster(&bar->got, round & 1, p.status);
+        if (!(ok = together(ok))) break;
+        for (int n = 0; n < mine; ++n) {
+          float sum = 0.0f;
+          for (int i = 0; i < split; ++i) sum = __fadd_rn(sum, shares[(i * own + n) * kWeights + r]);
+          results[n * kWeights + r] = sum;
+        }
+        __syncwarp();
+        if (t + step < tiles && lane < split) mbar_arrive_cluster_release(map_to_cta(smem_u32(&bar->taken), lane));
+        ++round;
+      }
+      // results[n]: the sums of token first + n of the segment
+      if constexpr (kDown) {
+        const int o = kWeights * tile + r;
+        if (o < p.rows)
+          for (int n = 0; n < mine; ++n) {
+            const int row = seg.y + first + n, slot = p.plan.slot_of_row[row];
+            const float v = __fmul_rn(__fmul_rn(results[n * kWeights + r], p.in.unit[row]), factor);
+            p.parts[(int64_t)slot * p.rows + o] = __fmul_rn(v, p.gates[slot]);
+          }
+      } else {
+        together(true);  // gate and up sums come from different warps
+        // 16 lanes take a token's 64 hidden values, four each
+        const int64_t f = kTileRows * (int64_t)tile + 4 * (lane & 15);
+        const int64_t out_tiles = (p.inner + 4 * kBlock - 1) / (4 * kBlock);
+        for (int n = 2 * w + (lane >> 4); n - (lane >> 4) < mine; n += 2 * kOutWarps) {
+          const bool there = n < mine;
+          const int row = seg.y + first + (there ? n : 0);
+          const float unit = __fmul_rn(p.in.unit[row], factor);
+          float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (there && f < p.inner) {
+            const float4 a = *reinterpret_cast<const float4*>(results + n * kWeights + 4 * (lane & 15));
+            const float4 b = *reinterpret_cast<const float4*>(results + n * kWeights + 64 + 4 * (lane & 15));
+            const float gate[4] = {a.x, a.y, a.z, a.w}, up[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float z = __fmul_rn(gate[i], unit);
+              v[i] = __fmul_rn(__fdiv_rn(z, __fadd_rn(1.0f, expf(-z))), __fmul_rn(up[i], unit));
             }
           }
+          uint32_t codes[kTerms], scales[2];
+          to_terms<kBlock>(v, p.out.unit[row], codes, scales);
+          if (!there) continue;
+          if (f < p.inner)
+            store_codes<kBlock>(p.out.codes + (int64_t)row * kTerms * (p.inner / 2), p.inner / 2, f, codes);
+          store_scales<kBlock>(p.out.scales + segment * out_tiles * kScaleTile, (first + n) * kTerms, f, lane, scales);
         }
-      };
-      auto unpack = [&](int i, float (&v)[8]) {
-        if constexpr (kDown) {
-          v[0] = __uint_as_float(u[i][0].x), v[1] = __uint_as_float(u[i][0].y), v[2] = __uint_as_float(u[i][0].z);
-          v[3] = __uint_as_float(u[i][0].w), v[4] = __uint_as_float(u[i][1].x), v[5] = __uint_as_float(u[i][1].y);
-          v[6] = __uint_as_float(u[i][1].z), v[7] = __uint_as_float(u[i][1].w);
-        } else {
-          v[0] = bf16_lo(u[i][0].x), v[1] = bf16_hi(u[i][0].x), v[2] = bf16_lo(u[i][0].y), v[3] = bf16_hi(u[i][0].y);
-          v[4] = bf16_lo(u[i][0].z), v[5] = bf16_hi(u[i][0].z), v[6] = bf16_lo(u[i][0].w), v[7] = bf16_hi(u[i][0].w);
-        }
-      };
-      float m = 0.0f;
-      for (int b = b0 + lane; b < b1; b += 32 * kBatch) {
-        fetch(b);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          float v[8];
-          unpack(i, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float a = fabsf(v[j]);
-            m = a <= kFltMax ? fmaxf(m, a) : m;  // (an infinity or a NaN stays one whatever the others' scale)
-          }
-        }
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-      // 2^s with s = 14 - floor(log2 m), at most 126 (m may be subnormal)
-      const int up = m == 0.0f ? 0 : min(14 - ((int)(__float_as_uint(m) >> 23) - 127), 126);
-      const float scale = __uint_as_float((uint32_t)(127 + up) << 23);
-      if (lane == 0) xinv[part * L::kRows + n] = __uint_as_float((uint32_t)(127 - up) << 23);
-      const bool again = b1 - b0 > 32 * kBatch;  // what was read last is not all of it
-      for (int b = b0 + lane; b < b1; b += 32 * kBatch) {
-        if (again) fetch(b);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int at = b + 32 * i;
-          if (at >= b1) break;
-          float v[8];
-          unpack(i, v);
-          uint32_t h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-                : "=r"(h[j])
-                : "f"(__fmul_rn(v[2 * j + 1], scale)), "f"(__fmul_rn(v[2 * j], scale)));
-          // Pieces in the order in which lanes 4 n .. 4 n + 3 read them together; odd rows half a line further.
-          const int piece = at & 15;
-          const int to = (kBlock == 16 ? (piece & 3) * 4 + (piece >> 2) : piece) ^ ((n & 1) * 4);
-          sts_v4(xs + ((at >> 4) * L::kRows + n) * (2 * kChunk) + 16 * to, h[0], h[1], h[2], h[3]);
-        }
+        together(true);  // the results may be overwritten
       }
     }
-  };
-
-  auto join = [&]() {  // the warps of a worker meet
-    if (p.ks == 1)
-      __syncwarp();
-    else  // (at most six workers then)
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "r"(32 * p.ks) : "memory");
-  };
-  // The worker's sums of an item, joined; then what becomes of them.
-  auto finish = [&]() {
-    join();  // the sums of the item before are read
-    float* mine = red + w * L::kRedFloats;
-#pragma unroll
-    for (int i = 0; i < kNT; ++i)
-      if (i < nt) {
-        const int n = 8 * i + 2 * t;
-        const float f0 = xinv[k * L::kRows + n], f1 = xinv[k * L::kRows + n + 1];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float* to = mine + n * kRedPitch + 16 * m + g;
-          to[0] = __fmul_rn(acc[m][i][0], f0);
-          to[kRedPitch] = __fmul_rn(acc[m][i][1], f1);
-          to[8] = __fmul_rn(acc[m][i][2], f0);
-          to[kRedPitch + 8] = __fmul_rn(acc[m][i][3], f1);
-        }
-      }
-    join();
-    const float* all = red + worker * p.ks * L::kRedFloats;
-    const int tile = item - seg * tiles;
-    constexpr int kOut = kDown ? 32 : 16;
-    for (int o = k * 32 + lane; o < ntok * kOut; o += 32 * p.ks) {
-      const int n = o / kOut, r = o % kOut, slot = sorted[first_row + n];
-      // (first kernel: gate and up rows alternate in eights)
-      const float* from = all + n * kRedPitch + (kDown ? r : (r & 7) + 2 * (r & 8));
-      float a = 0.0f, b = 0.0f;
-      for (int i = 0; i < p.ks; ++i, from += L::kRedFloats) {
-        a = __fadd_rn(a, from[0]);
-        if (!kDown) b = __fadd_rn(b, from[8]);
-      }
-      a = __fmul_rn(a, factor);
-      if constexpr (kDown) {
-        p.parts[(int64_t)slot * p.rows + kItemRows * tile + r] = __fmul_rn(a, p.gates[slot]);
-      } else {
-        b = __fmul_rn(b, factor);
-        p.hidden[(int64_t)slot * (p.rows / 2) + kItemRows / 2 * tile + r] =
-            __fmul_rn(__fdiv_rn(a, __fadd_rn(1.0f, expf(-a))), b);
-      }
-    }
-  };
-
-  // One chunk of kN x 8 rows of activations: its weights from the ring, 16 kN MMAs.
-  const uint32_t xl = xs + g * (2 * kChunk) + 16 * (t ^ ((g & 1) * 4));
-  auto multiply = [&](Chunk& d, auto rows) {
-    constexpr int kN = decltype(rows)::value;
-    const uint32_t xc = xl + c * (L::kRows * 2 * kChunk);
-    uint32_t sc[4];
-    if constexpr (kBlock == 16) {  // two E4M3 scales as FP16
-#pragma unroll
-      for (int i = 0; i < 4; ++i) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sc[i]) : "h"((uint16_t)d.s[i]));
-    } else {  // the chunk's four scales of each row
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        transpose4(d.q[i], t);
-        sc[i] = d.s[i] << (8 * t);
-        sc[i] |= __shfl_xor_sync(0xFFFFFFFFu, sc[i], 1);
-        sc[i] |= __shfl_xor_sync(0xFFFFFFFFu, sc[i], 2);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint4 b[kN];
-#pragma unroll
-      for (int n = 0; n < kN; ++n) b[n] = lds_v4((xc ^ (64 * j)) + n * 8 * (2 * kChunk));
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        uint32_t a[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4& q = d.q[2 * m + i];
-          to_f16(j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w, a[i]);
-          if constexpr (kBlock == 16) {
-            const uint32_t both = __byte_perm(sc[2 * m + i], 0, j < 2 ? 0x1010 : 0x3232);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) a[i][h] = mul_f16x2(a[i][h], both);
-          }
-        }
-        if constexpr (kBlock == 16) {
-#pragma unroll
-          for (int n = 0; n < kN; ++n) mma_f16(acc[m][n], a[0][0], a[1][0], a[0][1], a[1][1], b[n].x, b[n].y);
-#pragma unroll
-          for (int n = 0; n < kN; ++n) mma_f16(acc[m][n], a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
-        } else {
-          const float f0 = power_of_two((sc[2 * m] >> (8 * j)) & 255u);
-          const float f1 = power_of_two((sc[2 * m + 1] >> (8 * j)) & 255u);
-#pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma_f16(v, a[0][0], a[1][0], a[0][1], a[1][1], b[n].x, b[n].y);
-            mma_f16(v, a[0][2], a[1][2], a[0][3], a[1][3], b[n].z, b[n].w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][n][i] = __fmaf_rn(v[i], i < 2 ? f0 : f1, acc[m][n][i]);
-          }
-        }
-      }
-    }
-  };
-
-  auto step = [&](Chunk& d) {
-    if (c == c1) {  // the next item, and the next segments' activations on the way
-      if (end > i0) item += workers;
-      while (item >= end) {
-        if (end >= i1) return false;
-        __syncthreads();
-        item = end + worker;
-        ++seg;
-        end = min(i1, (seg + 1) * tiles);
-        const int e = expert_of(seg);
-        first_row = row0[e] + (seg - seg0[e]) * L::kRows;
-        ntok = min(L::kRows, row0[e + 1] - first_row);
-        nt = (ntok + 7) / 8;
-        factor = kBlock == 16 ? __fdiv_rn(p.amax[p.amax_per_expert ? e : 0], 2688.0f) : 1.0f;
-        load_x();
-        __syncthreads();
-      }
-      c = c0;
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int i = 0; i < kNT; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.0f;
-    }
-    if (kNT == 1 || nt == 1)
-      multiply(d, Count<1>());
-    else if (kNT == 2 || nt == 2)
-      multiply(d, Count<kNT == 1 ? 1 : 2>());
-    else
-      multiply(d, Count<kNT>());
-    load(d);
-    if (++c == c1) finish();
-    return true;
-  };
-  while (step(ring[0]) && step(ring[1])) {
+    if (!ok) report_timeout(p.status);
   }
+  __syncwarp();
+  tcgen05_before_sync();
+  __syncthreads();
+  // No CTA leaves before the others are done with its barriers.  What they
+  // send it has arrived by then, as it waited for it; a CTA that gave up waiting
+  // stays until stores in flight have landed.
+  if (split > 1) {
+    cluster_arrive_relaxed();
+    cluster_wait();
+    if (!ok) {
+      const long long c0 = clock64();
+      while (clock64() - c0 < 1000000LL) {
+      }
+    }
+  }
+  tcgen05_after_sync();
+  if (w == kOutWarps + 1) tmem_dealloc(tmem, L::kTmemCols);
 }
 
 // y[t] = the sum of a token's weighted results in the order of its choices.
@@ -533,86 +653,141 @@ __global__ void __launch_bounds__(256) join_slots_kernel(const float* __restrict
   }
 }
 
-// Warps that share an item: the split that keeps most warps busy, over the
-// chunks of the contracted dimension and over the items.
-int split_for(int width, int64_t items, int sms) {
-  const int C = (width + kChunk - 1) / kChunk;
-  int best = 1;
-  double most = 0.0;
-  for (int ks = 1; ks <= kWarps && ks <= C; ++ks) {
-    if (kWarps % ks != 0) continue;
-    const int64_t workers = (int64_t)sms * (kWarps / ks);
-    const double by_items = (double)items / (double)((items + workers - 1) / workers * workers);
-    const double by_chunks = (double)C / ((C + ks - 1) / ks * ks);
-    if (by_items * by_chunks > most * 1.02) {
-      most = by_items * by_chunks;
-      best = ks;
-    }
-  }
-  return best;
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+// Tokens of a segment: more cost columns that few experts fill, fewer read an
+// expert's weights again.
+int tokens_per_segment(int64_t tokens) { return tokens <= 2 ? 2 : tokens <= 8 ? 8 : 16; }
+int64_t most_segments(const ExpertMlpArgs& a) {
+  const int64_t slots = a.tokens * a.topk, used = slots < a.experts ? slots : a.experts;
+  return used + slots / tokens_per_segment(a.tokens);
 }
 
-constexpr int kMostShared = 227 * 1024;
+// The workspace, cut into its parts.
+struct Workspace {
+  Rows x, h;
+  Plan plan;
+  float* parts;
+  size_t bytes;
+};
+Workspace cut(const ExpertMlpArgs& a) {
+  Workspace ws = {};
+  uint8_t* at = static_cast<uint8_t*>(a.workspace);
+  size_t used = 0;
+  auto take = [&](int64_t bytes) {
+    uint8_t* p = at + used;
+    used += (size_t)((bytes + 127) / 128 * 128);
+    return p;
+  };
+  const int64_t slots = a.tokens * a.topk, segs = most_segments(a), per = 4 * a.block;
+  ws.x.codes = take(slots * kTerms * (a.hidden / 2));
+  ws.x.scales = take(segs * ((a.hidden + per - 1) / per) * kScaleTile);
+  ws.x.unit = reinterpret_cast<float*>(take(4 * slots));
+  ws.h.codes = take(slots * kTerms * (a.inner / 2));
+  ws.h.scales = take(segs * ((a.inner + per - 1) / per) * kScaleTile);
+  ws.h.unit = reinterpret_cast<float*>(take(4 * slots));
+  ws.plan.segments = reinterpret_cast<int32_t*>(take(4));
+  ws.plan.table = reinterpret_cast<int4*>(take(16 * segs));
+  ws.plan.slot_of_row = reinterpret_cast<int32_t*>(take(4 * slots));
+  ws.parts = reinterpret_cast<float*>(take(4 * slots * a.hidden));
+  ws.bytes = used;
+  return ws;
+}
 
-template <bool kDown, int kBlock, int kNT>
-cudaError_t launch(KernelArgs p, int64_t segments, const LaunchCtx& ctx) {
-  const auto kernel = expert_mlp_kernel<kDown, kBlock, kNT>;
-  static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kMostShared, allowed);
+template <bool kDown, int kTok, int kBlock>
+cudaError_t launch_product(const Fp4Side& weights, MlpKernelArgs p, int64_t slots, int64_t segments, const LaunchCtx& ctx) {
+  using L = Layout<kTok, kBlock>;
+  CUtensorMap wmap, xmap;
+  const int64_t all = (int64_t)p.experts * p.rows;
+  cudaError_t e = make_fp8_tensor_map(&wmap, weights.data, all, p.width / 2, kDown ? kWeights : kWeights / 2);
   if (e != cudaSuccess) return e;
-  p.ks = split_for(p.width, segments * (p.rows / kItemRows), ctx.num_sms);
-  void* args[] = {&p};
-  return launch_dependent(reinterpret_cast<const void*>(kernel), dim3((unsigned)ctx.num_sms), dim3(kThreads),
-                          Layout<kNT>::bytes(p.width, p.slots, p.experts), ctx.stream, args);
+  e = make_fp8_tensor_map(&xmap, p.in.codes, slots * kTerms, p.width / 2, L::kBN);
+  if (e != cudaSuccess) return e;
+  p.scale = weights.scale;
+  p.amax = weights.amax;
+  p.amax_per_expert = weights.amax_per_row;
+  p.tiles = kDown ? (p.rows + kWeights - 1) / kWeights : (p.inner + kWeights / 2 - 1) / (kWeights / 2);
+  p.status = ctx.status;
+  const int64_t tiles = segments * p.tiles, stages_k = (p.width + kStageK - 1) / kStageK;
+  int split = 1;
+  for (int s = 8; s >= 2 && split == 1; s /= 2)
+    if (tiles * s <= 2 * ctx.num_sms && stages_k >= 2 * s) split = s;
+  constexpr int kPerCta = 113 * 1024;  // two CTAs share an SM's 228 KB, 1 KB of it reserved for each
+  const int rest = 1024 + L::rest(split);
+  int stages = (kPerCta - rest) / L::kStageBytes;
+  if (stages > kMaxStages) stages = kMaxStages;
+  const int smem = rest + stages * L::kStageBytes;
+  const auto kernel = expert_product_kernel<kDown, kTok, kBlock>;
+  static std::atomic<uint64_t> allowed{0};
+  e = allow_smem(reinterpret_cast<const void*>(kernel), kPerCta, allowed);
+  if (e != cudaSuccess) return e;
+  const int64_t room = 2 * ctx.num_sms / split;
+  void* args[] = {&wmap, &xmap, &p, &stages, &split};
+  return launch_dependent(reinterpret_cast<const void*>(kernel), dim3((unsigned)((tiles < room ? tiles : room) * split)),
+                          dim3(kThreads), smem, ctx.stream, args, split);
 }
 
-// Rows of a segment: as many as the tokens, where shared memory holds them.
-template <bool kDown, int kBlock>
-cudaError_t launch_rows(const KernelArgs& p, int64_t tokens, int64_t experts_used, const LaunchCtx& ctx) {
-  if (tokens > 16 && Layout<4>::bytes(p.width, p.slots, p.experts) <= kMostShared)
-    return launch<kDown, kBlock, 4>(p, experts_used, ctx);
-  if (tokens > 8 && Layout<2>::bytes(p.width, p.slots, p.experts) <= kMostShared)
-    return launch<kDown, kBlock, 2>(p, experts_used, ctx);
-  return launch<kDown, kBlock, 1>(p, experts_used, ctx);
+template <int kTok, int kBlock>
+cudaError_t launch_products(const ExpertMlpArgs& a, const Workspace& ws, const LaunchCtx& ctx) {
+  const int64_t slots = a.tokens * a.topk, used = slots < a.experts ? slots : a.experts;
+  MlpKernelArgs p = {};
+  p.experts = a.experts;
+  p.plan = ws.plan;
+  p.gates = a.gates;
+  p.parts = ws.parts;
+  p.inner = (int)a.inner;
+  MlpKernelArgs up = p, down = p;
+  up.rows = (int)(2 * a.inner), up.width = (int)a.hidden, up.in = ws.x, up.out = ws.h;
+  down.rows = (int)a.hidden, down.width = (int)a.inner, down.in = ws.h;
+  const cudaError_t e = launch_product<false, kTok, kBlock>(a.up, up, slots, used, ctx);
+  return e != cudaSuccess ? e : launch_product<true, kTok, kBlock>(a.down, down, slots, used, ctx);
+}
+
+template <int kBlock>
+cudaError_t launch_layer(const ExpertMlpArgs& a, const LaunchCtx& ctx) {
+  const Workspace ws = cut(a);
+  PrepArgs p = {};
+  p.x = static_cast<const uint16_t*>(a.x);
+  p.ids = a.ids;
+  p.amax = a.up.amax;
+  p.amax_per_expert = a.up.amax_per_row;
+  p.slots = (int)(a.tokens * a.topk);
+  p.topk = a.topk;
+  p.experts = a.experts;
+  p.width = (int)a.hidden;
+  p.tok = tokens_per_segment(a.tokens);
+  p.x_rows = ws.x;
+  p.h_unit = ws.h.unit;
+  p.plan = ws.plan;
+  void* args[] = {&p};
+  const unsigned parts = (unsigned)((a.hidden + kPrepPart - 1) / kPrepPart);
+  cudaError_t e = launch_dependent(reinterpret_cast<const void*>(prepare_kernel<kBlock>), dim3((unsigned)a.tokens * parts),
+                                   dim3(kPrepThreads), 4 * (p.slots + 3 * p.experts), ctx.stream, args);
+  if (e != cudaSuccess) return e;
+  e = p.tok == 2 ? launch_products<2, kBlock>(a, ws, ctx)
+      : p.tok == 8 ? launch_products<8, kBlock>(a, ws, ctx)
+                   : launch_products<16, kBlock>(a, ws, ctx);
+  if (e != cudaSuccess) return e;
+  int rows = (int)a.hidden, tokens = (int)a.tokens, topk = a.topk, experts = a.experts;
+  const float* slots = ws.parts;
+  const int32_t* ids = a.ids;
+  void* y = a.y;
+  const int64_t want = ((int64_t)tokens * rows / 4 + 255) / 256;
+  void* join[] = {&slots, &ids, &topk, &experts, &rows, &tokens, &y};
+  return launch_dependent(reinterpret_cast<const void*>(join_slots_kernel),
+                          dim3((unsigned)(want < 8 * ctx.num_sms ? want : 8 * ctx.num_sms)), dim3(256), 0, ctx.stream, join);
 }
 
 }  // namespace
+}  // namespace fp4
 
-// One row tile's worth of rows always fits, whatever the call.
-static_assert(Layout<1>::bytes(kMaxMlpWidth, kMaxMlpSlots, kMaxExperts) <= kMostShared, "shared memory of one CTA");
-
-// The workspace: hidden values and weighted results of every slot.
-size_t expert_mlp_workspace(const ExpertMlpArgs& a) { return 4 * (size_t)(a.tokens * a.topk * (a.inner + a.hidden)); }
+size_t expert_mlp_workspace(const ExpertMlpArgs& a) { return fp4::cut(a).bytes; }
 
 cudaError_t launch_expert_mlp(const ExpertMlpArgs& a, const LaunchCtx& ctx) {
   if (a.tokens == 0 || a.hidden == 0) return cudaSuccess;
   if (a.inner == 0) return cudaMemsetAsync(a.y, 0, (size_t)a.tokens * a.hidden * 2, ctx.stream);
-  KernelArgs p = {};
-  p.x = static_cast<const uint16_t*>(a.x);
-  p.slots = (int)(a.tokens * a.topk);
-  p.topk = a.topk;
-  p.experts = a.experts;
-  p.ids = a.ids;
-  p.gates = a.gates;
-  p.hidden = static_cast<float*>(a.workspace);
-  p.parts = p.hidden + (size_t)p.slots * a.inner;
-  const int64_t used = p.slots < a.experts ? p.slots : a.experts;
-  KernelArgs up = p, down = p;
-  up.data = a.up.data, up.scale = a.up.scale, up.amax = a.up.amax, up.amax_per_expert = a.up.amax_per_row;
-  up.width = (int)a.hidden, up.rows = (int)(2 * a.inner);
-  down.data = a.down.data, down.scale = a.down.scale, down.amax = a.down.amax, down.amax_per_expert = a.down.amax_per_row;
-  down.width = (int)a.inner, down.rows = (int)a.hidden;
-  cudaError_t e = a.block == 16 ? launch_rows<false, 16>(up, a.tokens, used, ctx)
-                                : launch_rows<false, 32>(up, a.tokens, used, ctx);
-  if (e != cudaSuccess) return e;
-  e = a.block == 16 ? launch_rows<true, 16>(down, a.tokens, used, ctx) : launch_rows<true, 32>(down, a.tokens, used, ctx);
-  if (e != cudaSuccess) return e;
-  int rows = down.rows, tokens = (int)a.tokens;
-  const int64_t want = ((int64_t)tokens * rows / 4 + 255) / 256;
-  void* y = a.y;
-  void* args[] = {&p.parts, &p.ids, &p.topk, &p.experts, &rows, &tokens, &y};
-  return launch_dependent(reinterpret_cast<const void*>(join_slots_kernel),
-                          dim3((unsigned)(want < 8 * ctx.num_sms ? want : 8 * ctx.num_sms)), dim3(256), 0, ctx.stream, args);
+  return a.block == 16 ? fp4::launch_layer<16>(a, ctx) : fp4::launch_layer<32>(a, ctx);
 }
 
 }  // namespace nvfp4

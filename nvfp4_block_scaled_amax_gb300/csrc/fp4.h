@@ -39,6 +39,7 @@ struct Fp4MatmulArgs {
 };
 cudaError_t launch_fp4_matmul(const Fp4MatmulArgs& a, const LaunchCtx& ctx);
 
+constexpr int kMaxTopk = 64;
 constexpr int kMaxMlpSlots = 1024;
 constexpr int kMaxMlpWidth = 10240;  // hidden and inner sizes
 
@@ -56,7 +57,7 @@ struct ExpertMlpArgs {
   void* workspace;
   void* y;         // [tokens][hidden] BF16
 };
-size_t expert_mlp_workspace(const ExpertMlpArgs& a);
+size_t expert_mlp_workspace(const ExpertMlpArgs& a);  // (of its sizes and block)
 cudaError_t launch_expert_mlp(const ExpertMlpArgs& a, const LaunchCtx& ctx);
 
 // Tensor map of a row-major byte matrix, box 128 bytes x `box_rows` rows,

@@ -26,6 +26,7 @@ nvfp4_status check_operand(const nvfp4_operand* o, int block, int64_t rows, int6
   return NVFP4_OK;
 }
 
+static_assert(NVFP4_MAX_TOPK == kMaxTopk, "limits of the header");
 static_assert(NVFP4_MAX_MLP_SLOTS == kMaxMlpSlots && NVFP4_MAX_MLP_WIDTH == kMaxMlpWidth, "limits of the header");
 
 nvfp4_status check_mlp(int64_t tokens, int topk, int experts, int64_t hidden, int64_t inner) {
@@ -125,15 +126,18 @@ nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, in
 }
 
 nvfp4_status nvfp4_expert_mlp_workspace(int64_t tokens, int topk, int num_experts, int64_t hidden, int64_t inner,
-                                        size_t* bytes) {
+                                        int block, size_t* bytes) {
   if (bytes == nullptr) return NVFP4_ERR_NULL;
+  if (block != 16 && block != 32) return NVFP4_ERR_SHAPE;
   const nvfp4_status st = check_mlp(tokens, topk, num_experts, hidden, inner);
   if (st != NVFP4_OK) return st;
   ExpertMlpArgs a = {};
   a.tokens = tokens;
   a.topk = topk;
+  a.experts = num_experts;
   a.hidden = hidden;
   a.inner = inner;
+  a.block = block;
   *bytes = expert_mlp_workspace(a);
   return NVFP4_OK;
 }
@@ -151,7 +155,7 @@ nvfp4_status nvfp4_expert_mlp(const void* x, int64_t tokens, int64_t hidden, int
   if ((st = check_experts(down, block, any)) != NVFP4_OK) return st;
   if (tokens > 0 && hidden > 0 && y == nullptr) return NVFP4_ERR_NULL;
   if (any && (x == nullptr || expert_ids == nullptr || gates == nullptr || workspace == nullptr)) return NVFP4_ERR_NULL;
-  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(workspace, 16) || !aligned(expert_ids, 4) || !aligned(gates, 4))
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(workspace, 128) || !aligned(expert_ids, 4) || !aligned(gates, 4))
     return NVFP4_ERR_ALIGN;
   ExpertMlpArgs a = {};
   a.x = x;

@@ -25,6 +25,7 @@ constexpr int kOutWarps = 4, kScaleWarps = 4;
 constexpr int kThreads = 32 * (kOutWarps + 2 + kScaleWarps);
 constexpr int kWeights = 128;  // rows of B in a tile
 constexpr int kMaxStages = 8;
+static_assert(kScaleWarps == 4, "stages are dealt out to 4, 2 or 1 of them");
 
 struct Barriers {
   uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
@@ -181,12 +182,14 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   } else if (w > kOutWarps + 1) {
     if (compact) {
       uint32_t s = 0, phase = 1, it = 0;
-      const int mine = w - kOutWarps - 2;
+      // No more warps than stages: a warp's stage may then not be two uses of its slot
+      // ahead, where the barrier's parity would be that of a phase long over.
+      const int mine = w - kOutWarps - 2, active = stages >= kScaleWarps ? kScaleWarps : stages >= 2 ? 2 : 1;
       const int64_t pitch = p.K / kBlock;
       for (int t = t0; t < tiles && ok; t += step) {
         const int64_t n0 = (int64_t)(t / p.tiles_a) * kWeights, m0 = (int64_t)(t % p.tiles_a) * kBN;
         for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-          if ((it & (kScaleWarps - 1)) == (uint32_t)mine) {
+          if ((it & (active - 1)) == (uint32_t)mine) {
             const int64_t at = (int64_t)kb * F::kRowBytes;
             const int n = (int)min((int64_t)F::kRowBytes, pitch - at);
             constexpr int kW = F::kTiles;

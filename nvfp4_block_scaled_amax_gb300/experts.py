@@ -13,11 +13,12 @@ function beside the call.
 For decoding, a whole layer of gated experts over 4-bit weights:
 
     up, down = quantize_experts(gate_up), quantize_experts(down)      # [E, 2 F, H], [E, H, F], once
-    y = expert_mlp(x, up, down, expert_ids, gates)                    # three launches
+    y = expert_mlp(x, up, down, expert_ids, gates)                    # four launches
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -96,6 +97,14 @@ def quantize_experts(weights: torch.Tensor, block: int = 16) -> FP4Operand:
     return FP4Operand(data, scale, amax[:, 0].contiguous(), 16)
 
 
+@functools.lru_cache(maxsize=256)
+def _mlp_workspace(T: int, topk: int, E: int, H: int, F: int, block: int) -> int:
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.load().nvfp4_expert_mlp_workspace(T, topk, E, H, F, block, ctypes.byref(n)),
+               "nvfp4_expert_mlp_workspace")
+    return n.value
+
+
 def expert_mlp(x: torch.Tensor, up: FP4Operand, down: FP4Operand, expert_ids: torch.Tensor, gates: torch.Tensor,
                out: torch.Tensor | None = None) -> torch.Tensor:
     """y[t] = sum_j gates[t, j] * down[e] @ (silu(gate[e] @ x[t]) * (up[e] @ x[t])), e = expert_ids[t, j], for a few
@@ -130,7 +139,7 @@ def expert_mlp(x: torch.Tensor, up: FP4Operand, down: FP4Operand, expert_ids: to
         out = torch.empty_like(x)
     elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bfloat16 {tuple(x.shape)} tensor on {dev}")
-    need = 4 * T * topk * (H + F)
+    need = _mlp_workspace(T, topk, E, H, F, up.block)
     work = torch.empty(need, dtype=torch.uint8, device=dev)
     call("nvfp4_expert_mlp", dev, x.data_ptr(), T, H, F, ctypes.byref(_struct(up, E)), ctypes.byref(_struct(down, E)),
          up.block, expert_ids.data_ptr(), gates.data_ptr(), topk, E, work.data_ptr(), need, out.data_ptr())

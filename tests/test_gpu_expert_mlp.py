@@ -7,7 +7,7 @@ from fp4_testutil import random_parts, values
 
 pytestmark = pytest.mark.gpu
 
-U32, U16, F16 = 2.0 ** -24, 2.0 ** -8, 2.0 ** -11
+U32, U16 = 2.0 ** -24, 2.0 ** -8
 
 
 def stack(E, rows, cols, block, seed, std):
@@ -26,14 +26,22 @@ def stack(E, rows, cols, block, seed, std):
     return op, v
 
 
-def reference(x, up, down, ids, gates):
+def block_max(v, block):
+    return v.abs().view(-1, block).amax(1).repeat_interleave(block)
+
+
+def reference(x, up, down, ids, gates, block, amax):
     """(y, bound on the error) in 64 bits.
 
-    The products are exact in FP32 and x in FP16 scaled is exact (or off by 2^-31 of the largest beside it), so a sum of n
-    of them is off by n U32 of the sum of magnitudes; the factor, SiLU (derivative below 1.1) and the product cost a
-    handful of roundings; h is rounded to 11 bits, or by 2^-39 of the largest beside it; then the same again."""
+    x enters the products as eight 4-bit terms, each of which leaves 3/16 (NVFP4) or 1/4 (MXFP4) of the largest
+    remainder of its block: 2^-19 or 2^-16 of the block's largest element at last, and for NVFP4 never less than half of
+    the smallest scale, 2^-29 of the row's.  A sum of n products in each of eight columns is off by n U32 of the
+    magnitudes, which the terms at most double (1 + 3/16 + ..., 1 + 1/4 + ...).  The factor, SiLU (derivative below 1.1)
+    and the product cost a handful of roundings; h is cut like x, its NVFP4 unit being taken from 2 (amax sum|x|)^2; then
+    the same again."""
     T, H = x.shape
     F = down.shape[2]
+    left = 2.0 ** -19 if block == 16 else 2.0 ** -16
     y, bound = torch.zeros(T, H, dtype=torch.float64), torch.zeros(T, H, dtype=torch.float64)
     for t in range(T):
         for j in range(ids.shape[1]):
@@ -41,15 +49,19 @@ def reference(x, up, down, ids, gates):
             if not 0 <= e < up.shape[0]:
                 continue
             v = x[t].double()
-            s, m = up[e] @ v, up[e].abs() @ (v.abs() + 2.0 ** -7 * v.abs().max() * 2.0 ** -24)
-            ds = (H + 8) * U32 * m
+            dx = left * block_max(v, block) + (2.0 ** -29 * v.abs().max() if block == 16 else 0.0)
+            s = up[e] @ v
+            ds = up[e].abs() @ (dx + 2 * (H + 8) * U32 * v.abs())
             g, u, dg, du = s[:F], s[F:], ds[:F], ds[F:]
             act = g / (1 + torch.exp(-g))
             h = act * u
-            dh = 1.1 * dg * (u.abs() + du) + act.abs() * du + 12 * U32 * h.abs() + F16 * h.abs() + 2.0 ** -39 * h.abs().max()
+            dh = 1.1 * dg * (u.abs() + du) + act.abs() * du + 12 * U32 * h.abs()
+            dh = dh + left * block_max(h.abs() + dh, block)
+            if block == 16:
+                dh = dh + 2.0 ** -29 * 2 * (float(amax[e]) * float(v.abs().sum())) ** 2
             w = float(gates[t, j])
             y[t] += w * (down[e] @ h)
-            bound[t] += abs(w) * (down[e].abs() @ (dh + (F + 8) * U32 * h.abs()))
+            bound[t] += abs(w) * (down[e].abs() @ (dh + 2 * (F + 8) * U32 * h.abs()))
     return y, bound * 1.01 + U16 * (y.abs() + bound)
 
 
@@ -63,7 +75,7 @@ def check(T, topk, E, H, F, block, seed=0, ids=None):
     gates = torch.softmax(torch.randn(T, topk, generator=g), 1)
     args = (x.cuda(), up, down, ids.cuda(), gates.cuda())
     y = nv.expert_mlp(*args)
-    want, bound = reference(x, up_v, down_v, ids, gates)
+    want, bound = reference(x, up_v, down_v, ids, gates, block, None if up.amax is None else up.amax.cpu())
     assert bool(((y.cpu().double() - want).abs() <= bound).all())
     for _ in range(3):
         assert torch.equal(nv.expert_mlp(*args), y)  # whatever the order in which the CTAs finish
@@ -75,7 +87,8 @@ def check(T, topk, E, H, F, block, seed=0, ids=None):
 @pytest.mark.parametrize("T,topk,E,H,F", [(1, 1, 1, 32, 32), (1, 2, 8, 256, 128), (3, 2, 4, 160, 96), (8, 2, 4, 512, 352),
                                           (9, 4, 6, 1184, 160), (16, 3, 5, 96, 1056), (17, 2, 3, 288, 256),
                                           (40, 2, 3, 256, 192), (64, 4, 32, 128, 64), (5, 8, 200, 64, 32),
-                                          (1, 2, 4, 4096, 2048), (100, 1, 1, 64, 64)])
+                                          (1, 2, 4, 4096, 2048), (100, 1, 1, 64, 64),
+                                          (13, 4, 16, 2720, 1184), (40, 2, 5, 1056, 5120)])
 def test_layer(T, topk, E, H, F, block):
     check(T, topk, E, H, F, block, seed=T + H)
 
@@ -109,7 +122,7 @@ def test_quantized_experts(block):
     ids = torch.randint(0, E, (T, 2), generator=g, dtype=torch.int32)
     gates = torch.rand(T, 2, generator=g)
     y = nv.expert_mlp(x.cuda(), up, down, ids.cuda(), gates.cuda())
-    want, bound = reference(x, *vals, ids, gates)
+    want, bound = reference(x, *vals, ids, gates, block, None if up.amax is None else up.amax.cpu())
     assert bool(((y.cpu().double() - want).abs() <= bound).all())
 
 
@@ -131,7 +144,7 @@ def test_range_of_activations(block):
     ids = torch.zeros(8, 1, dtype=torch.int32)
     gates = torch.ones(8, 1)
     y = nv.expert_mlp(x.cuda(), up, down, ids.cuda(), gates.cuda()).cpu().double()
-    want, bound = reference(x, up_v, down_v, ids, gates)
+    want, bound = reference(x, up_v, down_v, ids, gates, block, None if up.amax is None else up.amax.cpu())
     fine = [0, 1, 2, 3, 4, 7]
     assert bool(((y - want).abs() <= bound)[fine].all())
     assert bool((y[4] == 0).all())

@@ -104,6 +104,17 @@ def test_product(shape, block):
                 check_product(m, n, k, block, block == 16, a_sw, b_sw, out_dtype, False, 1)
 
 
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("shape", [(64, 130, 16416), (16, 128, 16416), (50, 5000, 8224), (120, 20000, 1056),
+                                   (1500, 2500, 1312), (128, 40064, 640)])
+def test_product_long(shape, block):
+    """More stages than shared memory holds, and more tiles than CTAs, with scales of both layouts."""
+    m, n, k = shape
+    check_product(m, n, k, block, False, False, False, torch.float32, True)
+    if n % 128 == 0 and k % 128 == 0:
+        check_product(m, n, k, block, False, m % 128 == 0, True, torch.bfloat16, True)
+
+
 def test_product_of_nothing():
     for block in (16, 32):
         for m, n, k in ((0, 5, 64), (5, 0, 64), (5, 7, 0)):
