@@ -65,6 +65,10 @@ cudaError_t launch_expert_mlp(const ExpertMlpArgs& a, const LaunchCtx& ctx);
 cudaError_t make_fp8_tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int box_rows);
 // The same for stores of 4-bit codes: box 64 bytes x 128 rows, 64-byte swizzle.
 cudaError_t make_fp4_tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols);
+// Swizzled scales: a row for each 128 rows of the operand, `bytes` long; box
+// `box_bytes` (at most 2048) x `box_rows`, no swizzle, zero fill outside.
+cudaError_t make_scale_tensor_map(CUtensorMap* map, const void* p, int64_t rows, int64_t bytes, int box_bytes,
+                                  int box_rows);
 // Tensor map of a product (fp8.h).
 cudaError_t make_matmul_out_map(CUtensorMap* map, void* out, bool bf16, int64_t rows, int64_t cols);
 

@@ -106,7 +106,8 @@ def test_product(shape, block):
 
 @pytest.mark.parametrize("block", [16, 32])
 @pytest.mark.parametrize("shape", [(64, 130, 16416), (16, 128, 16416), (50, 5000, 8224), (120, 20000, 1056),
-                                   (1500, 2500, 1312), (128, 40064, 640)])
+                                   (1500, 2500, 1312), (128, 40064, 640), (5000, 4100, 96), (2560, 4864, 1408),
+                                   (4096, 4352, 256), (65, 257, 4128)])
 def test_product_long(shape, block):
     """More stages than shared memory holds, and more tiles than CTAs, with scales of both layouts."""
     m, n, k = shape
