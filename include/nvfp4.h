@@ -492,8 +492,9 @@ nvfp4_status nvfp4_fp8_matmul_grouped_wgrad(const uint8_t* a, const float* a_sca
  * 4-bit operands: the MXFP4 cast and its reading back, and the product of
  * NVFP4 or MXFP4 operands.  These entry points have no counterpart on the
  * pages this library follows.  The conventions above hold, except that compact
- * scales need no alignment, amaxes that of a float, and that there is no noop
- * flag.
+ * scales need no alignment (the products read them in aligned groups of 16 bytes,
+ * those that hold at least one of them), amaxes that of a float, and that there is
+ * no noop flag.
  *
  * MXFP4: E2M1 codes as above and, for each block of 32 elements with a =
  * max|x|, a power of two 2^(floor(log2 a) - 2), at least 2^-127, stored as one
@@ -550,8 +551,7 @@ nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, in
  * for x [tokens][hidden] BF16, y the same.  up: [experts][2 * inner][hidden]
  * operands, an expert's gate rows before its up rows; down:
  * [experts][hidden][inner]; both of one format (block 16 or 32), compact scales,
- * rowwise amax: one float, or with ROW_SCALED one for each expert.  NVFP4
- * scales need 2-byte alignment.  A choice outside 0..num_experts - 1 (-1, say)
+ * amax one float, or with ROW_SCALED one for each expert.  A choice outside 0..num_experts - 1 (-1, say)
  * adds nothing; a token with none left gives zero.
  * Sums are FP32; x and h enter a product as sums of eight 4-bit operands, which
  * leave at most 2^-19 (NVFP4) or 2^-16 (MXFP4) of the largest value of each block,

@@ -273,11 +273,10 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
 // ---------------------------------------------------------------------------
 // The products
 // ---------------------------------------------------------------------------
-constexpr int kOutWarps = 4, kScaleWarps = 4;
+constexpr int kOutWarps = 4;
 constexpr int kThreads = 32 * (kOutWarps + 2 + kScaleWarps);
 constexpr int kWeights = 128;  // weight rows of a tile
 constexpr int kMaxStages = 8;
-static_assert(kScaleWarps == 4, "stages are dealt out to 4, 2 or 1 of them");
 
 struct MlpKernelArgs {
   const uint8_t* scale;  // of the weights, compact
@@ -472,42 +471,32 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
     }
     if (!ok) report_timeout(p.status);
   } else if (w > kOutWarps + 1) {
-    uint32_t s = 0, phase = 1, it = 0;
-    // No more warps than stages: a warp's stage may then not be two uses of its slot
-    // ahead, where the barrier's parity would be that of a phase long over.
-    const int mine = w - kOutWarps - 2, active = stages >= kScaleWarps ? kScaleWarps : stages >= 2 ? 2 : 1;
-    const int64_t pitch = p.width / kBlock;
-    const int last = p.experts * p.rows;
-    for (int t = t0; t < tiles && ok; t += step) {
-      const int r0 = first_row(p.plan.table[t / p.tiles], t % p.tiles);
-      for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-        if ((it & (active - 1)) == (uint32_t)mine) {
-          const int64_t at = (int64_t)kb * F::kRowBytes;
-          const int n = (int)min((int64_t)F::kRowBytes, pitch - at);
-          constexpr int kW = F::kTiles;
-          uint32_t v[4][kW];
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int r = r0 + (kDown || g < 2 ? 32 * g : p.inner + 32 * (g - 2)) + lane;
-            compact_scales<kW>(p.scale + r * pitch + at, r < last ? n : 0, v[g]);
+    const int mine = w - kOutWarps - 2, active = active_scale_warps(stages);
+    if (mine < active) {
+      uint32_t s = 0, phase = 1, it = 0;
+      const CompactScales<kBlock> scales(p.scale, p.width, (int64_t)p.experts * p.rows);
+      for (int t = t0; t < tiles && ok; t += step) {
+        const int r0 = first_row(p.plan.table[t / p.tiles], t % p.tiles);
+        for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+          if ((it & (active - 1)) == (uint32_t)mine) {
+            uint32_t v[4][F::kTiles];
+            scales.read(r0, kWeights, kb, v, kDown ? 0 : p.inner - kWeights / 2);
+            ok = mbar_wait(&bar->empty[s], phase);
+            if (ok) {
+              scales.write(smem_u32(smem + s * L::kStageBytes) + L::kCodes, v);
+              fence_proxy_async_shared();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar->full[s]);
+            }
           }
-          ok = mbar_wait(&bar->empty[s], phase);
-          if (ok) {
-            const uint32_t dst = smem_u32(smem + s * L::kStageBytes) + L::kCodes + 16 * lane;
-#pragma unroll
-            for (int j = 0; j < kW; ++j) sts_v4(dst + j * kScaleTile, v[0][j], v[1][j], v[2][j], v[3][j]);
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->full[s]);
+          if (++s == (uint32_t)stages) {
+            s = 0;
+            phase ^= 1;
           }
-        }
-        if (++s == (uint32_t)stages) {
-          s = 0;
-          phase ^= 1;
         }
       }
+      if (!ok) report_timeout(p.status);
     }
-    if (!ok) report_timeout(p.status);
   } else {
     const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
     const int r = 32 * w + lane;

@@ -41,9 +41,7 @@ nvfp4_status check_mlp(int64_t tokens, int topk, int experts, int64_t hidden, in
 // A stack of weight matrices.
 nvfp4_status check_experts(const nvfp4_operand* o, int block, bool any) {
   if (o->flags & NVFP4_SWIZZLED) return NVFP4_ERR_FLAGS;
-  const nvfp4_status st = check_operand(o, block, any, any);
-  if (st != NVFP4_OK) return st;
-  return aligned(o->scale, block == 16 ? 2 : 1) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+  return check_operand(o, block, any, any);
 }
 
 Fp4Side side(const nvfp4_operand* o, int64_t rows) {

@@ -24,8 +24,8 @@ namespace {
 
 constexpr int kStages = 5;
 constexpr int kStageA = 128 * kStageRow, kCodes = 2 * kStageA;
-constexpr int kScaleWarps = 4, kOutWarps = 8, kFirstOut = 8;
-static_assert(kScaleWarps <= kStages, "a scale warp's stage is at most one use of its slot ahead");
+constexpr int kFirstScale = 4, kOutWarps = 8, kFirstOut = 8;
+static_assert(kScaleWarps <= kStages, "see active_scale_warps");
 constexpr int kThreads = 32 * (kFirstOut + kOutWarps);
 constexpr int kSecond = 208;  // first column of the second accumulator
 constexpr int kScaleCols = kSecond + 256;  // then the scales
@@ -162,7 +162,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       tphase ^= 1;
       const uint32_t d = tmem + buf * kSecond;
       for (int kb = 0; kb < nkb; ++kb) {
-        if (!(compact ? mbar_wait_cluster(&bar->full[s], phase, p.status) : mbar_wait(&bar->full[s], phase))) {
+        if (!mbar_wait(&bar->full[s], phase)) {
           ok = false;
           break;
         }
@@ -197,47 +197,35 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       buf ^= 1;
     }
     if (!ok) report_timeout(p.status);
-  } else if (w >= 4 && w < 4 + kScaleWarps) {
+  } else if (w >= kFirstScale && w < kFirstScale + kScaleWarps) {
     if (compact) {
       uint32_t s = 0, phase = 1, n_it = 0;
-      const uint32_t mine = w - 4;
-      const int64_t pitch = p.K / kBlock;
+      const CompactScales<kBlock> of_a(p.a.scale, p.K, p.a.rows), of_b(p.b.scale, p.K, p.b.rows);
       for (int i = t0; i < items && ok; i += step) {
         const Item it = at(i);
         if (it.n0 >= p.b.rows) continue;
-        const int64_t arow = it.m0 + 128 * (int64_t)rank, brow = it.n0;
         for (int kb = 0; kb < nkb && ok; ++kb, ++n_it) {
-          if ((n_it & (kScaleWarps - 1)) == mine) {
-            const int64_t off = (int64_t)kb * F::kRowBytes;
-            const int n = (int)min((int64_t)F::kRowBytes, pitch - off);
-            constexpr int kW = F::kTiles;
-            uint32_t va[4][kW], vb[8][kW];
-            if (!p.a.swizzled)
-#pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const int64_t r = arow + lane + 32 * g;
-                compact_scales<kW>(p.a.scale + r * pitch + off, r < p.a.rows ? n : 0, va[g]);
-              }
-            if (!p.b.swizzled)
-#pragma unroll
-              for (int g = 0; g < 8; ++g) {
-                const int64_t r = brow + lane + 32 * g;
-                compact_scales<kW>(p.b.scale + r * pitch + off, r < p.b.rows ? n : 0, vb[g]);
-              }
+          if ((n_it & (kScaleWarps - 1)) == (uint32_t)(w - kFirstScale)) {
+            uint32_t va[4][F::kTiles], vb[2][4][F::kTiles];
+            if (!p.a.swizzled) of_a.read(it.m0 + 128 * (int64_t)rank, 128, kb, va);
+            if (!p.b.swizzled) {
+              of_b.read(it.n0, 128, kb, vb[0]);
+              if (!it.half) of_b.read(it.n0 + 128, 128, kb, vb[1]);
+            }
             ok = mbar_wait(&bar->empty[s], phase);
             if (ok) {
-              const uint32_t dst = smem_u32(smem + s * L::kStageBytes) + kCodes + 16 * lane;
-#pragma unroll
-              for (int j = 0; j < kW; ++j) {
-                if (!p.a.swizzled) sts_v4(dst + j * kScaleTile, va[0][j], va[1][j], va[2][j], va[3][j]);
-                if (!p.b.swizzled) {
-                  sts_v4(dst + L::kScales + j * kScaleTile, vb[0][j], vb[1][j], vb[2][j], vb[3][j]);
-                  sts_v4(dst + 2 * L::kScales + j * kScaleTile, vb[4][j], vb[5][j], vb[6][j], vb[7][j]);
-                }
+              const uint32_t dst = smem_u32(smem + s * L::kStageBytes) + kCodes;
+              if (!p.a.swizzled) of_a.write(dst, va);
+              if (!p.b.swizzled) {
+                of_b.write(dst + L::kScales, vb[0]);
+                if (!it.half) of_b.write(dst + 2 * L::kScales, vb[1]);
               }
+              // What the first CTA's tensor-core copies read here is ordered by the
+              // fence; the arrival carries nothing else, so it needs no cluster-scope
+              // release, which would wait for every load in flight.
               fence_proxy_async_shared();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_release(map_to_cta(smem_u32(&bar->full[s]), 0));
+              if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&bar->full[s]), 0));
             }
           }
           if (++s == kStages) {

@@ -13,19 +13,17 @@
 //
 // Warps 0-3 write the results, warp 4 issues the copies, warp 5 the MMAs (two
 // accumulators, so that a tile is multiplied while the one before it is
-// written), warps 6-9 put compact scales in order, a stage each in turn: the
-// loads of four stages are in flight, which hides their latency.
+// written), warps 6-9 put compact scales in order, a stage each in turn.
 #include "fp4_tiles.cuh"
 
 namespace nvfp4 {
 namespace fp4 {
 namespace {
 
-constexpr int kOutWarps = 4, kScaleWarps = 4;
+constexpr int kOutWarps = 4;
 constexpr int kThreads = 32 * (kOutWarps + 2 + kScaleWarps);
 constexpr int kWeights = 128;  // rows of B in a tile
 constexpr int kMaxStages = 8;
-static_assert(kScaleWarps == 4, "stages are dealt out to 4, 2 or 1 of them");
 
 struct Barriers {
   uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
@@ -180,41 +178,22 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     }
     if (!ok) report_timeout(p.status);
   } else if (w > kOutWarps + 1) {
-    if (compact) {
+    const int mine = w - kOutWarps - 2, active = active_scale_warps(stages);
+    if (compact && mine < active) {
       uint32_t s = 0, phase = 1, it = 0;
-      // No more warps than stages: a warp's stage may then not be two uses of its slot
-      // ahead, where the barrier's parity would be that of a phase long over.
-      const int mine = w - kOutWarps - 2, active = stages >= kScaleWarps ? kScaleWarps : stages >= 2 ? 2 : 1;
-      const int64_t pitch = p.K / kBlock;
+      const CompactScales<kBlock> of_a(p.a.scale, p.K, p.a.rows), of_b(p.b.scale, p.K, p.b.rows);
       for (int t = t0; t < tiles && ok; t += step) {
         const int64_t n0 = (int64_t)(t / p.tiles_a) * kWeights, m0 = (int64_t)(t % p.tiles_a) * kBN;
         for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
           if ((it & (active - 1)) == (uint32_t)mine) {
-            const int64_t at = (int64_t)kb * F::kRowBytes;
-            const int n = (int)min((int64_t)F::kRowBytes, pitch - at);
-            constexpr int kW = F::kTiles;
-            uint32_t vb[4][kW], va[4][kW];
-            if (!p.b.swizzled)
-#pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const int64_t r = n0 + lane + 32 * g;
-                compact_scales<kW>(p.b.scale + r * pitch + at, r < p.b.rows ? n : 0, vb[g]);
-              }
-            if (!p.a.swizzled)
-#pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const int64_t r = m0 + lane + 32 * g;
-                compact_scales<kW>(p.a.scale + r * pitch + at, lane + 32 * g < kBN && r < p.a.rows ? n : 0, va[g]);
-              }
+            uint32_t va[4][F::kTiles], vb[4][F::kTiles];
+            if (!p.b.swizzled) of_b.read(n0, kWeights, kb, vb);
+            if (!p.a.swizzled) of_a.read(m0, kBN, kb, va);
             ok = mbar_wait(&bar->empty[s], phase);
             if (ok) {
-              const uint32_t dst = smem_u32(smem + s * L::kStageBytes) + L::kCodes + 16 * lane;
-#pragma unroll
-              for (int j = 0; j < kW; ++j) {
-                if (!p.b.swizzled) sts_v4(dst + j * kScaleTile, vb[0][j], vb[1][j], vb[2][j], vb[3][j]);
-                if (!p.a.swizzled)
-                  sts_v4(dst + F::kScaleBytes + j * kScaleTile, va[0][j], va[1][j], va[2][j], va[3][j]);
-              }
+              const uint32_t dst = smem_u32(smem + s * L::kStageBytes) + L::kCodes;
+              if (!p.b.swizzled) of_b.write(dst, vb);
+              if (!p.a.swizzled) of_a.write(dst + F::kScaleBytes, va);
               fence_proxy_async_shared();
               __syncwarp();
               if (lane == 0) mbar_arrive(&bar->full[s]);

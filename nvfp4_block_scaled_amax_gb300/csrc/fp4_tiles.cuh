@@ -131,33 +131,85 @@ __device__ __forceinline__ const uint8_t* swizzled_at(const Fp4Side& s, int64_t 
   return s.scale + ((row >> 7) * (K / (4 * kBlock)) + k0 / (4 * kBlock)) * kScaleTile;
 }
 
-// The scales of one row and stage, compact, as words; zeros past the row's end
-// and for a row that does not exist (n 0).  n: bytes there are.
-template <int kWords>
-__device__ __forceinline__ void compact_scales(const uint8_t* p, int n, uint32_t (&v)[kWords]) {
-  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
-  if (n == 4 * kWords && off % (4 * kWords) == 0) {
+// Compact scales on their way into the order of the swizzled layout: stage i's
+// words of 128 rows from row0 on, a lane taking four rows 32 apart (zeros past the
+// rows there are, past `limit` of the 128, and past a row's end).  A stage's scales
+// of a row are 16 (MXFP4: 8) bytes; where rows are not multiples of so many they
+// lie at any alignment and are put together from two aligned groups of so many
+// bytes, each of which holds at least one byte of the row.
+template <int kBlock>
+struct CompactScales {
+  static constexpr int kWords = Format<kBlock>::kTiles, kGroup = 4 * kWords;
+  const uint8_t* scale;
+  int64_t pitch, rows;
+  bool whole;  // every stage of every row is a group
+
+  __device__ __forceinline__ CompactScales(const uint8_t* at, int64_t K, int64_t rows_)
+      : scale(at), pitch(K / kBlock), rows(rows_),
+        whole(pitch % kGroup == 0 && (reinterpret_cast<uintptr_t>(at) & (kGroup - 1)) == 0) {}
+
+  static __device__ __forceinline__ void group(const uint8_t* p, bool there, uint32_t* w) {
     if constexpr (kWords == 4) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+      const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-      v[0] = w.x, v[1] = w.y;
+      const uint2 v = there ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+      w[0] = v.x, w[1] = v.y;
     }
-    return;
   }
-  // Words that hold a byte of the row, moved into place.
-  const uint32_t sh = (off & 3) * 8;
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(p - (off & 3));
-  uint32_t w[kWords + 1];
+  // gap: rows between the first 64 and the other 64.
+  __device__ __forceinline__ void read(int64_t row0, int limit, int i, uint32_t (&v)[4][kWords], int64_t gap = 0) const {
+    const int lane = threadIdx.x & 31;
+    const uint8_t* p = scale + (row0 + lane) * pitch + (int64_t)i * kGroup;
+    auto row = [&](int g) { return 32 * g + (g < 2 ? 0 : gap); };  // after the lane's first
+    if (whole) {
 #pragma unroll
-  for (int i = 0; i <= kWords; ++i) w[i] = 4 * i < n + (int)(off & 3) && n > 0 ? __ldg(q + i) : 0u;
+      for (int g = 0; g < 4; ++g)
+        group(p + row(g) * pitch, row0 + lane + row(g) < rows && lane + 32 * g < limit, v[g]);
+      return;
+    }
+    const int n = (int)min((int64_t)kGroup, pitch - (int64_t)i * kGroup);  // bytes of the stage
+    uint32_t w[4][2 * kWords];
 #pragma unroll
-  for (int i = 0; i < kWords; ++i) {
-    const int left = n - 4 * i;  // bytes of this word that the row has
-    const uint32_t x = __funnelshift_r(w[i], w[i + 1], sh);
-    v[i] = left >= 4 ? x : left <= 0 ? 0u : x & ((1u << (8 * left)) - 1);
+    for (int g = 0; g < 4; ++g) {
+      const uint8_t* q = p + row(g) * pitch;
+      const int off = (int)(reinterpret_cast<uintptr_t>(q) & (kGroup - 1));
+      const bool there = row0 + lane + row(g) < rows && lane + 32 * g < limit;
+      group(q - off, there, w[g]);
+      group(q - off + kGroup, there && off + n > kGroup, w[g] + kWords);
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int off = (int)(reinterpret_cast<uintptr_t>(p + row(g) * pitch) & (kGroup - 1));
+      uint32_t(&all)[2 * kWords] = w[g];
+      if constexpr (kWords == 4) {
+#pragma unroll
+        for (int k = 0; k < 6; ++k) all[k] = off & 8 ? all[k + 2] : all[k];
+      }
+#pragma unroll
+      for (int k = 0; k <= kWords; ++k) all[k] = off & 4 && k + 1 < 2 * kWords ? all[k + 1] : all[k];
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        const uint32_t x = __funnelshift_r(all[k], all[k + 1], 8 * (off & 3));
+        const int left = n - 4 * k;  // bytes of this word that the row has
+        v[g][k] = left >= 4 ? x : left <= 0 ? 0u : x & ((1u << (8 * left)) - 1);
+      }
+    }
   }
+  static __device__ __forceinline__ void write(uint32_t to, const uint32_t (&v)[4][kWords]) {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j)
+      sts_v4(to + j * kScaleTile + 16 * (threadIdx.x & 31), v[0][j], v[1][j], v[2][j], v[3][j]);
+  }
+};
+
+// The stages are dealt out to the warps that do this, so that the loads of
+// several are in flight; to no more warps than there are slots, for a warp's stage
+// may not be two uses of its slot ahead: the barrier's parity would be that of a
+// phase long over.
+constexpr int kScaleWarps = 4;
+__device__ __forceinline__ int active_scale_warps(int stages) {
+  return stages >= kScaleWarps ? kScaleWarps : stages >= 2 ? 2 : 1;
 }
 
 // The factor of an output: value * first * second, in that order.  One
