@@ -29,14 +29,11 @@
 // 128 weight rows on the tensor-memory lanes (64 gate and 64 up rows) by kTok
 // tokens' terms, the contracted dimension of a tile split over a cluster where
 // there are few tiles; partial results travel with their terms already added.
-#include "fp4_tiles.cuh"
-#include "tokens.h"
+#include "expert_mlp.cuh"
 
 namespace nvfp4 {
 namespace fp4 {
 namespace {
-
-constexpr int kTerms = 8;
 
 // What the launches hand to each other, in the workspace.
 struct Rows {
@@ -49,95 +46,6 @@ struct Plan {
   int4* table;           // [segments] expert, first sorted slot, slots
   int32_t* slot_of_row;  // [slots] slot of a sorted one
 };
-
-// ---------------------------------------------------------------------------
-// Terms
-// ---------------------------------------------------------------------------
-// Four elements of a block into terms: v is left with the remainders.  The
-// block lies in 4 (NVFP4) or 8 (MXFP4) neighbouring lanes.  codes[i]: four codes
-// of term i; scales: byte i the scale of term i.
-template <int kBlock>
-__device__ __forceinline__ void to_terms(float (&v)[4], float unit, uint32_t (&codes)[kTerms], uint32_t (&scales)[2]) {
-  scales[0] = scales[1] = 0;
-  float inv_unit6 = __fdiv_rn(1.0f / 6.0f, unit);
-#pragma unroll
-  for (int i = 0; i < kTerms; ++i) {
-    float m = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = fabsf(v[j]);
-      m = a >= m ? a : a != a ? __int_as_float(0x7F800000) : m;  // (a NaN counts as an infinity)
-    }
-#pragma unroll
-    for (int d = 1; d < kBlock / 4; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    uint32_t byte;
-    float value, inv;  // the scale, and its reciprocal (any rounding: what it leaves goes to the next term)
-    if constexpr (kBlock == 16) {
-      const float q = __fmul_rn(m, inv_unit6);
-      byte = e4m3_rn_satfinite(q);
-      if (byte < 126u && e4m3_decode(byte) < q) ++byte;
-      value = __fmul_rn(e4m3_decode(byte), unit);
-      inv = byte == 0 ? 0.0f : __fdividef(1.0f, value);
-      unit = __fmul_rn(unit, 0.25f);
-      inv_unit6 = __fmul_rn(inv_unit6, 4.0f);
-      if (!(q <= 449.0f)) byte = 127u;  // not finite: the whole row becomes NaN
-    } else {
-      const uint32_t e = __float_as_uint(m) >> 23;
-      byte = e < 2u ? 0u : e - 2u;
-      value = __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
-      inv = __uint_as_float((254u - byte) << 23);
-      if (!(m <= kFltMax)) byte = 255u;
-    }
-    if (!(m <= kFltMax)) inv = 0.0f;
-    uint16_t h;
-    asm("{\n .reg .b8 lo, hi;\n"
-        " cvt.rn.satfinite.e2m1x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 hi, %4, %3;\n"
-        " mov.b16 %0, {lo, hi};\n}"
-        : "=h"(h)
-        : "f"(__fmul_rn(v[0], inv)), "f"(__fmul_rn(v[1], inv)), "f"(__fmul_rn(v[2], inv)), "f"(__fmul_rn(v[3], inv)));
-    if (inv == 0.0f) h = 0;  // (an infinity times 0)
-    codes[i] = h;
-    scales[i >> 2] |= byte << (8 * (i & 3));
-    uint32_t f01, f23;
-    asm("{\n .reg .b8 lo, hi;\n mov.b16 {lo, hi}, %2;\n cvt.rn.f16x2.e2m1x2 %0, lo;\n cvt.rn.f16x2.e2m1x2 %1, hi;\n}"
-        : "=r"(f01), "=r"(f23)
-        : "h"(h));
-    float c[4];
-    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}"
-        : "=f"(c[0]), "=f"(c[1])
-        : "r"(f01));
-    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}"
-        : "=f"(c[2]), "=f"(c[3])
-        : "r"(f23));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = __fmaf_rn(-c[j], value, v[j]);
-  }
-}
-
-// Their places: four codes of each term in rows of `pitch` bytes, and the
-// lane's share of the block's scales (row n0 + i of a segment is term i).
-template <int kBlock>
-__device__ __forceinline__ void store_codes(uint8_t* row, int64_t pitch, int64_t element, const uint32_t (&codes)[kTerms]) {
-#pragma unroll
-  for (int i = 0; i < kTerms; ++i)
-    *reinterpret_cast<uint16_t*>(row + i * pitch + element / 2) = (uint16_t)codes[i];
-}
-template <int kBlock>
-__device__ __forceinline__ void store_scales(uint8_t* segment, int n0, int64_t element, int lane,
-                                             const uint32_t (&scales)[2]) {
-  constexpr int kLanes = kBlock / 4, kEach = kTerms / kLanes;
-  uint8_t* tile = segment + element / (4 * kBlock) * kScaleTile + element % (4 * kBlock) / kBlock;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int term = (lane % kLanes) * kEach + i, n = n0 + term;
-    tile[n % 32 * 16 + n / 32 * 4] = (uint8_t)(scales[term >> 2] >> (8 * (term & 3)));
-  }
-}
-// Power of two at which scales up to 448 reach a sixth of `largest`.
-__device__ __forceinline__ float unit_of(float largest) {
-  const int e = (int)(__float_as_uint(largest) >> 23) - 127;  // floor(log2)
-  return __uint_as_float((uint32_t)(max(-100, e - 10) + 127) << 23);
-}
 
 // ---------------------------------------------------------------------------
 // Slots by expert, and x into terms
@@ -156,24 +64,54 @@ struct PrepArgs {
   Plan plan;
 };
 
+// Slots by expert, by all threads of a CTA: how many chose each expert before e
+// (row0[e], and how many segments they make, seg0[e]; e up to `experts`).  ids:
+// those outside the range become -1.  Ends with a barrier.
+__device__ __forceinline__ void group_slots(const int32_t* from, int slots, int experts, int tok, int* ids, int* row0,
+                                            int* seg0, int threads) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int e = tid; e <= experts; e += threads) row0[e] = 0;
+  for (int s = tid; s < slots; s += threads) {
+    const int e = from[s];
+    ids[s] = e >= 0 && e < experts ? e : -1;
+  }
+  __syncthreads();
+  for (int s = tid; s < slots; s += threads)
+    if (ids[s] >= 0) atomicAdd(&row0[ids[s]], 1);
+  __syncthreads();
+  if (tid < 32) {
+    int rows = 0, segs = 0;
+    for (int base = 0; base < experts; base += 32) {
+      const int e = base + lane, n = e < experts ? row0[e] : 0, s = (n + tok - 1) / tok;
+      int rn = n, rs = s;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int un = __shfl_up_sync(0xFFFFFFFFu, rn, d), us = __shfl_up_sync(0xFFFFFFFFu, rs, d);
+        if (lane >= d) rn += un, rs += us;
+      }
+      if (e < experts) row0[e] = rows + rn - n, seg0[e] = segs + rs - s;
+      rows += __shfl_sync(0xFFFFFFFFu, rn, 31);
+      segs += __shfl_sync(0xFFFFFFFFu, rs, 31);
+    }
+    if (lane == 0) row0[experts] = rows, seg0[experts] = segs;
+  }
+  __syncthreads();
+}
+
 template <int kBlock>
 __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_constant__ PrepArgs p) {
   extern __shared__ int lists[];
   int* ids = lists;                      // [slots]
-  int* row0 = ids + p.slots;             // [experts] first sorted slot
-  int* seg0 = row0 + p.experts;          // [experts] first segment
-  int* count = seg0 + p.experts;         // [experts]
+  int* row0 = ids + p.slots;             // [experts + 1] first sorted slot
+  int* seg0 = row0 + p.experts + 1;      // [experts + 1] first segment
   __shared__ float largest[kPrepWarps], sums[kPrepWarps];
   __shared__ int place[kMaxTopk];
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int parts = (p.width + kPrepPart - 1) / kPrepPart;
   const int token = blockIdx.x / parts, part = blockIdx.x % parts;
-  grid_begin();
-  for (int s = tid; s < p.slots; s += kPrepThreads) {
-    const int e = p.ids[s];
-    ids[s] = e >= 0 && e < p.experts ? e : -1;
-  }
-  for (int e = tid; e < p.experts; e += kPrepThreads) count[e] = 0;
+  // (first the wait: the next kernel reads what precedes this one ahead of its own)
+  grid_dependency_wait();
+  grid_launch_dependents();
   // The row's largest finite element and the sum of magnitudes.
   const uint16_t* row = p.x + (int64_t)token * p.width;
   float m = 0.0f, sum = 0.0f;
@@ -197,29 +135,10 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
     sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, d));
   }
   if (lane == 0) largest[w] = m, sums[w] = sum;
-  __syncthreads();
+  group_slots(p.ids, p.slots, p.experts, p.tok, ids, row0, seg0, kPrepThreads);
   m = largest[0], sum = sums[0];
 #pragma unroll
   for (int i = 1; i < kPrepWarps; ++i) m = fmaxf(m, largest[i]), sum = __fadd_rn(sum, sums[i]);
-  for (int s = tid; s < p.slots; s += kPrepThreads)
-    if (ids[s] >= 0) atomicAdd(&count[ids[s]], 1);
-  __syncthreads();
-  if (w == 0) {
-    int rows = 0, segs = 0;
-    for (int base = 0; base < p.experts; base += 32) {
-      const int e = base + lane, n = e < p.experts ? count[e] : 0, s = (n + p.tok - 1) / p.tok;
-      int rn = n, rs = s;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int un = __shfl_up_sync(0xFFFFFFFFu, rn, d), us = __shfl_up_sync(0xFFFFFFFFu, rs, d);
-        if (lane >= d) rn += un, rs += us;
-      }
-      if (e < p.experts) row0[e] = rows + rn - n, seg0[e] = segs + rs - s;
-      rows += __shfl_sync(0xFFFFFFFFu, rn, 31);
-      segs += __shfl_sync(0xFFFFFFFFu, rs, 31);
-    }
-    if (lane == 0 && blockIdx.x == 0) *p.plan.segments = segs;
-  }
   // The token's slots: how many earlier ones chose the same expert.
   for (int j = w; j < p.topk; j += kPrepWarps) {
     const int s = token * p.topk + j, e = ids[s];
@@ -229,10 +148,12 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
     if (lane == 0) place[j] = before;
   }
   __syncthreads();
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0) {
     for (int e = tid; e < p.experts; e += kPrepThreads)
-      for (int i = 0; i * p.tok < count[e]; ++i)
-        p.plan.table[seg0[e] + i] = make_int4(e, row0[e] + i * p.tok, min(p.tok, count[e] - i * p.tok), 0);
+      for (int r = row0[e], i = seg0[e]; r < row0[e + 1]; r += p.tok, ++i)
+        p.plan.table[i] = make_int4(e, r, min(p.tok, row0[e + 1] - r), 0);
+    if (tid == 0) *p.plan.segments = seg0[p.experts];
+  }
   const float unit = kBlock == 16 ? unit_of(m) : 1.0f;
   if (part == 0)
     for (int j = tid; j < p.topk; j += kPrepThreads) {
@@ -284,6 +205,8 @@ struct MlpKernelArgs {
   int amax_per_expert;
   int experts, rows, width;  // weight rows of an expert, contracted dimension
   int inner;                 // up: gate rows of an expert
+  const int32_t* ids;        // up
+  int slots;
   Plan plan;
   Rows in;                   // the activations' terms
   Rows out;                  // up: the hidden rows'
@@ -304,36 +227,22 @@ template <int kTok, int kBlock>
 struct Layout {
   using F = Format<kBlock>;
   static constexpr int kBN = kTok * kTerms;
-  static constexpr int kCodes = (kWeights + kBN) * kStageRow;
+  static constexpr int kWCodes = kWeights * kStageRow;
+  static constexpr int kCodes = kWCodes + kBN * kStageRow;
   static constexpr int kStageBytes = kCodes + 2 * F::kScaleBytes;
   static constexpr int kBuffers = kBN > 64 ? 1 : 2;
   static constexpr int kCols = kBuffers * kBN + 2 * F::kCols;
   static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
-  static_assert(kCols <= 256, "two CTAs share an SM's tensor memory");
+  static_assert(kCols <= 256 && kStageBytes % 1024 == 0, "tensor memory of two CTAs; swizzled operands");
   static constexpr int kResultBytes = kTok * kWeights * 4;  // a tile's results
   static __host__ __device__ int own(int split) { return (kTok + split - 1) / split; }  // tokens a CTA of a cluster joins
   static __host__ __device__ int share_bytes(int split) {
     return split == 1 ? 0 : split * own(split) * kWeights * 4;
   }
-  static int rest(int split) { return kResultBytes + share_bytes(split) + (int)sizeof(Barriers); }
+  static int rest(int split, int slots, int experts) {
+    return kResultBytes + share_bytes(split) + (int)sizeof(Barriers) + 4 * (2 * (experts + 1) + slots);
+  }
 };
-
-__device__ __forceinline__ void store_async(uint32_t dst, float v, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst),
-               "r"(__float_as_uint(v)), "r"(bar)
-               : "memory");
-}
-
-// The four writing warps meet, and stop together if one of them gave up waiting.
-__device__ __forceinline__ bool together(bool ok) {
-  uint32_t all;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(all)
-      : "r"((uint32_t)ok)
-      : "memory");
-  return all != 0;
-}
 
 template <bool kDown, int kTok, int kBlock>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -347,6 +256,9 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
   float* results = reinterpret_cast<float*>(smem + stages * L::kStageBytes);  // [token][row]
   float* shares = results + L::kResultBytes / 4;                              // [rank][own token][row]
   Barriers* bar = reinterpret_cast<Barriers*>(shares + L::share_bytes(split) / 4);
+  int* row0 = reinterpret_cast<int*>(bar + 1);  // up: as group_slots gives them
+  int* seg0 = row0 + p.experts + 1;
+  int* ids = seg0 + p.experts + 1;
   const int own = L::own(split);
   const int w = warp_index(), lane = threadIdx.x & 31;
   const int rank = split > 1 ? (int)cluster_rank() : 0;
@@ -372,7 +284,13 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
   }
   __syncwarp();
   if (split > 1) cluster_arrive();  // (the barriers are set up)
-  grid_begin();
+  // Ahead of the wait for the kernel before: what that one does not write, as it
+  // waited for its own predecessor before it let this one begin.
+  int segs;
+  if constexpr (kDown)
+    segs = *p.plan.segments;  // (two kernels back)
+  else
+    group_slots(p.ids, p.slots, p.experts, kTok, ids, row0, seg0, kThreads), segs = seg0[p.experts];
   tcgen05_before_sync();
   __syncthreads();
   if (split > 1) cluster_wait();
@@ -380,36 +298,83 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar->tmem, 0);
   const int lg_split = __ffs(split) - 1;
   const int t0 = blockIdx.x >> lg_split, step = gridDim.x >> lg_split;
-  const int tiles = __shfl_sync(0xFFFFFFFFu, *p.plan.segments, 0) * p.tiles;
+  const int tiles = __shfl_sync(0xFFFFFFFFu, segs, 0) * p.tiles;
   const int nkb = (p.width + kStageK - 1) / kStageK;
+  const int full_stages = p.width / kStageK, last_steps = (p.width % kStageK + 63) / 64;  // of 64 elements
   const int kb0 = (nkb * rank) >> lg_split, kb1 = (nkb * (rank + 1)) >> lg_split;
   bool ok = true;
-  // Row r of a tile's 128: of the stack of all experts' weights.
+  // A segment: its expert, first sorted slot and slots.
+  auto segment_of = [&](int i) -> int4 {
+    if constexpr (kDown) return p.plan.table[i];
+    int lo = 0, hi = p.experts;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (seg0[mid] <= i) lo = mid; else hi = mid;
+    }
+    const int r = row0[lo] + (i - seg0[lo]) * kTok;
+    return make_int4(lo, r, min(kTok, row0[lo + 1] - r), 0);
+  };
+  // First row of a tile of an expert, in the stack of all experts' weights.
   constexpr int kTileRows = kDown ? kWeights : kWeights / 2;
-  auto first_row = [&](const int4& seg, int tile) { return seg.x * p.rows + tile * kTileRows; };
+  auto first_row = [&](int expert, int tile) { return expert * p.rows + tile * kTileRows; };
+  // (The copying warp waits when it has sent the first weights, and the warps of
+  // the weights' scales need not: the next kernel begins when all have come here.)
+  if (w != kOutWarps && w <= kOutWarps + 1) grid_dependency_wait();
+  if (w != kOutWarps) grid_launch_dependents();
 
   if (w == kOutWarps) {
-    uint32_t s = 0, phase = 1, sent = 0;
+    const int scale_tiles = (p.width + 4 * kBlock - 1) / (4 * kBlock);
+    // A tile's places, worked out once for all of its stages: that takes as long as a stage's copies.
+    struct Place {
+      int row, x_row;
+      const uint8_t* x_scales;
+    };
+    auto place_of = [&](int t) {
+      const int i = t / p.tiles, tile = t - i * p.tiles;
+      const int4 seg = segment_of(i);
+      return Place{first_row(seg.x, tile), seg.y * kTerms,
+                   p.in.scales + (int64_t)i * scale_tiles * kScaleTile};
+    };
+    auto scale_bytes = [&](int kb) { return (uint32_t)min(F::kTiles, scale_tiles - kb * F::kTiles) * kScaleTile; };
+    auto weights = [&](const Place& at, int kb, uint32_t s) {
+      if (elect_one()) {
+        const uint32_t dst = smem_u32(smem + s * L::kStageBytes), full = smem_u32(&bar->full[s]);
+        mbar_arrive_expect_tx(&bar->full[s], L::kCodes + scale_bytes(kb));
+        tma_load(dst, &wmap, kb * kStageRow, at.row, full);
+        if (!kDown) tma_load(dst + L::kWCodes / 2, &wmap, kb * kStageRow, at.row + p.inner, full);
+      }
+      __syncwarp();
+    };
+    auto activations = [&](const Place& at, int kb, uint32_t s) {
+      if (elect_one()) {
+        const uint32_t dst = smem_u32(smem + s * L::kStageBytes), full = smem_u32(&bar->full[s]);
+        tma_load(dst + L::kWCodes, &xmap, kb * kStageRow, at.x_row, full);
+        bulk_load(dst + L::kCodes + F::kScaleBytes, at.x_scales + kb * F::kScaleBytes, scale_bytes(kb),
+                  &bar->full[s]);
+      }
+      __syncwarp();
+    };
+    // The first stages' weights ahead of the kernel before, whose results the activations are.
+    int early = 0;
+    for (int t = t0; t < tiles && early < stages; t += step) {
+      const Place at = place_of(t);
+      for (int kb = kb0; kb < kb1 && early < stages; ++kb, ++early) weights(at, kb, early);
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    uint32_t s = 0, phase = 1;
+    int sent = 0;
     for (int t = t0; t < tiles && ok; t += step) {
-      const int4 seg = p.plan.table[t / p.tiles];
-      const int r0 = first_row(seg, t % p.tiles);
-      const int64_t scale_tiles = (p.width + 4 * kBlock - 1) / (4 * kBlock);
-      const uint8_t* xs = p.in.scales + (t / p.tiles) * scale_tiles * kScaleTile;
+      const Place at = place_of(t);
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&bar->empty[s], phase)) {
-          ok = false;
-          break;
+        if (sent >= early) {
+          if (!mbar_wait(&bar->empty[s], phase)) {
+            ok = false;
+            break;
+          }
+          weights(at, kb, s);
         }
-        if (elect_one()) {
-          const uint32_t bytes = (uint32_t)min((int64_t)F::kTiles, scale_tiles - kb * F::kTiles) * kScaleTile;
-          const uint32_t dst = smem_u32(smem + s * L::kStageBytes), full = smem_u32(&bar->full[s]);
-          mbar_arrive_expect_tx(&bar->full[s], L::kCodes + bytes);
-          tma_load(dst, &wmap, kb * kStageRow, r0, full);
-          if (!kDown) tma_load(dst + kWeights / 2 * kStageRow, &wmap, kb * kStageRow, r0 + p.inner, full);
-          tma_load(dst + kWeights * kStageRow, &xmap, kb * kStageRow, seg.y * kTerms, full);
-          bulk_load(dst + L::kCodes + F::kScaleBytes, xs + (int64_t)kb * F::kScaleBytes, bytes, &bar->full[s]);
-        }
-        __syncwarp();
+        activations(at, kb, s);
         ++sent;
         if (++s == (uint32_t)stages) {
           s = 0;
@@ -420,8 +385,7 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
     if (!ok) {
       report_timeout(p.status);
       // let the copies in flight land
-      for (uint32_t i = sent < (uint32_t)stages ? 0 : sent - stages; i < sent; ++i)
-        mbar_wait(&bar->full[i % stages], (i / stages) & 1);
+      for (int i = sent < stages ? 0 : sent - stages; i < sent; ++i) mbar_wait(&bar->full[i % stages], (i / stages) & 1);
     }
   } else if (w == kOutWarps + 1) {
     constexpr uint32_t kIdesc = F::idesc(kWeights, kBN);
@@ -440,21 +404,27 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
           break;
         }
         tcgen05_after_sync();
+        const uint64_t a = desc0 + s * (L::kStageBytes / 16), b = a + L::kWCodes / 16;
+        const uint64_t ds = sdesc0 + s * (L::kStageBytes / 16);
+        const uint32_t add = kb > kb0;
+        auto copy = [&](int j) {
+          scales_to_tmem<1>(sw + 4 * j, ds + j * (kScaleTile / 16));
+          scales_to_tmem<1>(sx + 4 * j, ds + (F::kScaleBytes + j * kScaleTile) / 16);
+        };
+        auto multiply = [&](int k) {
+          umma_fp4<1, kBlock>(tmem + buf * kBN, a + 2 * k, b + 2 * k, kIdesc | F::half(k), sw + F::col(k), sx + F::col(k),
+                              k > 0 ? 1 : add);
+        };
         if (elect_one()) {
-          const uint64_t a = desc0 + s * (L::kStageBytes / 16), b = a + kWeights * kStageRow / 16;
-          const uint64_t ds = sdesc0 + s * (L::kStageBytes / 16);
-          const int left = p.width - kb * kStageK, steps = left >= kStageK ? 4 : (left + 63) / 64;
+          if (kb < full_stages) {
 #pragma unroll
-          for (int j = 0; j < F::kTiles; ++j)
-            if (j * 4 * kBlock < steps * 64) {
-              scales_to_tmem<1>(sw + 4 * j, ds + j * (kScaleTile / 16));
-              scales_to_tmem<1>(sx + 4 * j, ds + (F::kScaleBytes + j * kScaleTile) / 16);
-            }
+            for (int j = 0; j < F::kTiles; ++j) copy(j);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps)
-              umma_fp4<1, kBlock>(tmem + buf * kBN, a + 2 * k, b + 2 * k, kIdesc | F::half(k), sw + F::col(k),
-                                  sx + F::col(k), kb > kb0 || k > 0);
+            for (int k = 0; k < 4; ++k) multiply(k);
+          } else {
+            for (int j = 0; j * 4 * kBlock < last_steps * 64; ++j) copy(j);
+            for (int k = 0; k < last_steps; ++k) multiply(k);
+          }
           umma_commit(&bar->empty[s]);
           if (kb + 1 == kb1) umma_commit(&bar->tfull[buf]);
         }
@@ -476,7 +446,7 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
       uint32_t s = 0, phase = 1, it = 0;
       const CompactScales<kBlock> scales(p.scale, p.width, (int64_t)p.experts * p.rows);
       for (int t = t0; t < tiles && ok; t += step) {
-        const int r0 = first_row(p.plan.table[t / p.tiles], t % p.tiles);
+        const int r0 = first_row(segment_of(t / p.tiles).x, t % p.tiles);
         for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
           if ((it & (active - 1)) == (uint32_t)mine) {
             uint32_t v[4][F::kTiles];
@@ -503,10 +473,23 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
     uint32_t buf = 0, tphase = 0, round = 0;
     for (int t = t0; t < tiles && ok; t += step) {
       const int tile = t % p.tiles, segment = t / p.tiles;
-      const int4 seg = p.plan.table[segment];
+      const int4 seg = segment_of(segment);
       const float factor = kBlock == 16 ? __fdiv_rn(p.amax[p.amax_per_expert ? seg.x : 0], 2688.0f) : 1.0f;
       // this CTA's tokens of the segment, all or its share
       const int first = split == 1 ? 0 : rank * own, mine = max(0, min(split == 1 ? kTok : own, seg.z - first));
+      // what lane n needs to know of token first + n, ahead of the sums
+      float unit = 0.0f, more = 0.0f;  // of its terms; down: its gate, up: the unit of its hidden row's terms
+      int slot = 0;
+      if (lane < mine) {
+        const int row = seg.y + first + lane;
+        unit = __fmul_rn(p.in.unit[row], factor);
+        if constexpr (kDown) {
+          slot = p.plan.slot_of_row[row];
+          more = p.gates[slot];
+        } else {
+          more = p.out.unit[row];
+        }
+      }
       ok = mbar_wait(&bar->tfull[buf], tphase);
       if (ok && split > 1) ok = mbar_wait_cluster(&bar->taken, (round & 1) ^ 1, p.status);
       if (!(ok = together(ok))) break;
@@ -534,34 +517,31 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
           }
         }
       }
-      tcgen05_before_sync();
+      tcgen05_before_sync();  // everything is read
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->tempty[buf]);
-      if (++buf == L::kBuffers) {
-        buf = 0;
-        tphase ^= 1;
-      }
       if (split > 1) {
-        ok = mbar_wait_cluster(&bar->got, round & 1, p.status);
-        if (!(ok = together(ok))) break;
+        ok = together(mbar_wait_cluster(&bar->got, round & 1, p.status));
+        if (!ok) break;
         for (int n = 0; n < mine; ++n) {
           float sum = 0.0f;
           for (int i = 0; i < split; ++i) sum = __fadd_rn(sum, shares[(i * own + n) * kWeights + r]);
           results[n * kWeights + r] = sum;
         }
         __syncwarp();
-        if (t + step < tiles && lane < split) mbar_arrive_cluster_release(map_to_cta(smem_u32(&bar->taken), lane));
+        if (t + step < tiles && lane < split)
+          mbar_arrive_cluster_release(map_to_cta(smem_u32(&bar->taken), lane));
         ++round;
       }
       // results[n]: the sums of token first + n of the segment
       if constexpr (kDown) {
         const int o = kWeights * tile + r;
-        if (o < p.rows)
-          for (int n = 0; n < mine; ++n) {
-            const int row = seg.y + first + n, slot = p.plan.slot_of_row[row];
-            const float v = __fmul_rn(__fmul_rn(results[n * kWeights + r], p.in.unit[row]), factor);
-            p.parts[(int64_t)slot * p.rows + o] = __fmul_rn(v, p.gates[slot]);
-          }
+        for (int n = 0; n < mine; ++n) {
+          const float v = __fmul_rn(results[n * kWeights + r], __shfl_sync(0xFFFFFFFFu, unit, n));
+          const float weighted = __fmul_rn(v, __shfl_sync(0xFFFFFFFFu, more, n));
+          const int64_t to = (int64_t)__shfl_sync(0xFFFFFFFFu, slot, n) * p.rows + o;
+          if (o < p.rows) p.parts[to] = weighted;
+        }
       } else {
         together(true);  // gate and up sums come from different warps
         // 16 lanes take a token's 64 hidden values, four each
@@ -569,8 +549,8 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
         const int64_t out_tiles = (p.inner + 4 * kBlock - 1) / (4 * kBlock);
         for (int n = 2 * w + (lane >> 4); n - (lane >> 4) < mine; n += 2 * kOutWarps) {
           const bool there = n < mine;
-          const int row = seg.y + first + (there ? n : 0);
-          const float unit = __fmul_rn(p.in.unit[row], factor);
+          const int row = seg.y + first + n;
+          const float x_unit = __shfl_sync(0xFFFFFFFFu, unit, n & 31), h_unit = __shfl_sync(0xFFFFFFFFu, more, n & 31);
           float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           if (there && f < p.inner) {
             const float4 a = *reinterpret_cast<const float4*>(results + n * kWeights + 4 * (lane & 15));
@@ -578,18 +558,22 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
             const float gate[4] = {a.x, a.y, a.z, a.w}, up[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float z = __fmul_rn(gate[i], unit);
-              v[i] = __fmul_rn(__fdiv_rn(z, __fadd_rn(1.0f, expf(-z))), __fmul_rn(up[i], unit));
+              const float z = __fmul_rn(gate[i], x_unit);
+              v[i] = __fmul_rn(__fdiv_rn(z, __fadd_rn(1.0f, expf(-z))), __fmul_rn(up[i], x_unit));
             }
           }
           uint32_t codes[kTerms], scales[2];
-          to_terms<kBlock>(v, p.out.unit[row], codes, scales);
+          to_terms<kBlock>(v, there ? h_unit : 1.0f, codes, scales);
           if (!there) continue;
           if (f < p.inner)
             store_codes<kBlock>(p.out.codes + (int64_t)row * kTerms * (p.inner / 2), p.inner / 2, f, codes);
           store_scales<kBlock>(p.out.scales + segment * out_tiles * kScaleTile, (first + n) * kTerms, f, lane, scales);
         }
         together(true);  // the results may be overwritten
+      }
+      if (++buf == L::kBuffers) {
+        buf = 0;
+        tphase ^= 1;
       }
     }
     if (!ok) report_timeout(p.status);
@@ -703,7 +687,7 @@ cudaError_t launch_product(const Fp4Side& weights, MlpKernelArgs p, int64_t slot
   for (int s = 8; s >= 2 && split == 1; s /= 2)
     if (tiles * s <= 2 * ctx.num_sms && stages_k >= 2 * s) split = s;
   constexpr int kPerCta = 113 * 1024;  // two CTAs share an SM's 228 KB, 1 KB of it reserved for each
-  const int rest = 1024 + L::rest(split);
+  const int rest = 1024 + L::rest(split, p.slots, p.experts);
   int stages = (kPerCta - rest) / L::kStageBytes;
   if (stages > kMaxStages) stages = kMaxStages;
   const int smem = rest + stages * L::kStageBytes;
@@ -726,6 +710,8 @@ cudaError_t launch_products(const ExpertMlpArgs& a, const Workspace& ws, const L
   p.gates = a.gates;
   p.parts = ws.parts;
   p.inner = (int)a.inner;
+  p.ids = a.ids;
+  p.slots = (int)slots;
   MlpKernelArgs up = p, down = p;
   up.rows = (int)(2 * a.inner), up.width = (int)a.hidden, up.in = ws.x, up.out = ws.h;
   down.rows = (int)a.hidden, down.width = (int)a.inner, down.in = ws.h;
@@ -752,7 +738,7 @@ cudaError_t launch_layer(const ExpertMlpArgs& a, const LaunchCtx& ctx) {
   void* args[] = {&p};
   const unsigned parts = (unsigned)((a.hidden + kPrepPart - 1) / kPrepPart);
   cudaError_t e = launch_dependent(reinterpret_cast<const void*>(prepare_kernel<kBlock>), dim3((unsigned)a.tokens * parts),
-                                   dim3(kPrepThreads), 4 * (p.slots + 3 * p.experts), ctx.stream, args);
+                                   dim3(kPrepThreads), 4 * (p.slots + 2 * p.experts + 2), ctx.stream, args);
   if (e != cudaSuccess) return e;
   e = p.tok == 2 ? launch_products<2, kBlock>(a, ws, ctx)
       : p.tok == 8 ? launch_products<8, kBlock>(a, ws, ctx)
@@ -771,11 +757,15 @@ cudaError_t launch_layer(const ExpertMlpArgs& a, const LaunchCtx& ctx) {
 }  // namespace
 }  // namespace fp4
 
-size_t expert_mlp_workspace(const ExpertMlpArgs& a) { return fp4::cut(a).bytes; }
+size_t expert_mlp_workspace(const ExpertMlpArgs& a) {
+  const size_t any = fp4::cut(a).bytes, few = fp4::few_tokens_workspace(a);
+  return any > few ? any : few;
+}
 
 cudaError_t launch_expert_mlp(const ExpertMlpArgs& a, const LaunchCtx& ctx) {
   if (a.tokens == 0 || a.hidden == 0) return cudaSuccess;
   if (a.inner == 0) return cudaMemsetAsync(a.y, 0, (size_t)a.tokens * a.hidden * 2, ctx.stream);
+  if (fp4::few_tokens(a, ctx)) return fp4::launch_few_tokens(a, ctx);
   return a.block == 16 ? fp4::launch_layer<16>(a, ctx) : fp4::launch_layer<32>(a, ctx);
 }
 

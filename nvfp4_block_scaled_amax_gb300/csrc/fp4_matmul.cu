@@ -106,6 +106,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
                 column * 256 + (i < uncut ? 0 : 128 * ((i - uncut) & 1)), i >= uncut};
   };
   const int nkb = (int)((p.K + kStageK - 1) / kStageK);
+  const int full_stages = (int)(p.K / kStageK), last_steps = (int)((p.K % kStageK + 63) / 64);  // of 64 elements
   bool ok = true;
 
   if (w == 0) {
@@ -167,24 +168,28 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           break;
         }
         tcgen05_after_sync();
+        const uint64_t a = desc0 + s * (L::kStageBytes / 16), b = a + kStageA / 16;
+        const uint64_t ds = sdesc0 + s * (L::kStageBytes / 16);
+        const uint32_t add = kb > 0;
+        // A step's scales: four columns of A's, eight of B's (its second 128 rows behind the first).
+        auto copy = [&](int j) {
+          scales_to_tmem<2>(sa + 4 * j, ds + j * (kScaleTile / 16));
+          scales_to_tmem<2>(sb + 8 * j, ds + (L::kScales + j * kScaleTile) / 16);
+          scales_to_tmem<2>(sb + 8 * j + 4, ds + (2 * L::kScales + j * kScaleTile) / 16);
+        };
+        auto multiply = [&](int k) {
+          umma_fp4<2, kBlock>(d, a + 2 * k, b + 2 * k, idesc | F::half(k), sa + F::col(k), sb + 2 * F::col(k), k > 0 ? 1 : add);
+        };
         if (elect_one()) {
-          const uint64_t a = desc0 + s * (L::kStageBytes / 16), b = a + kStageA / 16;
-          const uint64_t ds = sdesc0 + s * (L::kStageBytes / 16);
-          const int64_t left = p.K - (int64_t)kb * kStageK;
-          const int steps = left >= kStageK ? 4 : (int)((left + 63) / 64);
-          // A step's scales: four columns of A's, eight of B's (its second 128 rows behind the first).
+          if (kb < full_stages) {
 #pragma unroll
-          for (int j = 0; j < F::kTiles; ++j)
-            if (j * 4 * kBlock < steps * 64) {
-              scales_to_tmem<2>(sa + 4 * j, ds + j * (kScaleTile / 16));
-              scales_to_tmem<2>(sb + 8 * j, ds + (L::kScales + j * kScaleTile) / 16);
-              scales_to_tmem<2>(sb + 8 * j + 4, ds + (2 * L::kScales + j * kScaleTile) / 16);
-            }
+            for (int j = 0; j < F::kTiles; ++j) copy(j);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps)
-              umma_fp4<2, kBlock>(d, a + 2 * k, b + 2 * k, idesc | F::half(k), sa + F::col(k), sb + 2 * F::col(k),
-                                  kb > 0 || k > 0);
+            for (int k = 0; k < 4; ++k) multiply(k);
+          } else {
+            for (int j = 0; j * 4 * kBlock < last_steps * 64; ++j) copy(j);
+            for (int k = 0; k < last_steps; ++k) multiply(k);
+          }
           if (kb + 1 == nkb) umma_commit_pair(&bar->tfull[buf]);
           umma_commit_pair(&bar->empty[s]);
         }

@@ -91,6 +91,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   const int lg_split = __ffs(split) - 1;
   const int t0 = blockIdx.x >> lg_split, step = gridDim.x >> lg_split, tiles = p.tiles_a * p.tiles_b;
   const int nkb = (int)((p.K + kStageK - 1) / kStageK);
+  const int full_stages = (int)(p.K / kStageK), last_steps = (int)((p.K % kStageK + 63) / 64);  // of 64 elements
   const int kb0 = (int)(((int64_t)nkb * rank) >> lg_split), kb1 = (int)(((int64_t)nkb * (rank + 1)) >> lg_split);
   bool ok = true;
 
@@ -148,22 +149,27 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           break;
         }
         tcgen05_after_sync();
+        const uint64_t b = desc0 + s * (L::kStageBytes / 16), a = b + kWeights * kStageRow / 16;
+        const uint64_t ds = sdesc0 + s * (L::kStageBytes / 16);
+        const uint32_t add = kb > kb0;
+        auto copy = [&](int j) {
+          scales_to_tmem<1>(sb + 4 * j, ds + j * (kScaleTile / 16));
+          scales_to_tmem<1>(sa + 4 * j, ds + (F::kScaleBytes + j * kScaleTile) / 16);
+        };
+        auto multiply = [&](int k) {
+          umma_fp4<1, kBlock>(tmem + buf * kBN, b + 2 * k, a + 2 * k, kIdesc | F::half(k), sb + F::col(k),
+                              sa + shift + F::col(k), k > 0 ? 1 : add);
+        };
         if (elect_one()) {
-          const uint64_t b = desc0 + s * (L::kStageBytes / 16), a = b + kWeights * kStageRow / 16;
-          const uint64_t ds = sdesc0 + s * (L::kStageBytes / 16);
-          const int64_t left = p.K - (int64_t)kb * kStageK;
-          const int steps = left >= kStageK ? 4 : (int)((left + 63) / 64);
+          if (kb < full_stages) {
 #pragma unroll
-          for (int j = 0; j < F::kTiles; ++j)
-            if (j * 4 * kBlock < steps * 64) {
-              scales_to_tmem<1>(sb + 4 * j, ds + j * (kScaleTile / 16));
-              scales_to_tmem<1>(sa + 4 * j, ds + (F::kScaleBytes + j * kScaleTile) / 16);
-            }
+            for (int j = 0; j < F::kTiles; ++j) copy(j);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps)
-              umma_fp4<1, kBlock>(tmem + buf * kBN, b + 2 * k, a + 2 * k, kIdesc | F::half(k), sb + F::col(k),
-                                  sa + shift + F::col(k), kb > kb0 || k > 0);
+            for (int k = 0; k < 4; ++k) multiply(k);
+          } else {
+            for (int j = 0; j * 4 * kBlock < last_steps * 64; ++j) copy(j);
+            for (int k = 0; k < last_steps; ++k) multiply(k);
+          }
           umma_commit(&bar->empty[s]);
           if (kb + 1 == kb1) umma_commit(&bar->tfull[buf]);
         }

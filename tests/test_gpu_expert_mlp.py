@@ -88,7 +88,9 @@ def check(T, topk, E, H, F, block, seed=0, ids=None):
                                           (9, 4, 6, 1184, 160), (16, 3, 5, 96, 1056), (17, 2, 3, 288, 256),
                                           (40, 2, 3, 256, 192), (64, 4, 32, 128, 64), (5, 8, 200, 64, 32),
                                           (1, 2, 4, 4096, 2048), (100, 1, 1, 64, 64),
-                                          (13, 4, 16, 2720, 1184), (40, 2, 5, 1056, 5120)])
+                                          (13, 4, 16, 2720, 1184), (40, 2, 5, 1056, 5120), (2, 4, 6, 1184, 1056),
+                                          (2, 1, 3, 10240, 64), (1, 8, 8, 320, 4096), (2, 2, 2, 64, 10240),
+                                          (2, 4, 40, 2048, 512), (1, 9, 20, 256, 96)])
 def test_layer(T, topk, E, H, F, block):
     check(T, topk, E, H, F, block, seed=T + H)
 
@@ -102,6 +104,11 @@ def test_ids(block):
     check(30, 2, 4, 128, 96, block, ids=torch.full((30, 2), 1, dtype=torch.int32))
     y = check(4, 2, 4, 128, 96, block, ids=torch.full((4, 2), -1, dtype=torch.int32))
     assert bool((y == 0).all())
+    for rows in ([[-1, -1, -1]], [[3, 3, 3]], [[2, 9, -5]], [[-1, -1, 0], [-1, -1, -1]], [[1, 0, 1], [3, 1, 2]],
+                 [[-1, -1, -1], [2, 2, 0]]):
+        y = check(len(rows), 3, 4, 1536, 96, block, ids=torch.tensor(rows, dtype=torch.int32))
+        for t, row in enumerate(rows):
+            assert any(0 <= e < 4 for e in row) or bool((y[t] == 0).all())
 
 
 @pytest.mark.parametrize("block", [16, 32])
