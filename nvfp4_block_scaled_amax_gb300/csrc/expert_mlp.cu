@@ -9,19 +9,21 @@
 // (tcgen05 block_scale), and the activations become 4 bits too: as the sum of
 // kTerms 4-bit operands, each the cast of what the earlier ones left over.
 //
-// Terms.  A term of a block (16 or 32 elements, as the weights') is its
-// E2M1 codes with a scale at which the block's largest remainder is at most 6
-// (NVFP4: the next E4M3 number above a sixth of it) or below 8 (MXFP4: a power
-// of two); a code is off by at most 1, or 2 above 6, so the remainder falls to
-// 3/16 (NVFP4) or 1/4 (MXFP4), and eight terms leave 2^-19 or 2^-16 of the
-// block's largest element, far below the 2^-9 of the BF16 output.  The
-// subtraction is exact in FP32.  Each term is a row of the product beside the
-// others: N = 8 tokens, where few rows leave an MMA's columns empty anyway.
-// E4M3 scales span 17 powers of two; they count in units of their row and term
-// (4^-i for term i), so that a row's small blocks lose nothing until 2^-29 of its
-// largest.  The unit of a row of x comes from its largest element; that of
-// the hidden row, which is cut into terms tile by tile, from a bound:
-// |g|, |u| <= amax sum|x|.  (The sums' own rounding in FP32 is of that order.)
+// Terms.  A block (16 or 32 elements, as the weights') has one scale s, at which
+// its largest element is at most 6 (NVFP4: the next E4M3 number above a sixth of it,
+// MXFP4: the next power of two), and six rows of E2M1 codes, counting in s, s / 4, s /
+// 32, s / 256, ...: a code of the first is off by at most s, which is 4 of the next
+// unit; from then on codes are off by at most half a unit, which is 4 of the next
+// again.  Six terms leave s 2^-15, which is 2^-17.4 (NVFP4) or 2^-16.5 (MXFP4) of the
+// block's largest element, far below the 2^-9 of the BF16 output.  Every step but the
+// choice of codes is exact in FP32, and the rows of a token are added with their
+// ratios after the product.  They are rows beside the others: N = 6 tokens, where
+// few rows leave an MMA's columns empty anyway.
+// E4M3 scales span 17 powers of two; they count in units of their row, so that a
+// row's small blocks lose nothing until 2^-34 of its largest.  The unit of a row of
+// x comes from its largest element; that of the hidden row, which is cut into terms
+// tile by tile, from a bound: |g|, |u| <= amax sum|x|.  (The sums' own rounding in
+// FP32 is of that order.)
 //
 // Four launches: slots sorted by expert and x into terms; gate and up products
 // with SiLU and the hidden rows' terms; down product, weighted by the gates;
@@ -177,17 +179,19 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
     const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + k));
     v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
   }
-  uint32_t codes[kTerms], scales[2];
-  to_terms<kBlock>(v, unit, codes, scales);
+  const int64_t tiles = (p.width + 4 * kBlock - 1) / (4 * kBlock), row_bytes = p.width / 2;
+  uint16_t codes[kTerms];
+  const uint32_t scale = to_terms<kBlock>(v, unit, [&](int i, uint16_t c) { codes[i] = c; });
   if (k >= (p.width + 63) / 64 * 64) return;
-  const int64_t tiles = (p.width + 4 * kBlock - 1) / (4 * kBlock);
   for (int j = 0; j < p.topk; ++j) {
     const int e = ids[token * p.topk + j];
     if (e < 0) continue;
     const int r = row0[e] + place[j], seg = seg0[e] + place[j] / p.tok;
     if (k < p.width)
-      store_codes<kBlock>(p.x_rows.codes + (int64_t)r * kTerms * (p.width / 2), p.width / 2, k, codes);
-    store_scales<kBlock>(p.x_rows.scales + seg * tiles * kScaleTile, place[j] % p.tok * kTerms, k, lane, scales);
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i)
+        *reinterpret_cast<uint16_t*>(p.x_rows.codes + ((int64_t)r * kTerms + i) * row_bytes + k / 2) = codes[i];
+    put_scale<kBlock>(p.x_rows.scales + seg * tiles * kScaleTile, place[j] % p.tok * kTerms, k, scale);
   }
 }
 
@@ -226,12 +230,11 @@ struct Barriers {
 template <int kTok, int kBlock>
 struct Layout {
   using F = Format<kBlock>;
-  static constexpr int kBN = kTok * kTerms;
+  static constexpr int kBN = (kTok * kTerms + 15) / 16 * 16;  // (the last rows of 16: of whichever segment follows)
   static constexpr int kWCodes = kWeights * kStageRow;
   static constexpr int kCodes = kWCodes + kBN * kStageRow;
   static constexpr int kStageBytes = kCodes + 2 * F::kScaleBytes;
-  static constexpr int kBuffers = kBN > 64 ? 1 : 2;
-  static constexpr int kCols = kBuffers * kBN + 2 * F::kCols;
+  static constexpr int kCols = 2 * kBN + 2 * F::kCols;
   static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
   static_assert(kCols <= 256 && kStageBytes % 1024 == 0, "tensor memory of two CTAs; swizzled operands");
   static constexpr int kResultBytes = kTok * kWeights * 4;  // a tile's results
@@ -269,7 +272,7 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
         mbar_init(&bar->full[i], 2);
         mbar_init(&bar->empty[i], 1);
       }
-      for (int i = 0; i < L::kBuffers; ++i) {
+      for (int i = 0; i < 2; ++i) {
         mbar_init(&bar->tfull[i], 1);
         mbar_init(&bar->tempty[i], kOutWarps);
       }
@@ -391,7 +394,7 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
     constexpr uint32_t kIdesc = F::idesc(kWeights, kBN);
     const uint64_t desc0 = operand_desc(smem_u32(smem));
     const uint64_t sdesc0 = scale_desc(smem_u32(smem) + L::kCodes);
-    const uint32_t sw = tmem + L::kBuffers * kBN, sx = sw + F::kCols;
+    const uint32_t sw = tmem + 2 * kBN, sx = sw + F::kCols;
     uint32_t s = 0, phase = 0, buf = 0, tphase = 1;
     for (int t = t0; t < tiles && ok; t += step) {
       if (!mbar_wait(&bar->tempty[buf], tphase)) {
@@ -434,10 +437,8 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
           phase ^= 1;
         }
       }
-      if (++buf == L::kBuffers) {
-        buf = 0;
-        tphase ^= 1;
-      }
+      buf ^= 1;
+      tphase ^= buf ^ 1;
     }
     if (!ok) report_timeout(p.status);
   } else if (w > kOutWarps + 1) {
@@ -502,10 +503,7 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
         tmem_read(lane_base + buf * kBN + n * kTerms, v);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float sum = __uint_as_float(v[8 * h + kTerms - 1]);
-#pragma unroll
-          for (int i = kTerms - 2; i >= 0; --i)
-            sum = __fmaf_rn(sum, kBlock == 16 ? 0.25f : 1.0f, __uint_as_float(v[8 * h + i]));
+          const float sum = add_terms(v + kTerms * h);
           const int token = n + h;
           if (token >= seg.z) break;
           if (split == 1) {
@@ -562,19 +560,17 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
               v[i] = __fmul_rn(__fdiv_rn(z, __fadd_rn(1.0f, expf(-z))), __fmul_rn(up[i], x_unit));
             }
           }
-          uint32_t codes[kTerms], scales[2];
-          to_terms<kBlock>(v, there ? h_unit : 1.0f, codes, scales);
-          if (!there) continue;
-          if (f < p.inner)
-            store_codes<kBlock>(p.out.codes + (int64_t)row * kTerms * (p.inner / 2), p.inner / 2, f, codes);
-          store_scales<kBlock>(p.out.scales + segment * out_tiles * kScaleTile, (first + n) * kTerms, f, lane, scales);
+          uint8_t* codes_at = p.out.codes + (int64_t)row * kTerms * (p.inner / 2) + f / 2;
+          const uint32_t scale = to_terms<kBlock>(v, there ? h_unit : 1.0f, [&](int i, uint16_t codes) {
+            if (there && f < p.inner) *reinterpret_cast<uint16_t*>(codes_at + (int64_t)i * (p.inner / 2)) = codes;
+          });
+          if (there)
+            put_scale<kBlock>(p.out.scales + segment * out_tiles * kScaleTile, (first + n) * kTerms, f, scale);
         }
         together(true);  // the results may be overwritten
       }
-      if (++buf == L::kBuffers) {
-        buf = 0;
-        tphase ^= 1;
-      }
+      buf ^= 1;
+      tphase ^= buf ^ 1;
     }
     if (!ok) report_timeout(p.status);
   }

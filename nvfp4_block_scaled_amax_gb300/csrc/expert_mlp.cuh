@@ -9,47 +9,59 @@
 namespace nvfp4 {
 namespace fp4 {
 
-constexpr int kTerms = 8;
+constexpr int kTerms = 6;
 
 // ---------------------------------------------------------------------------
 // Terms
 // ---------------------------------------------------------------------------
-// Four elements of a block into terms: v is left with the remainders.  The
-// block lies in 4 (NVFP4) or 8 (MXFP4) neighbouring lanes.  codes[i]: four codes
-// of term i; scales: byte i the scale of term i.
-template <int kBlock>
-__device__ __forceinline__ void to_terms(float (&v)[4], float unit, uint32_t (&codes)[kTerms], uint32_t (&scales)[2]) {
-  scales[0] = scales[1] = 0;
-  float inv_unit6 = __fdiv_rn(1.0f / 6.0f, unit);
+// What a scale of 1 stands for in term i, of what it does in the first.
+__device__ __forceinline__ constexpr float term_ratio(int i) { return i == 0 ? 1.0f : 1.0f / (float)(4 << (3 * (i - 1))); }
+// The sum of a row's terms, the smallest first.
+__device__ __forceinline__ float add_terms(const uint32_t* v) {
+  float sum = __uint_as_float(v[kTerms - 1]);
+#pragma unroll
+  for (int i = kTerms - 2; i >= 0; --i) sum = __fmaf_rn(sum, i == 0 ? 0.25f : 0.125f, __uint_as_float(v[i]));
+  return sum;
+}
+
+// Four elements of a block into terms: put(i, codes) gets the four codes of each
+// term i; the block's scale byte is returned.  The block lies in 4 (NVFP4) or 8
+// (MXFP4) neighbouring lanes.
+template <int kBlock, class Put>
+__device__ __forceinline__ uint32_t to_terms(float (&v)[4], float unit, Put&& put) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[j])));
+#pragma unroll
+  for (int d = 1; d < kBlock / 4; d <<= 1)
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(__shfl_xor_sync(0xFFFFFFFFu, m, d)));
+  uint32_t byte;
+  float value, inv;  // the scale, and its reciprocal (any rounding: what it leaves goes to the next term)
+  if constexpr (kBlock == 16) {
+    // the next E4M3 number not below a sixth of the largest; its value through FP16, which holds them all
+    const float q = __fmul_rn(m, __fdividef(1.0f / 6.0f, unit));
+    byte = e4m3_rn_satfinite(q);
+    auto decoded = [](uint32_t c) {
+      float f;
+      asm("{\n .reg .b32 h;\n .reg .b16 lo, hi;\n cvt.rn.f16x2.e4m3x2 h, %1;\n mov.b32 {lo, hi}, h;\n cvt.f32.f16 %0, lo;\n}"
+          : "=f"(f)
+          : "h"((uint16_t)c));
+      return f;
+    };
+    byte += byte < 126u && decoded(byte) < q;
+    value = __fmul_rn(decoded(byte), unit);
+    inv = byte == 0 ? 0.0f : __fdividef(1.0f, value);
+    if (!(q <= 449.0f)) byte = 127u, inv = 0.0f;  // not finite: the whole row becomes NaN
+  } else {
+    // the next power of two not below a sixth of the largest (and 2^-107, so that no term's leaves FP32's range)
+    const uint32_t bits = __float_as_uint(m), e = (bits >> 23) + ((bits & 0x7FFFFFu) > 0x400000u);
+    byte = e < 22u ? 20u : e - 2u;
+    value = __uint_as_float(byte << 23);
+    inv = __uint_as_float((254u - byte) << 23);
+    if (!(m <= kFltMax)) byte = 255u, inv = 0.0f;
+  }
 #pragma unroll
   for (int i = 0; i < kTerms; ++i) {
-    float m = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = fabsf(v[j]);
-      m = a >= m ? a : a != a ? __int_as_float(0x7F800000) : m;  // (a NaN counts as an infinity)
-    }
-#pragma unroll
-    for (int d = 1; d < kBlock / 4; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    uint32_t byte;
-    float value, inv;  // the scale, and its reciprocal (any rounding: what it leaves goes to the next term)
-    if constexpr (kBlock == 16) {
-      const float q = __fmul_rn(m, inv_unit6);
-      byte = e4m3_rn_satfinite(q);
-      if (byte < 126u && e4m3_decode(byte) < q) ++byte;
-      value = __fmul_rn(e4m3_decode(byte), unit);
-      inv = byte == 0 ? 0.0f : __fdividef(1.0f, value);
-      unit = __fmul_rn(unit, 0.25f);
-      inv_unit6 = __fmul_rn(inv_unit6, 4.0f);
-      if (!(q <= 449.0f)) byte = 127u;  // not finite: the whole row becomes NaN
-    } else {
-      const uint32_t e = __float_as_uint(m) >> 23;
-      byte = e < 2u ? 0u : e - 2u;
-      value = __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
-      inv = __uint_as_float((254u - byte) << 23);
-      if (!(m <= kFltMax)) byte = 255u;
-    }
-    if (!(m <= kFltMax)) inv = 0.0f;
     uint16_t h;
     asm("{\n .reg .b8 lo, hi;\n"
         " cvt.rn.satfinite.e2m1x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 hi, %4, %3;\n"
@@ -57,41 +69,31 @@ __device__ __forceinline__ void to_terms(float (&v)[4], float unit, uint32_t (&c
         : "=h"(h)
         : "f"(__fmul_rn(v[0], inv)), "f"(__fmul_rn(v[1], inv)), "f"(__fmul_rn(v[2], inv)), "f"(__fmul_rn(v[3], inv)));
     if (inv == 0.0f) h = 0;  // (an infinity times 0)
-    codes[i] = h;
-    scales[i >> 2] |= byte << (8 * (i & 3));
-    uint32_t f01, f23;
-    asm("{\n .reg .b8 lo, hi;\n mov.b16 {lo, hi}, %2;\n cvt.rn.f16x2.e2m1x2 %0, lo;\n cvt.rn.f16x2.e2m1x2 %1, hi;\n}"
-        : "=r"(f01), "=r"(f23)
-        : "h"(h));
+    put(i, h);
     float c[4];
-    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}"
-        : "=f"(c[0]), "=f"(c[1])
-        : "r"(f01));
-    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}"
-        : "=f"(c[2]), "=f"(c[3])
-        : "r"(f23));
+    asm("{\n .reg .b8 lo, hi;\n .reg .b32 p, q;\n .reg .b16 a, b, c, d;\n mov.b16 {lo, hi}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 p, lo;\n cvt.rn.f16x2.e2m1x2 q, hi;\n mov.b32 {a, b}, p;\n mov.b32 {c, d}, q;\n"
+        " cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n cvt.f32.f16 %2, c;\n cvt.f32.f16 %3, d;\n}"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "h"(h));
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = __fmaf_rn(-c[j], value, v[j]);
+    value = __fmul_rn(value, i == 0 ? 0.25f : 0.125f);
+    inv = __fmul_rn(inv, i == 0 ? 4.0f : 8.0f);
   }
+  return byte;
 }
 
-// Their places: four codes of each term in rows of `pitch` bytes, and the
-// lane's share of the block's scales (row n0 + i of a segment is term i).
+// The scale of the block of this element, at rows n0 .. of a segment's tiles (one
+// for each term), by the lanes of the block.
 template <int kBlock>
-__device__ __forceinline__ void store_codes(uint8_t* row, int64_t pitch, int64_t element, const uint32_t (&codes)[kTerms]) {
-#pragma unroll
-  for (int i = 0; i < kTerms; ++i)
-    *reinterpret_cast<uint16_t*>(row + i * pitch + element / 2) = (uint16_t)codes[i];
-}
-template <int kBlock>
-__device__ __forceinline__ void store_scales(uint8_t* segment, int n0, int64_t element, int lane,
-                                             const uint32_t (&scales)[2]) {
-  constexpr int kLanes = kBlock / 4, kEach = kTerms / kLanes;
+__device__ __forceinline__ void put_scale(uint8_t* segment, int n0, int64_t element, uint32_t byte) {
+  constexpr int kLanes = kBlock / 4;
   uint8_t* tile = segment + element / (4 * kBlock) * kScaleTile + element % (4 * kBlock) / kBlock;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int term = (lane % kLanes) * kEach + i, n = n0 + term;
-    tile[n % 32 * 16 + n / 32 * 4] = (uint8_t)(scales[term >> 2] >> (8 * (term & 3)));
+  for (int i = 0; i < kTerms; i += kLanes) {
+    const int term = i + (threadIdx.x & (kLanes - 1)), n = n0 + term;
+    if (term < kTerms) tile[n % 32 * 16 + n / 32 * 4] = (uint8_t)byte;
   }
 }
 // Power of two at which scales up to 448 reach a sixth of `largest`.

@@ -14,7 +14,8 @@ namespace nvfp4 {
 namespace fp4 {
 namespace {
 
-constexpr int kTok = 2, kBN = kTok * kTerms;
+constexpr int kTok = 2, kBN = 16;
+static_assert(kTok * kTerms <= kBN, "rows of the terms");
 constexpr int kMaxChoices = 8;  // and experts at most
 constexpr int kOutWarps = 4;
 constexpr int kThreads = 32 * (kOutWarps + 2 + kScaleWarps);
@@ -39,32 +40,35 @@ struct FewArgs {
   unsigned* status;
 };
 
+// The experts that were chosen, in the order of their first choice.
+struct Chosen {
+  int n;
+  uint32_t by;  // bit kTok i + token: the token chose expert i
+  int expert[kMaxChoices];
+};
+
 struct Barriers {
   uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
   uint64_t terms;        // up: x's terms are there
   uint64_t got, taken;   // the cluster's partial results
   uint32_t tmem;
   float largest[kTermWarps][kTok], sums[kTermWarps][kTok];
+  Chosen chosen;
 };
 
-// The experts that were chosen, in the order of their first choice.
-struct Chosen {
-  int n;
-  int expert[kMaxChoices];
-  uint32_t by;  // bit kTok i + token: the token chose expert i
-
-  __device__ __forceinline__ Chosen(const FewArgs& p) {
-    n = 0, by = 0;
-    for (int s = 0; s < p.tokens * p.topk; ++s) {
-      const int e = p.ids[s];
-      if (e < 0 || e >= p.experts) continue;
-      int i = 0;
-      while (i < n && expert[i] != e) ++i;
-      if (i == n) expert[n++] = e;
-      by |= 1u << (kTok * i + s / p.topk);
-    }
-  }
-};
+// One warp finds them: lane s has choice s.
+__device__ __forceinline__ void find_chosen(const FewArgs& p, Chosen& to) {
+  const int lane = threadIdx.x & 31;
+  int e = lane < p.tokens * p.topk ? p.ids[lane] : -1;
+  if (e >= p.experts) e = -1;
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+  const int leader = __ffs(same) - 1;
+  const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, e >= 0 && lane == leader);
+  const int i = __popc(firsts & ((1u << leader) - 1));
+  const uint32_t by = __reduce_or_sync(0xFFFFFFFFu, e >= 0 ? 1u << (kTok * i + lane / p.topk) : 0u);
+  if (e >= 0 && lane == leader) to.expert[i] = e;
+  if (lane == 0) to.n = __popc(firsts), to.by = by;
+}
 
 template <bool kDown, int kBlock>
 struct Layout {
@@ -82,6 +86,32 @@ struct Layout {
     return resident * kXBytes + kTok * kWeights * 4 + split * kWeights * 4 + (int)sizeof(Barriers);
   }
 };
+
+// x's largest finite element and its sum of magnitudes: warp `me` of kTermWarps, its part.
+__device__ __forceinline__ void look_at_x(const FewArgs& p, int me, Barriers& bar) {
+  const int lane = threadIdx.x & 31;
+  for (int token = 0; token < p.tokens; ++token) {
+    const uint4* row = reinterpret_cast<const uint4*>(p.x + (int64_t)token * p.width);
+    float m = 0.0f, sum = 0.0f;
+#pragma unroll 2
+    for (int k = 32 * me + lane; k < p.width / 8; k += 32 * kTermWarps) {
+      const uint4 u = __ldg(row + k);
+      const float v[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
+                          bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = fabsf(v[i]), b = a <= kFltMax ? a : 0.0f;
+        m = fmaxf(m, b), sum = __fadd_rn(sum, b);
+      }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+      sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, d));
+    }
+    if (lane == 0) bar.largest[me][token] = m, bar.sums[me][token] = sum;
+  }
+}
 
 // ---------------------------------------------------------------------------
 template <bool kDown, int kBlock>
@@ -127,7 +157,9 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     grid_dependency_wait();
     grid_launch_dependents();
   }
-  const Chosen chosen(p);
+  if (w == 0) find_chosen(p, bar->chosen);
+  float sum[kTok] = {0.0f, 0.0f};
+  if (!kDown && w != kOutWarps && w != kOutWarps + 1) look_at_x(p, w < kOutWarps ? w : w - 2, *bar);
   tcgen05_before_sync();
   __syncthreads();
   if (split > 1) cluster_wait();
@@ -139,6 +171,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
   const int full_stages = p.width / kStageK, last_steps = (p.width % kStageK + 63) / 64;  // of 64 elements
   // up: a tile for each chosen expert's 64 gate and 64 up rows, its stages shared by the cluster; down: a
   // tile for 128 rows, the stages of all chosen experts shared
+  const Chosen& chosen = bar->chosen;
   const int n_experts = __shfl_sync(0xFFFFFFFFu, chosen.n, 0);
   const int tiles = kDown ? p.tiles : n_experts * p.tiles, per_tile = kDown ? n_experts * nkb : nkb;
   const int i0 = (per_tile * rank) >> lg_split, i1 = (per_tile * (rank + 1)) >> lg_split;
@@ -146,43 +179,15 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
   bool ok = true;
 
   // x into terms: the CTA's share of the stages, by the warps that neither copy nor multiply.
-  float unit[kTok] = {1.0f, 1.0f}, sum[kTok] = {0.0f, 0.0f};
+  float unit[kTok] = {1.0f, 1.0f};
   auto cut_x = [&](int me) {  // me: 0 .. kTermWarps - 1
-    float m[kTok] = {0.0f, 0.0f};
-    for (int token = 0; token < p.tokens; ++token) {
-      const uint4* row = reinterpret_cast<const uint4*>(p.x + (int64_t)token * p.width);
-#pragma unroll 4
-      for (int k = 32 * me + lane; k < p.width / 8; k += 32 * kTermWarps) {
-        const uint4 u = __ldg(row + k);
-        const float v[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
-                            bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = fabsf(v[i]);
-          const bool finite = a <= kFltMax;
-          const float b = finite ? a : 0.0f;
-          if (token == 0) m[0] = fmaxf(m[0], b), sum[0] = __fadd_rn(sum[0], b);
-          else m[1] = fmaxf(m[1], b), sum[1] = __fadd_rn(sum[1], b);
-        }
-      }
-    }
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
+      float m = bar->largest[0][i];
+      sum[i] = bar->sums[0][i];
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], d));
-        sum[i] = __fadd_rn(sum[i], __shfl_xor_sync(0xFFFFFFFFu, sum[i], d));
-      }
-      if (lane == 0) bar->largest[me][i] = m[i], bar->sums[me][i] = sum[i];
-    }
-    asm volatile("bar.sync 2, %0;" ::"n"(32 * kTermWarps) : "memory");
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      m[i] = bar->largest[0][i], sum[i] = bar->sums[0][i];
-#pragma unroll
-      for (int j = 1; j < kTermWarps; ++j)
-        m[i] = fmaxf(m[i], bar->largest[j][i]), sum[i] = __fadd_rn(sum[i], bar->sums[j][i]);
-      unit[i] = kBlock == 16 ? unit_of(m[i]) : 1.0f;
+      for (int j = 1; j < kTermWarps; ++j) m = fmaxf(m, bar->largest[j][i]), sum[i] = __fadd_rn(sum[i], bar->sums[j][i]);
+      unit[i] = kBlock == 16 ? unit_of(m) : 1.0f;
     }
     // 128 elements of a token at a time, up to the last step of 64 padded with zeros
     const int parts = 2 * (i1 - i0);
@@ -194,16 +199,13 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         const uint2 u = __ldg(reinterpret_cast<const uint2*>(p.x + (int64_t)token * p.width + k));
         v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
       }
-      uint32_t codes[kTerms], scales[2];
-      to_terms<kBlock>(v, token == 0 ? unit[0] : unit[1], codes, scales);
-      const int in_stage = k % kStageK;
+      const int in_stage = k % kStageK, b = in_stage / 2;
       uint8_t* stage = x_terms + (k / kStageK - i0) * L::kXBytes;
-#pragma unroll
-      for (int i = 0; i < kTerms; ++i) {  // (rows of 128 bytes, 16-byte places swizzled by the row)
-        const int n = token * kTerms + i, b = in_stage / 2;
-        *reinterpret_cast<uint16_t*>(stage + n * kStageRow + (((b >> 4) ^ (n & 7)) * 16) + (b & 15)) = (uint16_t)codes[i];
-      }
-      store_scales<kBlock>(stage + L::kXCodes, token * kTerms, in_stage, lane, scales);
+      const uint32_t scale = to_terms<kBlock>(v, token == 0 ? unit[0] : unit[1], [&](int i, uint16_t codes) {
+        const int n = token * kTerms + i;  // (rows of 128 bytes, 16-byte places swizzled by the row)
+        *reinterpret_cast<uint16_t*>(stage + n * kStageRow + (((b >> 4) ^ (n & 7)) * 16) + (b & 15)) = codes;
+      });
+      put_scale<kBlock>(stage + L::kXCodes, token * kTerms, in_stage, scale);
     }
     fence_proxy_async_shared();
     __syncwarp();
@@ -389,11 +391,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         tmem_read(lane_base + buf * L::kDCols + e * kBN, v);
 #pragma unroll
         for (int token = 0; token < kTok; ++token) {
-          // a token's terms added, the smallest first
-          float sums = __uint_as_float(v[kTerms * token + kTerms - 1]);
-#pragma unroll
-          for (int i = kTerms - 2; i >= 0; --i)
-            sums = __fmaf_rn(sums, kBlock == 16 ? 0.25f : 1.0f, __uint_as_float(v[kTerms * token + i]));
+          const float sums = add_terms(v + kTerms * token);
           if constexpr (kDown) {
             const float by = __shfl_sync(0xFFFFFFFFu, weight, kTok * e + token);
             if (chosen.by >> (kTok * e + token) & 1) out[token] = __fadd_rn(out[token], __fmul_rn(sums, by));
@@ -456,15 +454,15 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
               v[i] = __fmul_rn(__fdiv_rn(z, __fadd_rn(1.0f, expf(-z))), __fmul_rn(up[i], x_unit));
             }
           }
-          uint32_t codes[kTerms], scales[2];
-          to_terms<kBlock>(v, h_unit, codes, scales);
-          if (token < end) {
-            if (f < p.inner)
-              store_codes<kBlock>(p.h_codes + (int64_t)(e0 * kBN + token * kTerms) * (p.inner / 2), p.inner / 2, f, codes);
-            const int64_t out_tiles = (p.inner + 4 * kBlock - 1) / (4 * kBlock);
-            store_scales<kBlock>(p.h_scales + e0 * out_tiles * kScaleTile, token * kTerms, f, lane, scales);
-            if (tile == 0 && (lane & 15) == 0) p.h_unit[kTok * e0 + token] = h_unit;
-          }
+          const bool mine = token < end;
+          uint8_t* codes_at = p.h_codes + (int64_t)(e0 * kBN + token * kTerms) * (p.inner / 2) + f / 2;
+          const uint32_t scale = to_terms<kBlock>(v, h_unit, [&](int i, uint16_t codes) {
+            if (mine && f < p.inner) *reinterpret_cast<uint16_t*>(codes_at + i * (p.inner / 2)) = codes;
+          });
+          if (mine)
+            put_scale<kBlock>(p.h_scales + (int64_t)e0 * ((p.inner + 4 * kBlock - 1) / (4 * kBlock)) * kScaleTile,
+                              token * kTerms, f, scale);
+          if (mine && tile == 0 && (lane & 15) == 0) p.h_unit[kTok * e0 + token] = h_unit;
         }
         together(true);  // the results may be overwritten
       }

@@ -33,15 +33,15 @@ def block_max(v, block):
 def reference(x, up, down, ids, gates, block, amax):
     """(y, bound on the error) in 64 bits.
 
-    x enters the products as eight 4-bit terms, each of which leaves 3/16 (NVFP4) or 1/4 (MXFP4) of the largest
-    remainder of its block: 2^-19 or 2^-16 of the block's largest element at last, and for NVFP4 never less than half of
-    the smallest scale, 2^-29 of the row's.  A sum of n products in each of eight columns is off by n U32 of the
-    magnitudes, which the terms at most double (1 + 3/16 + ..., 1 + 1/4 + ...).  The factor, SiLU (derivative below 1.1)
-    and the product cost a handful of roundings; h is cut like x, its NVFP4 unit being taken from 2 (amax sum|x|)^2; then
-    the same again."""
+    x enters the products as six rows of E2M1 codes with one scale s for a block: the first is off by at most s, each
+    later one by half its unit, s / 4 / 8^i, so s 2^-15 is left; s is at most the next E4M3 number above a sixth of the
+    largest element (1/8 more, or the smallest one, 2^-9 of a unit that is at most 2^-10 of the row's largest), or the
+    next power of two (a third of it).  A sum of n products in each of six columns is off by n U32 of the magnitudes,
+    which the terms at most double.  The factor, SiLU (derivative below 1.1) and the product cost a handful of roundings;
+    h is cut like x, its NVFP4 unit being taken from 2 (amax sum|x|)^2; then the same again."""
     T, H = x.shape
     F = down.shape[2]
-    left = 2.0 ** -19 if block == 16 else 2.0 ** -16
+    left = 2.0 ** -15 * (1.125 / 6 if block == 16 else 1 / 3)
     y, bound = torch.zeros(T, H, dtype=torch.float64), torch.zeros(T, H, dtype=torch.float64)
     for t in range(T):
         for j in range(ids.shape[1]):
@@ -49,7 +49,7 @@ def reference(x, up, down, ids, gates, block, amax):
             if not 0 <= e < up.shape[0]:
                 continue
             v = x[t].double()
-            dx = left * block_max(v, block) + (2.0 ** -29 * v.abs().max() if block == 16 else 0.0)
+            dx = left * block_max(v, block) + (2.0 ** -34 * v.abs().max() if block == 16 else 0.0)
             s = up[e] @ v
             ds = up[e].abs() @ (dx + 2 * (H + 8) * U32 * v.abs())
             g, u, dg, du = s[:F], s[F:], ds[:F], ds[F:]
@@ -58,7 +58,7 @@ def reference(x, up, down, ids, gates, block, amax):
             dh = 1.1 * dg * (u.abs() + du) + act.abs() * du + 12 * U32 * h.abs()
             dh = dh + left * block_max(h.abs() + dh, block)
             if block == 16:
-                dh = dh + 2.0 ** -29 * 2 * (float(amax[e]) * float(v.abs().sum())) ** 2
+                dh = dh + 2.0 ** -34 * 2 * (float(amax[e]) * float(v.abs().sum())) ** 2
             w = float(gates[t, j])
             y[t] += w * (down[e] @ h)
             bound[t] += abs(w) * (down[e].abs() @ (dh + 2 * (F + 8) * U32 * h.abs()))
