@@ -251,7 +251,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     for (int i = t0; i < items && ok; i += step) {
       const Item it = at(i);
       if (it.n0 >= p.b.rows) continue;
-      const int rows = (int)min((int64_t)256, p.a.rows - it.m0) - row0;  // that this warp has (32 or more: all)
+      const int rows = (int)min((int64_t)256, p.a.rows - it.m0) - row0;  // that this warp has
       const int cols = (int)min((int64_t)(it.half ? 128 : 256), p.b.rows - it.n0) - 128 * half;
       const float fa = row_factor(p.a, p.a.amax_per_row ? it.m0 + row0 + lane : 0);
       const Factor all = factor(fa, p.b.amax_per_row ? 1.0f : row_factor(p.b, 0));
@@ -270,15 +270,14 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       };
       if (!holds || !work) release();
       const uint32_t src = lane_base + buf * kSecond;
-      const bool by_tma = p.out_map && rows >= 32;
-      // 128 bytes of the rows, from column c of the warp's: what TMA cannot
-      // write (past the last row, rows off 16-byte boundaries) the warp writes itself.
+      // 128 bytes of the rows, from column c of the warp's: by TMA, which leaves out
+      // rows past the last; rows off 16-byte boundaries the warp writes itself.
       auto put = [&](int c, auto&& fill) {
         if (c >= cols) return;
         if (lane == 0) bulk_wait_read_all();
         __syncwarp();
         fill();
-        if (by_tma) {
+        if (p.out_map) {
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
@@ -364,6 +363,19 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   if (w == 1) tmem_dealloc_pair(tmem, 512);
 }
 
+// Which of the two kernels a product runs on.  Up to 32 rows the thin one wins
+// (8 / 24 rows, N 4096, K 4096: 4.9 / 5.4 us against 8.7 / 10.6; N 512, K 512: 2.6 /
+// 3.1 against 4.5 / 6.0).  Above, it does where its tiles are few and long, so that
+// eight CTAs share each (64 rows, N 1024, K 8192: 6.1 against 9.3 us; N 4096, K 4096:
+// 7.3 / 7.3), and else the paired one (64 rows, N 2048, K 2048: 6.4 against 4.9; N 8192, K
+// 8192: 12.1 / 11.9).  Past 64 rows the paired one, within 6 percent, always (96
+// rows, N 512, K 8192: 12.4 against 10.4; N 10240, K 8192: 13.7 / 14.5).  Swept over 8
+// to 1024 rows, N 512 to 10240, K 512 to 8192, in CUDA graphs.
+bool thin_is_faster(const Fp4MatmulArgs& a, const LaunchCtx& ctx) {
+  if (a.a.rows <= 32) return true;
+  return a.a.rows <= kThinRows && a.K >= 4096 && thin_plan(a, ctx).split == 8;
+}
+
 template <int kBlock>
 cudaError_t launch_pair(const Fp4MatmulArgs& a, MatmulKernelArgs p, const LaunchCtx& ctx) {
   using L = Layout<kBlock>;
@@ -406,7 +418,7 @@ cudaError_t launch_fp4_matmul(const Fp4MatmulArgs& a, const LaunchCtx& ctx) {
   p.out = a.out;
   p.out_bf16 = a.out_bf16;
   p.status = ctx.status;
-  if (a.a.rows <= 64) return launch_matmul_thin(a, p, ctx);
+  if (thin_is_faster(a, ctx)) return launch_matmul_thin(a, p, ctx);
   return a.block == 16 ? launch_pair<16>(a, p, ctx) : launch_pair<32>(a, p, ctx);
 }
 

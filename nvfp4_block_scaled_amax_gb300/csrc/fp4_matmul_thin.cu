@@ -2,7 +2,7 @@
 // decoding step, a small matrix).
 //
 // The operands change places: a CTA's tile is 128 rows of B (the weights, on
-// the tensor-memory lanes) by kBN = 16, 32, 64 or 128 rows of A (the columns),
+// the tensor-memory lanes) by kBN = 16, 32 or 64 rows of A (the columns),
 // so that few rows waste little of an MMA and every weight is read once per kBN
 // rows.  The contracted dimension of a tile is split over a cluster of 2, 4
 // or 8 CTAs where there are too few tiles to fill the machine: each CTA sums its
@@ -38,8 +38,8 @@ struct Layout {
   static constexpr int kCodes = (kWeights + kBN) * kStageRow;
   static constexpr int kStageBytes = kCodes + 2 * F::kScaleBytes;  // a multiple of 1024
   static constexpr int kCols = 2 * kBN + 2 * F::kCols;
-  static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static constexpr int kPerSm = kTmemCols > 256 ? 1 : 2;
+  static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
+  static_assert(kCols <= 256, "two CTAs share an SM's tensor memory");
   // Columns a CTA of a cluster owns (of few columns and many CTAs, the last CTAs own none).
   static __host__ __device__ int own(int split) { return split == 1 ? 0 : kBN / split < 4 ? 4 : kBN / split; }
   static __host__ __device__ int share_floats(int split) { return split * own(split) * kWeights; }
@@ -47,7 +47,7 @@ struct Layout {
 };
 
 template <int kBN, int kBlock>
-__global__ void __launch_bounds__(kThreads, (Layout<kBN, kBlock>::kPerSm))
+__global__ void __launch_bounds__(kThreads, 2)
 matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                    const __grid_constant__ MatmulKernelArgs p, int stages, int split) {
   using L = Layout<kBN, kBlock>;
@@ -334,7 +334,7 @@ cudaError_t launch(const Fp4MatmulArgs& a, MatmulKernelArgs p, const ThinPlan& t
   if (e != cudaSuccess) return e;
   e = make_fp8_tensor_map(&bmap, a.b.data, a.b.rows, a.K / 2, kWeights);
   if (e != cudaSuccess) return e;
-  constexpr int kPerCta = L::kPerSm == 2 ? 113 * 1024 : 227 * 1024;  // of an SM's 228 KB 1 KB is reserved for each CTA
+  constexpr int kPerCta = 113 * 1024;  // two CTAs share an SM's 228 KB, 1 KB of it reserved for each
   const int rest = 1024 + L::rest(t.split);
   int stages = (kPerCta - rest) / L::kStageBytes;
   if (stages > kMaxStages) stages = kMaxStages;
@@ -345,7 +345,7 @@ cudaError_t launch(const Fp4MatmulArgs& a, MatmulKernelArgs p, const ThinPlan& t
   if (e != cudaSuccess) return e;
   p.tiles_a = (int)((a.a.rows + kBN - 1) / kBN);
   p.tiles_b = (int)((a.b.rows + kWeights - 1) / kWeights);
-  const int64_t room = L::kPerSm * ctx.num_sms / t.split;
+  const int64_t room = 2 * ctx.num_sms / t.split;
   int split = t.split;
   void* args[] = {&amap, &bmap, &p, &stages, &split};
   return launch_dependent(reinterpret_cast<const void*>(kernel),
@@ -357,22 +357,19 @@ template <int kBlock>
 cudaError_t launch_columns(const Fp4MatmulArgs& a, const MatmulKernelArgs& p, const ThinPlan& t, const LaunchCtx& ctx) {
   if (t.bn == 16) return launch<16, kBlock>(a, p, t, ctx);
   if (t.bn == 32) return launch<32, kBlock>(a, p, t, ctx);
-  if (t.bn == 64) return launch<64, kBlock>(a, p, t, ctx);
-  return launch<128, kBlock>(a, p, t, ctx);
+  return launch<64, kBlock>(a, p, t, ctx);
 }
 
 }  // namespace
 
 ThinPlan thin_plan(const Fp4MatmulArgs& a, const LaunchCtx& ctx) {
   ThinPlan t;
-  // (a swizzled A has 128 rows at least: no tile of 16 rows begins inside 32 of its scales)
-  t.bn = a.a.rows <= 16 ? 16 : a.a.rows <= 32 ? 32 : a.a.rows <= 64 ? 64 : 128;
+  t.bn = a.a.rows <= 16 ? 16 : a.a.rows <= 32 ? 32 : 64;
   t.tiles = (a.a.rows + t.bn - 1) / t.bn * ((a.b.rows + kWeights - 1) / kWeights);
   const int64_t stages = (a.K + kStageK - 1) / kStageK;
   t.split = 1;
-  if (t.bn < 128)
-    for (int s = 8; s >= 2 && t.split == 1; s /= 2)
-      if (t.tiles * s <= 2 * ctx.num_sms && stages >= 2 * s) t.split = s;
+  for (int s = 8; s >= 2 && t.split == 1; s /= 2)
+    if (t.tiles * s <= 2 * ctx.num_sms && stages >= 2 * s) t.split = s;
   return t;
 }
 

@@ -233,7 +233,8 @@ __device__ __forceinline__ float row_factor(const Fp4Side& s, int64_t row) {
   return __fdiv_rn(s.amax[s.amax_per_row ? (row < s.rows ? row : s.rows - 1) : 0], 2688.0f);
 }
 
-// fp4_matmul_thin.cu
+// fp4_matmul_thin.cu: at most kThinRows rows of A
+constexpr int kThinRows = 64;
 struct ThinPlan {
   int bn, split;
   int64_t tiles;
