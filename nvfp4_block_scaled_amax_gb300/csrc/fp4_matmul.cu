@@ -287,19 +287,29 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         } else {
           __syncwarp();
           const int n = min(32, rows);
-          for (int r = 0; r < n; ++r) {
-            uint32_t x;
-            asm volatile("ld.shared.u32 %0, [%1];"
-                         : "=r"(x)
-                         : "r"(box + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4)
-                         : "memory");
-            const int64_t to = (int64_t)(it.m0 + row0 + r) * p.b.rows + it.n0 + 128 * half + c;
+#pragma unroll 1
+          for (int r0 = 0; r0 < n; r0 += 8) {  // eight rows read, then written
+            uint32_t x[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+              asm volatile("ld.shared.u32 %0, [%1];"
+                           : "=r"(x[r])
+                           : "r"(box + (r0 + r) * 128 + (((lane >> 2) ^ r) * 16) + (lane & 3) * 4));
+            const int64_t to = (int64_t)(it.m0 + row0 + r0) * p.b.rows + it.n0 + 128 * half + c;
             if (p.out_bf16) {
               uint16_t* dst = static_cast<uint16_t*>(p.out) + to + 2 * lane;
-              if (c + 2 * lane < cols) dst[0] = (uint16_t)x;
-              if (c + 2 * lane + 1 < cols) dst[1] = (uint16_t)(x >> 16);
-            } else if (c + lane < cols) {
-              static_cast<uint32_t*>(p.out)[to + lane] = x;
+              const bool lo = c + 2 * lane < cols, hi = c + 2 * lane + 1 < cols;
+#pragma unroll
+              for (int r = 0; r < 8; ++r, dst += p.b.rows) {
+                if (lo && r0 + r < n) dst[0] = (uint16_t)x[r];
+                if (hi && r0 + r < n) dst[1] = (uint16_t)(x[r] >> 16);
+              }
+            } else {
+              uint32_t* dst = static_cast<uint32_t*>(p.out) + to + lane;
+              const bool there = c + lane < cols;
+#pragma unroll
+              for (int r = 0; r < 8; ++r, dst += p.b.rows)
+                if (there && r0 + r < n) *dst = x[r];
             }
           }
           __syncwarp();
