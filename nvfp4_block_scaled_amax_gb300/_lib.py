@@ -105,11 +105,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.nvfp4_fp8_matmul_grouped_wgrad.argtypes = [vp, vp, vp, vp, i64, i64, i64, c_int, vp, vp, c_int, vp]
         L.nvfp4_mxfp4_quantize.argtypes = [vp, c_int, i64, i64, vp, vp, vp, vp, uint, vp]
         L.nvfp4_mxfp4_dequantize.argtypes = [vp, vp, i64, i64, uint, vp, c_int, vp]
-        L.nvfp4_fp4_matmul.argtypes = [ctypes.POINTER(Operand), ctypes.POINTER(Operand), c_int, i64, i64, i64, vp,
+        L.nvfp4_fp4_matmul.argtypes = [vp, vp, c_int, i64, i64, i64, vp,
                                        c_int, vp]
         L.nvfp4_expert_mlp_workspace.argtypes = [i64, c_int, c_int, i64, i64, c_int, ctypes.POINTER(size)]
-        L.nvfp4_expert_mlp.argtypes = [vp, i64, i64, i64, ctypes.POINTER(Operand), ctypes.POINTER(Operand), c_int, vp,
-                                       vp, c_int, c_int, vp, size, vp, vp]
+        L.nvfp4_expert_mlp.argtypes = [vp, i64, i64, i64, vp, vp, c_int, vp, vp, c_int, c_int, vp, size, vp, vp]
         for name in EXPORTS[1:]:
             getattr(L, name).restype = c_int
         if path is None:

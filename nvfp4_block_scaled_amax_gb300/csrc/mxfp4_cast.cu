@@ -70,13 +70,23 @@ __device__ __forceinline__ float larger(float a, float b) {
   asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// The stored byte of a block's scale, from the bits of its maximum.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
-  const uint32_t e = (amax_bits >> 23) & 255u;
-  return e == 255u ? 255u : e < 2u ? 0u : e - 2u;
+// Two maxima, each as the upper half of an FP32 number, -> the bytes of their
+// scales in the halves of a word: max(E - 2, 0), and 255 for E = 255.
+__device__ __forceinline__ uint32_t scale_bytes(uint32_t maxima) {
+  const uint32_t e = (maxima >> 7) & 0x00FF00FFu;
+  uint32_t b;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(b) : "r"(e), "r"(0x00020002u));
+  return b - 0x00020002u + (((e + 0x00010001u) & 0x01000100u) >> 7);
 }
-// 1 / scale (of a block that is not finite: any number; its codes are masked).
-__device__ __forceinline__ float encode_of(uint32_t byte) { return __uint_as_float((254u - min(byte, 252u)) << 23); }
+__device__ __forceinline__ uint32_t byte_of(uint32_t bytes, int half) { return half ? bytes >> 16 : bytes & 0xFFFFu; }
+// 1 / scale (of a block that is not finite: anything; its codes become 0).
+__device__ __forceinline__ float encode_of(uint32_t byte) { return __uint_as_float(0x7F000000u - (byte << 23)); }
+// Two values times two factors.
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y, float f, float g) {
+  asm("{\n .reg .b64 p, q;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n mul.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}"
+      : "=f"(a), "=f"(b)
+      : "f"(x), "f"(y), "f"(f), "f"(g));
+}
 
 // Four scales of line r (a row, or a column), blocks 4 t .. of C.
 __device__ __forceinline__ void put_scales(uint8_t* base, int64_t r, int t, int64_t C, bool swizzled, uint32_t word) {
@@ -100,8 +110,8 @@ mxfp4_cast_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constan
                   const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CastKernelArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full;
-  __shared__ __align__(16) float col_max[kThreads / 32][kTile];
-  __shared__ __align__(16) uint8_t row_sc[kTile][4], col_sc[kTile][4];
+  __shared__ __align__(16) uint32_t col_max[kThreads / 32][kTile / 2];
+  __shared__ __align__(16) uint8_t row_sc[4][kTile], col_sc[4][kTile];  // [block][line]
   const uint32_t in = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t out_row = in + Smem<kBf16>::kInBytes, out_col = out_row + kCodeBytes;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
@@ -156,11 +166,10 @@ mxfp4_cast_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constan
     const int tm = (int)(t / a.tiles_n), tn = (int)(t % a.tiles_n);
     const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
 
-    // The scale bytes of the thread's rows (their block: lanes g & ~3 .. g | 3),
-    // four to a word, and the maxima of its columns over 16 rows.
-    uint32_t rs[2] = {0, 0};
+    // Maxima of the thread's rows (then over the four lanes of a block) and
+    // columns (over 16 rows), two to a word, as the upper halves of FP32 numbers.
+    uint32_t rm[4], cm[4] = {0, 0, 0, 0};
     if constexpr (kBf16) {
-      uint32_t rm[4], cm[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         uint32_t m = 0;
@@ -173,107 +182,97 @@ mxfp4_cast_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constan
         m = larger(m, __byte_perm(m, m, 0x1032));
         if (i & 1) rm[i >> 1] = __byte_perm(rm[i >> 1], m, 0x5410); else rm[i >> 1] = m;
       }
-      if constexpr (kRow) {
-#pragma unroll
-        for (int d = 1; d < 4; d <<= 1)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) rm[k] = larger(rm[k], __shfl_xor_sync(0xFFFFFFFFu, rm[k], d));
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          rs[k >> 2] |= scale_byte(k & 1 ? rm[k >> 1] & 0xFFFF0000u : rm[k >> 1] << 16) << (8 * (k & 3));
-      }
-      if constexpr (kCol) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) cm[k] = larger(cm[k], __shfl_xor_sync(0xFFFFFFFFu, cm[k], 16));
-        if (lane < 16) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(&col_max[w][8 * g + 4 * k]) =
-                make_float4(bf16_lo(cm[2 * k]), bf16_hi(cm[2 * k]), bf16_lo(cm[2 * k + 1]), bf16_hi(cm[2 * k + 1]));
-        }
-      }
     } else {
-      float rm[8], cm[8];
+      float r[8], c[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) cm[k] = 0.0f;
+      for (int k = 0; k < 8; ++k) c[k] = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        rm[i] = 0.0f;
+        r[i] = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float v = __uint_as_float(x[i][k]);
-          if (kRow) rm[i] = larger(rm[i], v);
-          if (kCol) cm[k] = larger(cm[k], v);
+          if (kRow) r[i] = larger(r[i], v);
+          if (kCol) c[k] = larger(c[k], v);
         }
       }
-      if constexpr (kRow) {
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) rm[i] = larger(rm[i], __shfl_xor_sync(0xFFFFFFFFu, rm[i], d));
-#pragma unroll
-        for (int k = 0; k < 8; ++k) rs[k >> 2] |= scale_byte(__float_as_uint(rm[k])) << (8 * (k & 3));
-      }
-      if constexpr (kCol) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) cm[k] = larger(cm[k], __shfl_xor_sync(0xFFFFFFFFu, cm[k], 16));
-        if (lane < 16) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(&col_max[w][8 * g + 4 * k]) =
-                make_float4(cm[4 * k], cm[4 * k + 1], cm[4 * k + 2], cm[4 * k + 3]);
-        }
+      for (int k = 0; k < 4; ++k) {
+        rm[k] = __byte_perm(__float_as_uint(r[2 * k]), __float_as_uint(r[2 * k + 1]), 0x7632);
+        cm[k] = __byte_perm(__float_as_uint(c[2 * k]), __float_as_uint(c[2 * k + 1]), 0x7632);
       }
     }
+    uint32_t rs[4], cs[4];  // the scale bytes of rows / columns 2 k, 2 k + 1
     if constexpr (kRow) {
-      if ((g & 3) == 0)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) row_sc[8 * rg + i][g >> 2] = (uint8_t)(rs[i >> 2] >> (8 * (i & 3)));
+      for (int k = 0; k < 4; ++k) {
+        rm[k] = larger(rm[k], __shfl_xor_sync(0xFFFFFFFFu, rm[k], 1));
+        rm[k] = larger(rm[k], __shfl_xor_sync(0xFFFFFFFFu, rm[k], 2));
+        rs[k] = scale_bytes(rm[k]);
+      }
+      if ((g & 3) == 0)
+        *reinterpret_cast<uint2*>(&row_sc[g >> 2][8 * rg]) =
+            make_uint2(__byte_perm(rs[0], rs[1], 0x6420), __byte_perm(rs[2], rs[3], 0x6420));
     }
-    __syncthreads();
-    // the column scales: the maxima of two warps make a block of 32 rows
-    uint32_t cs[2] = {0, 0};
     if constexpr (kCol) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float4 u = *reinterpret_cast<const float4*>(&col_max[w & ~1][8 * g + 4 * k]);
-        const float4 v = *reinterpret_cast<const float4*>(&col_max[w | 1][8 * g + 4 * k]);
-        cs[k] = scale_byte(__float_as_uint(larger(u.x, v.x))) | scale_byte(__float_as_uint(larger(u.y, v.y))) << 8 |
-                scale_byte(__float_as_uint(larger(u.z, v.z))) << 16 | scale_byte(__float_as_uint(larger(u.w, v.w))) << 24;
-      }
+      for (int k = 0; k < 4; ++k) cm[k] = larger(cm[k], __shfl_xor_sync(0xFFFFFFFFu, cm[k], 16));
+      if (lane < 16) *reinterpret_cast<uint4*>(&col_max[w][4 * g]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+    }
+    __syncthreads();
+    if constexpr (kCol) {  // the maxima of two warps make a block of 32 rows
+      const uint4 u = *reinterpret_cast<const uint4*>(&col_max[w & ~1][4 * g]);
+      const uint4 v = *reinterpret_cast<const uint4*>(&col_max[w | 1][4 * g]);
+      cs[0] = scale_bytes(larger(u.x, v.x)), cs[1] = scale_bytes(larger(u.y, v.y));
+      cs[2] = scale_bytes(larger(u.z, v.z)), cs[3] = scale_bytes(larger(u.w, v.w));
       if (lane < 16 && (w & 1) == 0)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) col_sc[8 * g + k][w >> 1] = (uint8_t)(cs[k >> 2] >> (8 * (k & 3)));
+        *reinterpret_cast<uint2*>(&col_sc[w >> 1][8 * g]) =
+            make_uint2(__byte_perm(cs[0], cs[1], 0x6420), __byte_perm(cs[2], cs[3], 0x6420));
     }
     auto value = [&](int i, int k) {  // element of row i, column k
       if constexpr (kBf16) return k & 1 ? bf16_hi(x[i][k >> 1]) : bf16_lo(x[i][k >> 1]);
       else return __uint_as_float(x[i][k]);
     };
+    auto any_bad = [](const uint32_t (&b)[4]) {  // a block that is not finite
+      uint32_t e = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) e |= b[k] + 0x00010001u;
+      return (e & 0x01000100u) != 0;
+    };
     // Rows of 64 bytes; 16-byte places swizzled by bits 1 and 2 of the row, as TMA expects them.
     if constexpr (kRow) {
+      uint32_t q[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t s = (rs[i >> 2] >> (8 * (i & 3))) & 255u;
-        const float f = encode_of(s);
+        const float f = encode_of(byte_of(rs[i >> 1], i & 1));
         float v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(value(i, k), f);
-        const uint32_t q = e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
-        sts_u32(out_row + (8 * rg + i) * 64 + (((g >> 2) ^ (i >> 1)) & 3) * 16 + (g & 3) * 4, s == 255u ? 0u : q);
+        for (int k = 0; k < 8; k += 2) mul2(v[k], v[k + 1], value(i, k), value(i, k + 1), f, f);
+        q[i] = e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
       }
+      if (any_bad(rs))
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (byte_of(rs[i >> 1], i & 1) == 255u) q[i] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        sts_u32(out_row + (8 * rg + i) * 64 + (((g >> 2) ^ (i >> 1)) & 3) * 16 + (g & 3) * 4, q[i]);
     }
     if constexpr (kCol) {
       uint32_t c[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t s = (cs[k >> 2] >> (8 * (k & 3))) & 255u;
-        const float f = encode_of(s);
-        float v[8];
+      for (int k = 0; k < 8; k += 2) {
+        const float f = encode_of(byte_of(cs[k >> 1], 0)), h = encode_of(byte_of(cs[k >> 1], 1));
+        float v[8], u[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(value(i, k), f);
-        const uint32_t q = e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
-        c[k] = s == 255u ? 0u : q;
+        for (int i = 0; i < 8; ++i) mul2(v[i], u[i], value(i, k), value(i, k + 1), f, h);
+        c[k] = e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+        c[k + 1] = e2m1x8(u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
       }
+      if (any_bad(cs))
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (byte_of(cs[k >> 1], k & 1) == 255u) c[k] = 0;
       // Lane g stores its column k ^ (g & 7) in turn k (three rounds of swaps
       // arrange them), so that a turn's stores fall into different banks.
 #pragma unroll
@@ -300,13 +299,15 @@ mxfp4_cast_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constan
       if (kCol) tma_store_2d(&cmap, out_col, (int32_t)(m0 / 2), (int32_t)n0);
       bulk_commit();
     }
+    // four bytes of a line, one from each block
+    auto word = [](const uint8_t (&sc)[4][kTile], int line) {
+      return (uint32_t)sc[0][line] | (uint32_t)sc[1][line] << 8 | (uint32_t)sc[2][line] << 16 | (uint32_t)sc[3][line] << 24;
+    };
     if (tid < kTile) {
-      if (kRow && m0 + tid < a.M)
-        put_scales(a.scale_row, m0 + tid, tn, a.N / 32, a.swizzled, *reinterpret_cast<const uint32_t*>(row_sc[tid]));
+      if (kRow && m0 + tid < a.M) put_scales(a.scale_row, m0 + tid, tn, a.N / 32, a.swizzled, word(row_sc, tid));
     } else {
       const int c = tid - kTile;
-      if (kCol && n0 + c < a.N)
-        put_scales(a.scale_col, n0 + c, tm, a.M / 32, a.swizzled, *reinterpret_cast<const uint32_t*>(col_sc[c]));
+      if (kCol && n0 + c < a.N) put_scales(a.scale_col, n0 + c, tm, a.M / 32, a.swizzled, word(col_sc, c));
     }
   }
   if (tid == 0) bulk_wait_all();

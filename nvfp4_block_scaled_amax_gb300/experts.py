@@ -114,33 +114,35 @@ def expert_mlp(x: torch.Tensor, up: FP4Operand, down: FP4Operand, expert_ids: to
     expert are faster through ``expert_layer``'s operators."""
     E, F2, H = _check_operand("up", up, 3)
     Ed, Hd, F = _check_operand("down", down, 3)
-    dev = x.device
+    x_shape, ids_shape, dev = x.shape, expert_ids.shape, x.device
     if x.dtype is not torch.bfloat16 or gates.dtype is not torch.float32 or expert_ids.dtype is not torch.int32:
         raise TypeError(f"bfloat16 x, float32 gates and int32 expert_ids, got {x.dtype}, {gates.dtype} and "
                         f"{expert_ids.dtype}")
-    if x.dim() != 2 or expert_ids.dim() != 2 or gates.shape != expert_ids.shape or expert_ids.shape[0] != x.shape[0]:
+    if len(x_shape) != 2 or len(ids_shape) != 2 or gates.shape != ids_shape or ids_shape[0] != x_shape[0]:
         raise ValueError("x [T, H], expert_ids and gates [T, topk]")
-    T, topk = expert_ids.shape
-    if Ed != E or Hd != H or F2 != 2 * F or x.shape[1] != H or up.block != down.block:
+    T, topk = ids_shape
+    if Ed != E or Hd != H or F2 != 2 * F or x_shape[1] != H or up.block != down.block:
         raise ValueError(f"up [E, 2 F, H] and down [E, H, F] of one format for x [T, H], got {(E, F2, H)} (block "
-                         f"{up.block}), {(Ed, Hd, F)} (block {down.block}) and {tuple(x.shape)}")
+                         f"{up.block}), {(Ed, Hd, F)} (block {down.block}) and {tuple(x_shape)}")
     if up.swizzled or down.swizzled:
         raise ValueError("expert_mlp takes compact scales")
-    if not 1 <= T * topk <= _lib.MAX_MLP_SLOTS and T:
-        raise ValueError(f"expert_mlp takes up to {_lib.MAX_MLP_SLOTS} choices, got {T} x {topk}")
-    if max(H, F) > _lib.MAX_MLP_WIDTH:
-        raise ValueError(f"expert_mlp takes sizes up to {_lib.MAX_MLP_WIDTH}")
-    for v in (x, expert_ids, gates):
-        if not (v.is_cuda and v.is_contiguous()) or v.device != dev:
-            raise ValueError("tensors passed to libnvfp4 must be contiguous CUDA tensors, on one device")
-    if up.data.device != dev or down.data.device != dev:
+    if T * topk > _lib.MAX_MLP_SLOTS or not 1 <= topk <= _lib.MAX_TOPK:
+        raise ValueError(f"expert_mlp takes up to {_lib.MAX_MLP_SLOTS} choices, up to {_lib.MAX_TOPK} a token, got {T} x "
+                         f"{topk}")
+    if max(H, F) > _lib.MAX_MLP_WIDTH or not 1 <= E <= _lib.MAX_EXPERTS:
+        raise ValueError(f"expert_mlp takes sizes up to {_lib.MAX_MLP_WIDTH} and up to {_lib.MAX_EXPERTS} experts")
+    index = x.get_device()
+    if index < 0 or not (x.is_contiguous() and expert_ids.is_contiguous() and gates.is_contiguous()) or \
+            expert_ids.get_device() != index or gates.get_device() != index:
+        raise ValueError("tensors passed to libnvfp4 must be contiguous CUDA tensors, on one device")
+    if up.data.get_device() != index or down.data.get_device() != index:
         raise ValueError("weights and x on one device")
     if out is None:
         out = torch.empty_like(x)
-    elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous bfloat16 {tuple(x.shape)} tensor on {dev}")
+    elif out.shape != x_shape or out.dtype != x.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous bfloat16 {tuple(x_shape)} tensor on {dev}")
     need = _mlp_workspace(T, topk, E, H, F, up.block)
     work = torch.empty(need, dtype=torch.uint8, device=dev)
-    call("nvfp4_expert_mlp", dev, x.data_ptr(), T, H, F, ctypes.byref(_struct(up, E)), ctypes.byref(_struct(down, E)),
-         up.block, expert_ids.data_ptr(), gates.data_ptr(), topk, E, work.data_ptr(), need, out.data_ptr())
+    call("nvfp4_expert_mlp", dev, x.data_ptr(), T, H, F, _struct(up, E), _struct(down, E), up.block,
+         expert_ids.data_ptr(), gates.data_ptr(), topk, E, work.data_ptr(), need, out.data_ptr())
     return out

@@ -15,14 +15,15 @@ products of a linear layer y = x w^T take the operands as
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 
 import torch
 
-from . import BF16, COLWISE, FP32, ROW_SCALED, ROWWISE, SWIZZLED, _lib
+from . import BF16, COLWISE, FP32, ROW_SCALED, ROWWISE, SWIZZLED
 from ._call import call
 
 _DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
+_U8, _F32 = torch.uint8, torch.float32
 
 
 class FP4Operand:
@@ -54,65 +55,81 @@ def quantize_mxfp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = False,
     """Casts x ([M, N], bfloat16 or float32) to MXFP4: E2M1 codes with a power of two for each 32 elements of a row.
     colwise: also the cast of x transposed, from the same pass over x.  N % 32 == 0; colwise also M % 32 == 0;
     swizzled scales: both multiples of 128."""
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [M, N]")
     if not x.is_cuda or not x.is_contiguous():
         raise ValueError("tensors passed to libnvfp4 must be contiguous CUDA tensors")
     dtype = _DTYPES.get(x.dtype)
     if dtype is None:
         raise TypeError(f"quantize_mxfp4 takes bfloat16 or float32 input, got {x.dtype}")
-    M, N = x.shape
+    M, N = shape
+    if N % 32 or colwise and M % 32:
+        raise ValueError(f"blocks of 32 do not divide {tuple(shape)}")
     dev = x.device
     row = col = None
     pointers = [None] * 4
     if rowwise:
-        row = FP4Operand(torch.empty((M, N // 2), dtype=torch.uint8, device=dev),
-                         torch.empty(M * (N // 32), dtype=torch.uint8, device=dev), None, 32, swizzled)
-        pointers[:2] = row.data.data_ptr(), row.scale.data_ptr()
+        data = torch.empty((M, N // 2), dtype=_U8, device=dev)
+        scale = torch.empty(M * (N // 32), dtype=_U8, device=dev)
+        row = FP4Operand(data, scale, None, 32, swizzled)
+        pointers[:2] = data.data_ptr(), scale.data_ptr()
     if colwise:
-        col = FP4Operand(torch.empty((N, M // 2), dtype=torch.uint8, device=dev),
-                         torch.empty(N * (M // 32), dtype=torch.uint8, device=dev), None, 32, swizzled)
-        pointers[2:] = col.data.data_ptr(), col.scale.data_ptr()
+        data = torch.empty((N, M // 2), dtype=_U8, device=dev)
+        scale = torch.empty(N * (M // 32), dtype=_U8, device=dev)
+        col = FP4Operand(data, scale, None, 32, swizzled)
+        pointers[2:] = data.data_ptr(), scale.data_ptr()
     call("nvfp4_mxfp4_quantize", dev, x.data_ptr(), dtype, M, N, *pointers,
          (ROWWISE if rowwise else 0) | (COLWISE if colwise else 0) | (SWIZZLED if swizzled else 0))
     return FP4Tensor(row, col)
 
 
 def _check_operand(name: str, q: FP4Operand, dims: int) -> tuple:
-    """(batch, rows, cols) of an operand whose parts fit each other."""
+    """(batch, rows, cols) of an operand whose parts fit each other.  (In few steps where all is well: a decoding step
+    makes many calls of a few microseconds.)"""
     d, s, amax, block = q.data, q.scale, q.amax, q.block
-    if d.dtype is not torch.uint8 or s.dtype is not torch.uint8:
+    shape = d.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name}: codes with {dims} dimensions, got {tuple(shape)}")
+    rows, cols = shape[-2], 2 * shape[-1]
+    batch = shape[0] if dims == 3 else 1
+    dev = d.get_device()
+    if d.dtype is not _U8 or s.dtype is not _U8:
         raise TypeError(f"{name}: uint8 codes and scales, got {d.dtype} and {s.dtype}")
-    if d.dim() != dims:
-        raise ValueError(f"{name}: codes with {dims} dimensions, got {tuple(d.shape)}")
-    if block not in (16, 32):
+    if dev < 0 or s.get_device() < 0 or not (d.is_contiguous() and s.is_contiguous()):
+        raise ValueError("tensors passed to libnvfp4 must be contiguous CUDA tensors")
+    if s.get_device() != dev:
+        raise ValueError(f"{name}: codes and scales on one device")
+    if block != 16 and block != 32:
         raise ValueError(f"{name}: block 16 (NVFP4) or 32 (MXFP4), got {block}")
-    batch, rows, cols = d.shape[0] if dims == 3 else 1, d.shape[-2], 2 * d.shape[-1]
     if cols % 32:
         raise ValueError(f"{name}: the contracted dimension must be a multiple of 32, got {cols}")
-    if s.numel() != batch * rows * (cols // block):
-        raise ValueError(f"{name}: {s.numel()} scales do not fit codes {tuple(d.shape)} with block {block}")
-    if not (d.is_cuda and d.is_contiguous() and s.is_contiguous()):
-        raise ValueError("tensors passed to libnvfp4 must be contiguous CUDA tensors")
-    if s.device != d.device:
-        raise ValueError(f"{name}: codes and scales on one device")
+    if s.numel() * block != batch * rows * cols:
+        raise ValueError(f"{name}: {s.numel()} scales do not fit codes {tuple(shape)} with block {block}")
     if block == 32:
         if amax is not None:
             raise ValueError(f"{name}: an MXFP4 operand has no amax")
-        return batch, rows, cols
-    if amax is None or amax.dtype is not torch.float32:
+    elif amax is None or amax.dtype is not _F32:
         raise TypeError(f"{name}: an NVFP4 operand needs a float32 amax")
-    if amax.dim() != 1 or amax.numel() not in (1, batch if dims == 3 else rows):
-        raise ValueError(f"{name}: amax {tuple(amax.shape)} does not fit codes {tuple(d.shape)}")
-    if amax.device != d.device or not amax.is_contiguous():
-        raise ValueError(f"{name}: amax must be contiguous, on the codes' device")
+    else:
+        n = amax.shape
+        if len(n) != 1 or n[0] != 1 and n[0] != (batch if dims == 3 else rows):
+            raise ValueError(f"{name}: amax {tuple(n)} does not fit codes {tuple(shape)}")
+        if amax.get_device() != dev or not amax.is_contiguous():
+            raise ValueError(f"{name}: amax must be contiguous, on the codes' device")
     return batch, rows, cols
 
 
-def _struct(q: FP4Operand, rows: int) -> _lib.Operand:
-    scaled = q.amax is not None and q.amax.numel() == rows and rows != 1
-    return _lib.Operand(q.data.data_ptr(), q.scale.data_ptr(), None if q.amax is None else q.amax.data_ptr(),
-                        (SWIZZLED if q.swizzled else 0) | (ROW_SCALED if scaled else 0))
+_pack = struct.Struct("@PPPIi").pack  # nvfp4_operand
+
+
+def _struct(q: FP4Operand, rows: int) -> bytes:
+    """The operand as the library takes it; an amax for each of `rows` or one for all."""
+    amax = q.amax
+    if amax is None:
+        return _pack(q.data.data_ptr(), q.scale.data_ptr(), 0, SWIZZLED if q.swizzled else 0, 0)
+    flags = ROW_SCALED if rows != 1 and amax.shape[0] == rows else 0
+    return _pack(q.data.data_ptr(), q.scale.data_ptr(), amax.data_ptr(), flags | SWIZZLED if q.swizzled else flags, 0)
 
 
 def dequantize_fp4(q: FP4Operand, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
@@ -141,20 +158,23 @@ def matmul_fp4(a: FP4Operand, b: FP4Operand, out_dtype: torch.dtype = torch.bflo
     one for all.  Summed in FP32 by the tensor cores, rounded once.  K % 32 == 0."""
     _, M, K = _check_operand("a", a, 2)
     _, N, Kb = _check_operand("b", b, 2)
-    dev = a.data.device
     if K != Kb:
         raise ValueError(f"the contracted dimensions of a ({K}) and b ({Kb}) differ")
     if a.block != b.block:
         raise ValueError("a and b must be of one format")
-    if b.data.device != dev:
+    dev = a.data.device
+    if b.data.get_device() != dev.index:
         raise ValueError("a and b on one device")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    elif out.shape != (M, N) or out.device != dev or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous {(M, N)} tensor on {dev}")
-    code = _DTYPES.get(out.dtype)
+        code = _DTYPES.get(out_dtype)
+        if code is not None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        if out.shape != (M, N) or out.device != dev or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous {(M, N)} tensor on {dev}")
+        out_dtype = out.dtype
+        code = _DTYPES.get(out_dtype)
     if code is None:
-        raise TypeError(f"products are bfloat16 or float32, not {out.dtype}")
-    call("nvfp4_fp4_matmul", dev, ctypes.byref(_struct(a, M)), ctypes.byref(_struct(b, N)), a.block, M, N, K,
-         out.data_ptr(), code)
+        raise TypeError(f"products are bfloat16 or float32, not {out_dtype}")
+    call("nvfp4_fp4_matmul", dev, _struct(a, M), _struct(b, N), a.block, M, N, K, out.data_ptr(), code)
     return out
