@@ -538,9 +538,11 @@ typedef struct {
  * block 16 (NVFP4: E2M1 * scale * (amax / 2688)) or 32 (MXFP4).  Codes and
  * scales are multiplied and summed by the tensor cores in FP32; the amax factors
  * are multiplied into the sum, which is rounded once (BF16) or kept (FP32).
- * K % 32 == 0; any M, N >= 0; K = 0 gives zero.  A swizzled operand needs its
- * rows and K to be multiples of 128; the two operands may differ in that.
+ * K % 32 == 0, K <= NVFP4_MAX_FP4_K; any M, N >= 0; K = 0 gives zero.  A swizzled
+ * operand needs its rows and K to be multiples of 128; the two operands may differ
+ * in that.
  */
+#define NVFP4_MAX_FP4_K (1 << 27)
 nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, int block, int64_t M, int64_t N,
                               int64_t K, void* out, int out_dtype, void* stream);
 

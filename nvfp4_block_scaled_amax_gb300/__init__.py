@@ -22,7 +22,9 @@ each block of 128, and ``matmul_fp8`` / ``matmul_fp8_grouped`` /
 runs them together.
 
 4-bit products: ``matmul_fp4`` multiplies what the casts make, ``quantize(...).row`` and ``.col`` or those of
-``quantize_mxfp4`` (MXFP4: a power of two for each block of 32); ``dequantize_fp4`` reads either back (``fp4``).
+``quantize_mxfp4`` (MXFP4: a power of two for each block of 32); ``dequantize_fp4`` reads either back (``fp4``);
+``linear`` runs them as a linear layer, and ``expert_mlp`` is a whole layer of gated experts over such weights for a
+few tokens (``experts``).
 
 Paths for "1d" / "2d" / "rht": "single_pass" (one persistent kernel: amax,
 grid barrier, cast; x read from HBM once; needs a small workspace, which

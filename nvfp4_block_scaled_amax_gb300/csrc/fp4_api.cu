@@ -62,7 +62,8 @@ nvfp4_status nvfp4_mxfp4_quantize(const void* x, int dtype, int64_t M, int64_t N
   const bool row = flags & NVFP4_ROWWISE, col = flags & NVFP4_COLWISE, swizzled = flags & NVFP4_SWIZZLED;
   if (!row && !col) return NVFP4_ERR_FLAGS;
   if (dtype != NVFP4_BF16 && dtype != NVFP4_FP32) return NVFP4_ERR_DTYPE;
-  if (!size_ok(M) || !size_ok(N) || N % 32 != 0 || (col && M % 32 != 0)) return NVFP4_ERR_SHAPE;
+  if (M < 0 || N < 0 || !size_ok(M + 512) || !size_ok(N + 512) || N % 32 != 0 || (col && M % 32 != 0))
+    return NVFP4_ERR_SHAPE;
   if (swizzled && (M % 128 != 0 || N % 128 != 0)) return NVFP4_ERR_ALIGN;
   if (M > 0 && N > 0 && (x == nullptr || (row && (data_row == nullptr || scale_row == nullptr)) ||
                          (col && (data_col == nullptr || scale_col == nullptr))))
@@ -104,7 +105,9 @@ nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, in
   if (a == nullptr || b == nullptr) return NVFP4_ERR_NULL;
   if (out_dtype != NVFP4_BF16 && out_dtype != NVFP4_FP32) return NVFP4_ERR_DTYPE;
   if (block != 16 && block != 32) return NVFP4_ERR_SHAPE;
-  if (!size_ok(M) || !size_ok(N) || !size_ok(K) || K % 32 != 0) return NVFP4_ERR_SHAPE;
+  // (a row index past the last tile; a tile's sum within the limit of a wait)
+  if (M < 0 || N < 0 || K < 0 || !size_ok(M + 512) || !size_ok(N + 512) || K > NVFP4_MAX_FP4_K || K % 32 != 0)
+    return NVFP4_ERR_SHAPE;
   if (!size_ok(blocks128(M) * blocks128(N))) return NVFP4_ERR_SHAPE;  // one tile index
   nvfp4_status st = check_operand(a, block, M, K);
   if (st != NVFP4_OK) return st;
