@@ -13,7 +13,8 @@
 //
 // Warps 0-3 write the results, warp 4 issues the copies, warp 5 the MMAs (two
 // accumulators, so that a tile is multiplied while the one before it is
-// written), warps 6-9 put compact scales in order, a stage each in turn.
+// written), warps 6-9 put compact scales in order, a stage each in turn: A's, which
+// so few rows always are, and B's if they are not swizzled.
 #include "fp4_tiles.cuh"
 
 namespace nvfp4 {
@@ -59,12 +60,11 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   Barriers* bar = reinterpret_cast<Barriers*>(shares + L::share_floats(split));
   const int w = warp_index(), lane = threadIdx.x & 31;
   const int rank = split > 1 ? (int)cluster_rank() : 0;
-  const bool compact = !p.a.swizzled || !p.b.swizzled;
 
   if (w == kOutWarps) {
     if (lane == 0) {
       for (int i = 0; i < stages; ++i) {
-        mbar_init(&bar->full[i], compact ? 2 : 1);
+        mbar_init(&bar->full[i], 2);  // the copies, and compact scales
         mbar_init(&bar->empty[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
@@ -108,13 +108,10 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           const int64_t k0 = (int64_t)kb * kStageK;
           const uint32_t scales = swizzled_bytes<kBlock>(p.K, k0);
           const uint32_t dst = smem_u32(smem + s * L::kStageBytes), full = smem_u32(&bar->full[s]);
-          mbar_arrive_expect_tx(&bar->full[s],
-                                L::kCodes + (p.a.swizzled ? scales : 0) + (p.b.swizzled ? scales : 0));
+          mbar_arrive_expect_tx(&bar->full[s], L::kCodes + (p.b.swizzled ? scales : 0));
           tma_load(dst, &bmap, kb * kStageRow, (int32_t)n0, full);
           tma_load(dst + kWeights * kStageRow, &amap, kb * kStageRow, (int32_t)m0, full);
           if (p.b.swizzled) bulk_load(dst + L::kCodes, swizzled_at<kBlock>(p.b, p.K, n0, k0), scales, &bar->full[s]);
-          if (p.a.swizzled)
-            bulk_load(dst + L::kCodes + F::kScaleBytes, swizzled_at<kBlock>(p.a, p.K, m0, k0), scales, &bar->full[s]);
         }
         __syncwarp();
         ++sent;
@@ -137,8 +134,6 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     const uint32_t sb = tmem + 2 * kBN, sa = sb + F::kCols;
     uint32_t s = 0, phase = 0, buf = 0, tphase = 1;
     for (int t = t0; t < tiles && ok; t += step) {
-      // rows m0 .. of a swizzled A may begin inside a tile of 128 scales, at a multiple of 32
-      const uint32_t shift = p.a.swizzled ? (uint32_t)((int64_t)(t % p.tiles_a) * kBN % 128 / 32) : 0u;
       if (!mbar_wait(&bar->tempty[buf], tphase)) {
         ok = false;
         break;
@@ -158,7 +153,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         };
         auto multiply = [&](int k) {
           umma_fp4<1, kBlock>(tmem + buf * kBN, b + 2 * k, a + 2 * k, kIdesc | F::half(k), sb + F::col(k),
-                              sa + shift + F::col(k), k > 0 ? 1 : add);
+                              sa + F::col(k), k > 0 ? 1 : add);
         };
         if (elect_one()) {
           if (kb < full_stages) {
@@ -185,7 +180,7 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     if (!ok) report_timeout(p.status);
   } else if (w > kOutWarps + 1) {
     const int mine = w - kOutWarps - 2, active = active_scale_warps(stages);
-    if (compact && mine < active) {
+    if (mine < active) {
       uint32_t s = 0, phase = 1, it = 0;
       const CompactScales<kBlock> of_a(p.a.scale, p.K, p.a.rows), of_b(p.b.scale, p.K, p.b.rows);
       for (int t = t0; t < tiles && ok; t += step) {
@@ -194,12 +189,12 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           if ((it & (active - 1)) == (uint32_t)mine) {
             uint32_t va[4][F::kTiles], vb[4][F::kTiles];
             if (!p.b.swizzled) of_b.read(n0, kWeights, kb, vb);
-            if (!p.a.swizzled) of_a.read(m0, kBN, kb, va);
+            of_a.read(m0, kBN, kb, va);
             ok = mbar_wait(&bar->empty[s], phase);
             if (ok) {
               const uint32_t dst = smem_u32(smem + s * L::kStageBytes) + L::kCodes;
               if (!p.b.swizzled) of_b.write(dst, vb);
-              if (!p.a.swizzled) of_a.write(dst + F::kScaleBytes, va);
+              of_a.write(dst + F::kScaleBytes, va);
               fence_proxy_async_shared();
               __syncwarp();
               if (lane == 0) mbar_arrive(&bar->full[s]);

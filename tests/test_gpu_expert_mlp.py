@@ -156,3 +156,37 @@ def test_range_of_activations(block):
     assert bool(((y - want).abs() <= bound)[fine].all())
     assert bool((y[4] == 0).all())
     assert not bool(torch.isfinite(y[5:7]).any())
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_range_of_one_or_two_tokens(block):
+    E, H, F = 3, 512, 96
+    up, up_v = stack(E, 2 * F, H, block, 1, H ** -0.5)
+    down, down_v = stack(E, H, F, block, 2, F ** -0.5)
+    amax = None if up.amax is None else up.amax.cpu()
+    ids = torch.tensor([[0, 2], [1, 0]], dtype=torch.int32)
+    gates = torch.tensor([[0.5, 0.25], [1.0, 2.0]])
+    for scale, at, value in ((1e6, 0, None), (1e-6, 0, None), (1.0, 7, float("inf")), (1.0, 500, float("nan"))):
+        x = torch.randn(2, H, generator=torch.Generator().manual_seed(5)) * torch.tensor([[scale], [1.0]])
+        if value is not None:
+            x[0, at] = value
+        x = x.bfloat16()
+        for T in (1, 2):
+            y = nv.expert_mlp(x[:T].cuda(), up, down, ids[:T].cuda(), gates[:T].cuda()).cpu().double()
+            want, bound = reference(x[:T], up_v, down_v, ids[:T], gates[:T], block, amax)
+            first = 0 if value is None else 1
+            assert bool(((y - want).abs() <= bound)[first:].all())
+            assert value is None or not bool(torch.isfinite(y[0]).any())
+
+
+def test_empty_sizes():
+    """No inner or no hidden columns: zeros, or nothing."""
+    def op(n, k):
+        return nv.FP4Operand(torch.zeros(2, n, k // 2, dtype=torch.uint8, device="cuda"),
+                             torch.zeros(2, n, k // 32, dtype=torch.uint8, device="cuda"), None, 32)
+    for T in (1, 5):
+        ids, gates = torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda")
+        y = nv.expert_mlp(torch.ones(T, 64, device="cuda").bfloat16(), op(0, 64), op(64, 0), ids, gates)
+        assert y.shape == (T, 64) and bool((y == 0).all())
+        y = nv.expert_mlp(torch.ones(T, 0, device="cuda").bfloat16(), op(64, 0), op(0, 32), ids, gates)
+        assert y.shape == (T, 0)
