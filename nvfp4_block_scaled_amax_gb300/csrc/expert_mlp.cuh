@@ -14,8 +14,6 @@ constexpr int kTerms = 6;
 // ---------------------------------------------------------------------------
 // Terms
 // ---------------------------------------------------------------------------
-// What a scale of 1 stands for in term i, of what it does in the first.
-__device__ __forceinline__ constexpr float term_ratio(int i) { return i == 0 ? 1.0f : 1.0f / (float)(4 << (3 * (i - 1))); }
 // The sum of a row's terms, the smallest first.
 __device__ __forceinline__ float add_terms(const uint32_t* v) {
   float sum = __uint_as_float(v[kTerms - 1]);
