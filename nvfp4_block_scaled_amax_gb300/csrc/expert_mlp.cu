@@ -4,10 +4,10 @@
 //
 // With a few rows an expert the time is that of reading its weights once, and
 // unpacking them to multiply in 16 bits costs more instructions than the SMs can
-// issue meanwhile (about two a weight; measured at the largest listed sizes 135
-// us where reading takes 51).  So the tensor cores take the weights as they are
+// issue meanwhile (about two a weight; 64 tokens, 4 of 32 experts of 4096 x 1536: 135
+// us, where reading takes 51).  So the tensor cores take the weights as they are
 // (tcgen05 block_scale), and the activations become 4 bits too: as the sum of
-// kTerms 4-bit operands, each the cast of what the earlier ones left over.
+// kTerms 4-bit operands.
 //
 // Terms.  A block (16 or 32 elements, as the weights') has one scale s, at which
 // its largest element is at most 6 (NVFP4: the next E4M3 number above a sixth of it,
@@ -31,6 +31,14 @@
 // 128 weight rows on the tensor-memory lanes (64 gate and 64 up rows) by kTok
 // tokens' terms, the contracted dimension of a tile split over a cluster where
 // there are few tiles; partial results travel with their terms already added.
+//
+// Measured: 13 tokens, 4 of 16 experts of 2720 x 1184 (MXFP4) 26.2 us, where reading
+// the weights takes 15.5; 64 tokens, 4 of 32 experts of 4096 x 1536 (NVFP4) 72 us of
+// 51.  Of the 72, 7 go by until the terms are there (the first three stages of
+// weights of every CTA are read meanwhile), 5 between the two products and 4 for
+// the join; in between, weights and scales come at 5.9 TB/s.  Not kept, as the time
+// stayed or grew: the next weights, or the next product's, or the next tile's
+// scales fetched into L2 ahead; two stages of scales a warp.
 #include "expert_mlp.cuh"
 
 namespace nvfp4 {
@@ -693,8 +701,11 @@ cudaError_t launch_product(const Fp4Side& weights, MlpKernelArgs p, int64_t slot
   p.tiles = kDown ? (p.rows + kWeights - 1) / kWeights : (p.inner + kWeights / 2 - 1) / (kWeights / 2);
   p.status = ctx.status;
   const int64_t tiles = segments * p.tiles, stages_k = (p.width + kStageK - 1) / kStageK;
+  // A tile's stages are shared by up to four CTAs where they fit beside one another, two
+  // stages each at least (6 tokens, one of 2 experts of 8192 x 1024: 18.4 us, unshared 21.1;
+  // 8 tokens, one expert of 4096 x 2048: 15.8, unshared 17.1, by up to eight 17.0).
   int split = 1;
-  for (int s = 8; s >= 2 && split == 1; s /= 2)
+  for (int s = 4; s >= 2 && split == 1; s /= 2)
     if (tiles * s <= 2 * ctx.num_sms && stages_k >= 2 * s) split = s;
   constexpr int kPerCta = 113 * 1024;  // two CTAs share an SM's 228 KB, 1 KB of it reserved for each
   const int rest = 1024 + L::rest(split, p.slots, p.experts);

@@ -16,6 +16,13 @@
 //
 // Swizzled scales are copied by TMA as they stand; compact ones are put in order
 // by four warps, a stage each in turn.
+//
+// 8192 x 5120 x 8192 (NVFP4, BF16 out): 98 us, 7.0 PFLOP/s, the tensor pipe 81 % busy at
+// the clock the power limit leaves (1.87 GHz in one launch).  An MMA of 64 elements
+// takes 128 cycles, so a stage asks the L2 for 74 bytes a cycle and SM, and the copies
+// alone (one MMA a stage) take 80 us, about as long as the MMAs alone at this clock:
+// the two bound it together.  Without the scales' way into tensor memory it would
+// be 95; each half of B's scales sent to both CTAs at once (multicast) changes nothing.
 #include "fp4_tiles.cuh"
 
 namespace nvfp4 {

@@ -11,6 +11,11 @@
 // on the owner's barrier), and the owner adds the shares in the order of
 // their rank, so the result does not depend on timing.
 //
+// One row through 5120 x 4096 (NVFP4, swizzled weights) takes 5.2 us in a graph, of which
+// the weights' bytes are 1.8: the start of the launch, the first copies' latency,
+// the cluster's join and the end are one after the other.  Eight rows through
+// 10240 x 8192 take 10.6 us, 4.5 TB/s.
+//
 // Warps 0-3 write the results, warp 4 issues the copies, warp 5 the MMAs (two
 // accumulators, so that a tile is multiplied while the one before it is
 // written), warps 6-9 put compact scales in order, a stage each in turn: A's, which
@@ -361,6 +366,8 @@ ThinPlan thin_plan(const Fp4MatmulArgs& a, const LaunchCtx& ctx) {
   ThinPlan t;
   t.bn = a.a.rows <= 16 ? 16 : a.a.rows <= 32 ? 32 : 64;
   t.tiles = (a.a.rows + t.bn - 1) / t.bn * ((a.b.rows + kWeights - 1) / kWeights);
+  // (8 rows, N 2048, K 8192: 5.2 us by eight CTAs a tile, 5.4 by up to four, 7.6 two, 9.8 one; 1 row, 5120 x 4096:
+  // 5.2 by four, 5.3 two, 6.6 one; 64 rows, N 1024, K 8192: 7.4 by eight, 11.0 by fewer.)
   const int64_t stages = (a.K + kStageK - 1) / kStageK;
   t.split = 1;
   for (int s = 8; s >= 2 && t.split == 1; s /= 2)
