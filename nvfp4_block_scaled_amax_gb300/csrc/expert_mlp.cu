@@ -82,7 +82,7 @@ __device__ __forceinline__ void group_slots(const int32_t* from, int slots, int 
   const int tid = threadIdx.x, lane = tid & 31;
   for (int e = tid; e <= experts; e += threads) row0[e] = 0;
   for (int s = tid; s < slots; s += threads) {
-    const int e = from[s];
+    const int e = __ldcg(&from[s]);
     ids[s] = e >= 0 && e < experts ? e : -1;
   }
   __syncthreads();
@@ -295,7 +295,7 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
   // waited for its own predecessor before it let this one begin.
   int segs;
   if constexpr (kDown)
-    segs = *p.plan.segments;  // (two kernels back)
+    segs = __ldcg(p.plan.segments);  // (two kernels back; from L2, as this memory served earlier calls)
   else
     group_slots(p.ids, p.slots, p.experts, kTok, ids, row0, seg0, kThreads), segs = seg0[p.experts];
   tcgen05_before_sync();
@@ -312,7 +312,7 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
   bool ok = true;
   // A segment: its expert, first sorted slot and slots.
   auto segment_of = [&](int i) -> int4 {
-    if constexpr (kDown) return p.plan.table[i];
+    if constexpr (kDown) return __ldcg(&p.plan.table[i]);
     int lo = 0, hi = p.experts;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;

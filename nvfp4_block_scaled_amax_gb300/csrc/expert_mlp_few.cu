@@ -61,7 +61,7 @@ struct Barriers {
 // One warp finds them: lane s has choice s.
 __device__ __forceinline__ void find_chosen(const FewArgs& p, Chosen& to) {
   const int lane = threadIdx.x & 31;
-  int e = lane < p.tokens * p.topk ? p.ids[lane] : -1;
+  int e = lane < p.tokens * p.topk ? __ldcg(&p.ids[lane]) : -1;
   if (e >= p.experts) e = -1;
   const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
   const int leader = __ffs(same) - 1;

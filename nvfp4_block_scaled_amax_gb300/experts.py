@@ -90,7 +90,7 @@ def quantize_experts(weights: torch.Tensor, block: int = 16) -> FP4Operand:
     scale = torch.empty((E, N, K // 16), dtype=torch.uint8, device=dev)
     amax = torch.zeros((E, 4), dtype=torch.float32, device=dev)  # (each at a 16-byte boundary, as the cast writes them)
     from . import NVFP4Tensor
-    for e0 in range(0, E, _lib.MAX_GROUPS):
+    for e0 in range(0, E if N * K else 0, _lib.MAX_GROUPS):
         members = range(e0, min(E, e0 + _lib.MAX_GROUPS))
         outs = [NVFP4Tensor(N, K, data[e], scale[e].view(-1), amax[e, :1]) for e in members]
         quantize_grouped(weights[e0:members.stop].view(-1, K), [N] * len(members), "1d", colwise=False, out=outs)

@@ -58,6 +58,14 @@ def test_mxfp4_cast_of_every_bf16_value():
     code, byte = mx_cast(x)
     assert torch.equal(q.scale.cpu(), byte.reshape(-1))
     assert torch.equal(q.data.cpu(), pack(code))
+    # as columns: neighbouring blocks of every size, beside ones that are not finite
+    for shuffled in (False, True):
+        y = x[torch.randperm(len(x), generator=torch.Generator().manual_seed(1))] if shuffled else x
+        q = nv.quantize_mxfp4(y.t().contiguous().cuda(), colwise=True)
+        for op, ref in ((q.row, y.t()), (q.col, y)):
+            code, byte = mx_cast(ref)
+            assert torch.equal(op.scale.cpu(), byte.reshape(-1))
+            assert torch.equal(op.data.cpu(), pack(code))
 
 
 def test_nvfp4_reading_back_is_dequantize():
