@@ -62,6 +62,7 @@ struct Plan {
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32;
 constexpr int kPrepPart = 128 * kPrepWarps;  // elements of a CTA
+constexpr int kScaleRows = 128;              // of a segment's scale tiles
 
 struct PrepArgs {
   const uint16_t* x;
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
   int* row0 = ids + p.slots;             // [experts + 1] first sorted slot
   int* seg0 = row0 + p.experts + 1;      // [experts + 1] first segment
   __shared__ float largest[kPrepWarps], sums[kPrepWarps];
-  __shared__ int place[kMaxTopk];
+  __shared__ int2 place[kMaxTopk];  // of a choice: its sorted slot (-1: dropped), and the row of its first scales
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int parts = (p.width + kPrepPart - 1) / kPrepPart;
   const int token = blockIdx.x / parts, part = blockIdx.x % parts;
@@ -157,11 +158,14 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
   }
   // This CTA's share of the token's choices: how many earlier slots chose the same expert.
   for (int j = blockIdx.y + w * gridDim.y; j < p.topk; j += kPrepWarps * gridDim.y) {
-    const int s = token * p.topk + j, e = ids[s];
+    const int s = token * p.topk + j, e = ids[s];  // (a dropped choice counts others that were dropped)
     int before = 0;
     for (int i = lane; i < s; i += 32) before += ids[i] == e;
     before = __reduce_add_sync(0xFFFFFFFFu, before);
-    if (lane == 0) place[j] = before;
+    if (lane == 0) {
+      const int seg = before / p.tok;
+      place[j] = e < 0 ? make_int2(-1, 0) : make_int2(row0[e] + before, (seg0[e] + seg) * kScaleRows + (before - seg * p.tok) * kTerms);
+    }
   }
   // Terms of 128 elements a warp, the last ones padded to a step of 64 with zeros.
   const float unit = kBlock == 16 ? unit_of(m) : 1.0f;
@@ -177,10 +181,10 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
   __syncthreads();
   // They go to the rows of those choices.
   for (int j = blockIdx.y; j < p.topk; j += gridDim.y) {
-    const int slot = token * p.topk + j, e = ids[slot];
-    if (e < 0) continue;
-    const int r = row0[e] + place[j], seg = seg0[e] + place[j] / p.tok;
+    const int r = place[j].x, n0 = place[j].y % kScaleRows, seg = place[j].y / kScaleRows;
+    if (r < 0) continue;
     if (part == 0 && tid == 0) {
+      const int slot = token * p.topk + j, e = ids[slot];
       p.plan.slot_of_row[r] = slot;
       p.x_rows.unit[r] = unit;
       if constexpr (kBlock == 16) {
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
       for (int i = 0; i < kTerms; ++i)
         *reinterpret_cast<uint16_t*>(p.x_rows.codes + ((int64_t)r * kTerms + i) * row_bytes + k / 2) = codes[i];
     if (k < (p.width + 63) / 64 * 64)
-      put_scale<kBlock>(p.x_rows.scales + seg * tiles * kScaleTile, place[j] % p.tok * kTerms, k, scale);
+      put_scale<kBlock>(p.x_rows.scales + seg * tiles * kScaleTile, n0, k, scale);
   }
 }
 
