@@ -262,6 +262,11 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       const int cols = (int)min((int64_t)(it.half ? 128 : 256), p.b.rows - it.n0) - 128 * half;
       const float fa = row_factor(p.a, p.a.amax_per_row ? it.m0 + row0 + lane : 0);
       const Factor all = factor(fa, p.b.amax_per_row ? 1.0f : row_factor(p.b, 0));
+      // with an amax for each column: lane l has those of columns l, 32 + l, ... of the warp's 128
+      float fb[4] = {};
+      if (p.b.amax_per_row)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) fb[k] = row_factor(p.b, it.n0 + 128 * half + 32 * k + lane);
       ok = mbar_wait(&bar->tfull[buf], tphase);
       if (!ok) break;
       __syncwarp();
@@ -331,10 +336,16 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
           tmem_read(src + c, v);
           if (h == 0 && holds) release();
           if (p.b.amax_per_row) {
+            const float f0 = c == 0 ? fb[0] : fb[2], f1 = c == 0 ? fb[1] : fb[3];
+            if (one_product(fa, f0, f1)) {
 #pragma unroll
-            for (int k = 0; k < 64; ++k) {
-              const float fb = row_factor(p.b, it.n0 + 128 * half + c + k);
-              v[k] = __float_as_uint(factor(fa, fb)(__uint_as_float(v[k])));
+              for (int k = 0; k < 64; ++k)
+                v[k] = __float_as_uint(__fmul_rn(__uint_as_float(v[k]),
+                                                 __fmul_rn(fa, __shfl_sync(0xFFFFFFFFu, k < 32 ? f0 : f1, k & 31))));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 64; ++k)
+                v[k] = __float_as_uint(factor(fa, __shfl_sync(0xFFFFFFFFu, k < 32 ? f0 : f1, k & 31))(__uint_as_float(v[k])));
             }
           } else {
 #pragma unroll

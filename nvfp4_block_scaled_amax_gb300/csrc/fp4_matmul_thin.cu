@@ -223,9 +223,15 @@ matmul_thin_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       const bool there = n0 + n_in_tile < p.b.rows;
       const float fb = row_factor(p.b, n0 + n_in_tile);
       const Factor whole = factor(p.a.amax_per_row ? 1.0f : row_factor(p.a, 0), fb);
-      auto store = [&](int c, float v) {
+      // with an amax for each row of A: lane l has those of columns l and 32 + l
+      float fa[2] = {};
+      if (p.a.amax_per_row)
+#pragma unroll
+        for (int k = 0; k < (kBN + 31) / 32; ++k) fa[k] = row_factor(p.a, m0 + 32 * k + lane);
+      auto store = [&](int c, float v) {  // (by whole warps)
+        const float mine = __shfl_sync(0xFFFFFFFFu, c < 32 ? fa[0] : fa[1], c & 31);
         if (c >= rows || !there) return;
-        v = p.a.amax_per_row ? factor(row_factor(p.a, m0 + c), fb)(v) : whole(v);
+        v = p.a.amax_per_row ? factor(mine, fb)(v) : whole(v);
         const int64_t at = (m0 + c) * p.b.rows + n0 + n_in_tile;
         if (p.out_bf16) {
           uint16_t h;

@@ -227,6 +227,19 @@ __device__ __forceinline__ Factor factor(float a, float b) {
   if (both > 0x1.fffffep127f && a <= 0x1.fffffep127f && b <= 0x1.fffffep127f) return {fminf(a, b), fmaxf(a, b)};
   return {both, 1.0f};
 }
+// Whether factor(a, b) is one product for every lane's a and each lane's two b.
+__device__ __forceinline__ bool one_product(float a, float b0, float b1) {
+  uint32_t lo = 0x7F7FFFFFu, hi = 0;  // the least positive b and the largest finite one, as bits
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t bits = __float_as_uint(i == 0 ? b0 : b1);
+    if (bits - 1u < 0x7F7FFFFFu) lo = min(lo, bits), hi = max(hi, bits);
+  }
+  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+  return __all_sync(0xFFFFFFFFu, !(a > 0.0f && __fmul_rn(a, __uint_as_float(lo)) < 0x1p-126f) &&
+                                     !(a <= 0x1.fffffep127f && __fmul_rn(a, __uint_as_float(hi)) > 0x1.fffffep127f));
+}
 // amax / 2688 of a row (1 of an MXFP4 operand).
 __device__ __forceinline__ float row_factor(const Fp4Side& s, int64_t row) {
   if (s.amax == nullptr) return 1.0f;

@@ -9,7 +9,7 @@ from fp4_testutil import operand, random_parts, values
 
 pytestmark = pytest.mark.gpu
 
-U32 = 2.0 ** -24
+U32, U16 = 2.0 ** -24, 2.0 ** -8
 
 
 def experts(E, H, F, block, seed):
@@ -148,6 +148,33 @@ def test_factors_far_apart(m, n):
         big = want.abs() > 3.4e38
         assert bool(((y - want).abs() <= 4 * U32 * want.abs() + 2.0 ** -148)[~big].all())
         assert bool(torch.isinf(y[big]).all())
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,n,per_a,per_b", [(6, 200, True, True), (40, 130, True, False), (40, 130, False, True),
+                                             (150, 300, True, True), (300, 520, False, True), (260, 256, True, False)])
+def test_factors_of_rows_far_apart(m, n, per_a, per_b, out_dtype):
+    """An amax for each row of either side or both, of every size side by side, zero and not finite."""
+    k = 128
+    (da, sa, _), (db, sb, _) = random_parts(m, k, 16, 1, True), random_parts(n, k, 16, 2, True)
+    da[3], db[5] = 0, 0                                 # sums of zero under each of them
+    sizes = torch.tensor([1.0, 1e-30, 3e38, 2688.0, 1e-37, 1e-22, 7e4, 1e20, 1e-40, 1e18, 0.0, float("inf"), float("nan")])
+    g = torch.Generator().manual_seed(m)
+    for plain in (True, False):                         # columns that one product serves, and columns of all sorts
+        def amaxes(rows, per):
+            pick = torch.randint(0, 4 if plain else len(sizes), (rows if per else 1,), generator=g)
+            some = torch.tensor([0, 3, 6, 0]) if plain else torch.arange(len(sizes))
+            return sizes[some[pick]] if per else torch.tensor([1e-3])
+        aa, ab = amaxes(m, per_a), amaxes(n, per_b)
+        y = nv.matmul_fp4(operand((da, sa, aa), 16), operand((db, sb, ab), 16), out_dtype=out_dtype).cpu().double()
+        f = (aa / 2688.0).double()[:, None] * (ab / 2688.0).double()
+        want = (values(da, sa, None, 16) @ values(db, sb, None, 16).t()) * f
+        # sums exact; the factors' product or two steps, and the rounding to FP32's or BF16's numbers
+        u, least, most = (U16, 2.0 ** -133, 3.3895e38) if out_dtype == torch.bfloat16 else (U32, 2.0 ** -148, 3.4e38)
+        nan, big = want.isnan(), want.abs() > most
+        assert bool(y[nan].isnan().all()) and bool((y[big] * want[big].sign() >= most * (1 - 2 * u)).all())
+        fine = ~(nan | big)
+        assert bool(((y - want).abs() <= (4 * U32 + u) * want.abs() + least)[fine].all())
 
 
 def test_nan_scale_stays_in_its_row():
