@@ -15,7 +15,7 @@
 // given back for the next tile at once.
 //
 // Swizzled scales are copied by TMA as they stand; compact ones are put in order
-// by five warps, a stage each in turn.
+// by six warps, 128 rows of two stages each in turn.
 //
 // 8192 x 5120 x 8192 (NVFP4, BF16 out): 98 us, 7.0 PFLOP/s, the tensor pipe 81 % busy at
 // the clock the power limit leaves (1.87 GHz in one launch).  An MMA of 64 elements
@@ -24,7 +24,7 @@
 // the two bound it together.  Without the scales' way into tensor memory it would
 // be 95; each half of B's scales sent to both CTAs at once (multicast) changes nothing.
 // 4096 x 4096 x 4096: swizzled scales 26 us, with an amax for each row of both 26.3 (75 when
-// every warp worked the columns' factors out for itself), compact scales 35.
+// every warp worked the columns' factors out for itself), compact scales 31.
 #include "fp4_tiles.cuh"
 
 namespace nvfp4 {
@@ -33,8 +33,7 @@ namespace {
 
 constexpr int kStages = 5;
 constexpr int kStageA = 128 * kStageRow, kCodes = 2 * kStageA;
-constexpr int kFirstScale = 3, kPairScaleWarps = 5, kOutWarps = 8, kFirstOut = 8;
-static_assert(kPairScaleWarps <= kStages, "see active_scale_warps");
+constexpr int kFirstScale = 2, kPairScaleWarps = 6, kOutWarps = 8, kFirstOut = 8;
 constexpr int kThreads = 32 * (kFirstOut + kOutWarps);
 constexpr int kSecond = 208;  // first column of the second accumulator
 constexpr int kScaleCols = kSecond + 256;  // then the scales
@@ -75,12 +74,13 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   Barriers* bar = reinterpret_cast<Barriers*>(out_stage + kOutWarps * kOutBox);
   const int w = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const bool compact = !p.a.swizzled || !p.b.swizzled;
+  // compact scales of a stage, 128 rows at a time: A's, and the halves of B's
+  const int pieces = (p.a.swizzled ? 0 : 1) + (p.b.swizzled ? 0 : 2);
 
   if (w == 0) {
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) {
-        mbar_init(&bar->full[i], compact ? 3 : 1);  // the copies (and a scale warp of each CTA)
+        mbar_init(&bar->full[i], 1 + 2 * pieces);  // the copies (and the pieces of each CTA)
         mbar_init(&bar->empty[i], 1);
       }
       mbar_init(&bar->tfull[0], 1);
@@ -212,38 +212,49 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     }
     if (!ok) report_timeout(p.status);
   } else if (w >= kFirstScale && w < kFirstScale + kPairScaleWarps) {
-    if (compact) {
+    // A warp puts a piece of two stages in order, whose loads are in flight together: a
+    // row's 16 bytes of one stage are half a sector (4096 x 4096 x 4096 31 us, a stage at
+    // a time 35).  At most three pairs of stages are dealt out at once: a warp that
+    // wrote stage i waits for stage i + 5 next, or an earlier one; it knows that stage i -
+    // kStages is over, so what it waits for is at most one phase of the barrier away.
+    static_assert(kStages == 5, "three pairs");
+    const int active = min(kPairScaleWarps, 3 * pieces);
+    if (w - kFirstScale < active) {
       uint32_t s = 0, phase = 1;
-      int turn = w - kFirstScale;  // stages until the next of this warp
+      int turn = w - kFirstScale;  // pieces until the next of this warp
       const CompactScales<kBlock> of_a(p.a.scale, p.K, p.a.rows), of_b(p.b.scale, p.K, p.b.rows);
       for (int i = t0; i < items && ok; i += step) {
         const Item it = at(i);
         if (it.n0 >= p.b.rows) continue;
-        for (int kb = 0; kb < nkb && ok; ++kb) {
-          if (turn-- == 0) {
-            turn = kPairScaleWarps - 1;
-            uint32_t va[4][F::kTiles], vb[2][4][F::kTiles];
-            if (!p.a.swizzled) of_a.read(it.m0 + 128 * (int64_t)rank, 128, kb, va);
-            if (!p.b.swizzled) {
-              of_b.read(it.n0, 128, kb, vb[0]);
-              if (!it.half) of_b.read(it.n0 + 128, 128, kb, vb[1]);
-            }
-            ok = mbar_wait(&bar->empty[s], phase);
-            if (ok) {
-              const uint32_t dst = smem_u32(smem + s * L::kStageBytes) + kCodes;
-              if (!p.a.swizzled) of_a.write(dst, va);
-              if (!p.b.swizzled) {
-                of_b.write(dst + L::kScales, vb[0]);
-                if (!it.half) of_b.write(dst + 2 * L::kScales, vb[1]);
-              }
+        for (int kb = 0; kb < nkb && ok; kb += 2) {
+          const bool two = kb + 1 < nkb;
+          const uint32_t slot[2] = {s, s + 1 == kStages ? 0 : s + 1};
+          const uint32_t use[2] = {phase, s + 1 == kStages ? phase ^ 1 : phase};
+          for (int j = 0; j < pieces; ++j) {
+            if (turn-- != 0) continue;
+            turn = active - 1;
+            const int piece = j + (p.a.swizzled ? 1 : 0);
+            const bool there = piece < 2 || !it.half;
+            uint32_t v[2][4][F::kTiles];
+            if (piece == 0)
+              of_a.read_two(it.m0 + 128 * (int64_t)rank, kb, two, v);
+            else if (there)
+              of_b.read_two(it.n0 + 128 * (piece - 1), kb, two, v);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h == 1 && !two) break;
+              ok = ok && mbar_wait(&bar->empty[slot[h]], use[h]);
+              if (!ok) break;
+              if (there) of_a.write(smem_u32(smem + slot[h] * L::kStageBytes) + kCodes + piece * L::kScales, v[h]);
               // What the first CTA's tensor-core copies read here is ordered by the
               // fence; the arrival carries nothing else, so it needs no cluster-scope
               // release, which would wait for every load in flight.
               fence_proxy_async_shared();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&bar->full[s]), 0));
+              if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&bar->full[slot[h]]), 0));
             }
           }
+          s = two ? slot[1] : slot[0], phase = two ? use[1] : use[0];
           if (++s == kStages) {
             s = 0;
             phase ^= 1;

@@ -143,10 +143,12 @@ struct CompactScales {
   const uint8_t* scale;
   int64_t pitch, rows;
   bool whole;  // every stage of every row is a group
+  bool pairs;  // and every two stages are two, aligned as such
 
   __device__ __forceinline__ CompactScales(const uint8_t* at, int64_t K, int64_t rows_)
       : scale(at), pitch(K / kBlock), rows(rows_),
-        whole(pitch % kGroup == 0 && (reinterpret_cast<uintptr_t>(at) & (kGroup - 1)) == 0) {}
+        whole(pitch % kGroup == 0 && (reinterpret_cast<uintptr_t>(at) & (kGroup - 1)) == 0),
+        pairs(pitch % (2 * kGroup) == 0 && (reinterpret_cast<uintptr_t>(at) & (2 * kGroup - 1)) == 0) {}
 
   static __device__ __forceinline__ void group(const uint8_t* p, bool there, uint32_t* w) {
     if constexpr (kWords == 4) {
@@ -194,6 +196,60 @@ struct CompactScales {
         const int left = n - 4 * k;  // bytes of this word that the row has
         v[g][k] = left >= 4 ? x : left <= 0 ? 0u : x & ((1u << (8 * left)) - 1);
       }
+    }
+  }
+  // Stages i and, if there is one, i + 1: where rows allow it, both at once.
+  __device__ __forceinline__ void read_two(int64_t row0, int i, bool two, uint32_t (&v)[2][4][kWords]) const {
+    const int64_t row = row0 + (threadIdx.x & 31);
+    const uint8_t* p = scale + row * pitch + (int64_t)i * kGroup;
+    if (!whole) {
+      const int n = (int)min((int64_t)2 * kGroup, pitch - (int64_t)i * kGroup);  // bytes of the stages
+      uint32_t w[4][3 * kWords];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint8_t* q = p + 32 * g * pitch;
+        const int off = (int)(reinterpret_cast<uintptr_t>(q) & (kGroup - 1));
+        const bool there = row + 32 * g < rows;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) group(q - off + k * kGroup, there && off + n > k * kGroup, w[g] + k * kWords);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int off = (int)(reinterpret_cast<uintptr_t>(p + 32 * g * pitch) & (kGroup - 1));
+        uint32_t(&all)[3 * kWords] = w[g];
+        if constexpr (kWords == 4) {
+#pragma unroll
+          for (int k = 0; k < 10; ++k) all[k] = off & 8 ? all[k + 2] : all[k];
+        }
+#pragma unroll
+        for (int k = 0; k <= 2 * kWords; ++k) all[k] = off & 4 ? all[k + 1] : all[k];
+#pragma unroll
+        for (int k = 0; k < 2 * kWords; ++k) {
+          const uint32_t x = __funnelshift_r(all[k], all[k + 1], 8 * (off & 3));
+          const int left = n - 4 * k;  // bytes of this word that the row has
+          v[k / kWords][g][k % kWords] = left >= 4 ? x : left <= 0 ? 0u : x & ((1u << (8 * left)) - 1);
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g, p += 32 * pitch) {
+      uint32_t w[2 * kWords] = {};
+      if (!pairs) {
+        group(p, row + 32 * g < rows, w);
+        group(p + kGroup, row + 32 * g < rows && two, w + kWords);
+      } else if (row + 32 * g < rows) {
+        if constexpr (kWords == 4) {
+          asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                       : "l"(p));
+        } else {
+          const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+          w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) v[0][g][k] = w[k], v[1][g][k] = w[kWords + k];
     }
   }
   static __device__ __forceinline__ void write(uint32_t to, const uint32_t (&v)[4][kWords]) {

@@ -124,6 +124,19 @@ def test_product_long(shape, block):
         check_product(m, n, k, block, False, m % 128 == 0, True, torch.bfloat16, True)
 
 
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("shape", [(640, 1280, 2048), (1300, 2600, 1536), (1300, 2600, 1280), (2304, 4480, 512),
+                                   (70, 9000, 1792), (1111, 2222, 2592)])
+def test_product_compact(shape, block):
+    """Compact scales of either side or both, read two stages at a time: rows that are whole pairs of stages, whole
+    stages, and neither; odd numbers of stages; many tiles."""
+    m, n, k = shape
+    for a_sw in (False, True) if m % 128 == 0 and k % 128 == 0 else (False,):
+        for b_sw in (False, True) if n % 128 == 0 and k % 128 == 0 else (False,):
+            check_product(m, n, k, block, block == 16, a_sw, b_sw, torch.float32, True)
+            check_product(m, n, k, block, False, a_sw, b_sw, torch.bfloat16, True, 3)
+
+
 def test_product_of_nothing():
     for block in (16, 32):
         for m, n, k in ((0, 5, 64), (5, 0, 64), (5, 7, 0)):

@@ -26,11 +26,12 @@ def layer_inputs(T, topk, E, H, seed):
 
 
 @pytest.mark.parametrize("block", [16, 32])
-@pytest.mark.parametrize("m,n,k", [(5, 300, 1056), (200, 300, 1056), (40, 260, 4128)])
+@pytest.mark.parametrize("m,n,k", [(5, 300, 1056), (200, 300, 1056), (40, 260, 4128), (200, 300, 1024),
+                                   (150, 400, 1280)])
 def test_scales_at_any_address(m, n, k, block):
     pa, pb = random_parts(m, k, block, 1, True), random_parts(n, k, block, 2, True)
     want = nv.matmul_fp4(operand(pa, block), operand(pb, block))
-    for shift in (1, 2, 3, 5, 7, 8, 11, 15):
+    for shift in (1, 2, 3, 5, 7, 8, 11, 15, 16):
         ops = []
         for data, scale, amax in (pa, pb):
             room = torch.full((scale.numel() + 64,), 255, dtype=torch.uint8, device="cuda")  # NaN on both sides
