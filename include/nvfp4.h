@@ -557,13 +557,13 @@ nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, in
  * adds nothing; a token with none left gives zero.
  * Sums are FP32; x and h enter a product as sums of six 4-bit operands, which
  * leave at most 2^-17 (NVFP4) or 2^-16 (MXFP4) of the largest value of each block,
- * or of an NVFP4 row's h 2^-33 of (amax sum|x|)^2; y is rounded once.  A token with
+ * or 2^-34 of the largest of an NVFP4 row of x or h; y is rounded once.  A token with
  * an infinity or a NaN, in x or in h, gives NaN.
  * tokens * topk <= NVFP4_MAX_MLP_SLOTS, hidden and inner multiples of 32 up to
  * NVFP4_MAX_MLP_WIDTH.  workspace: nvfp4_expert_mlp_workspace bytes of device
  * memory, 128-byte aligned, contents irrelevant, not shared by calls that can run
- * at the same time.  Four launches; two for one or two tokens with up to eight
- * choices in all.
+ * at the same time.  Four launches (NVFP4 five); two for one or two tokens with
+ * up to eight choices in all.
  */
 #define NVFP4_MAX_MLP_SLOTS 1024
 #define NVFP4_MAX_MLP_WIDTH 10240

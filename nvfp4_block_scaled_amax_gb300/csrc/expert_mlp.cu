@@ -20,14 +20,16 @@
 // ratios after the product.  They are rows beside the others: N = 6 tokens, where
 // few rows leave an MMA's columns empty anyway.
 // E4M3 scales span 17 powers of two; they count in units of their row, so that a
-// row's small blocks lose nothing until 2^-34 of its largest.  The unit of a row of
-// x comes from its largest element; that of the hidden row, which is cut into terms
-// tile by tile, from a bound: |g|, |u| <= amax sum|x|.  (The sums' own rounding in
-// FP32 is of that order.)
+// row's small blocks lose nothing until 2^-34 of its largest.  The unit comes from
+// the row's largest element, which of a hidden row is not known before all of its
+// tiles are: NVFP4 keeps the hidden rows in FP32 and cuts them in a launch of their
+// own.  (A unit from a bound, |g|, |u| <= amax sum|x|, would spare the launch but
+// hold h to 2^-34 of a number that may be any multiple of it.)  MXFP4's powers
+// of two need no unit, and its hidden rows are cut where they are made.
 //
-// Four launches: slots sorted by expert and x into terms; gate and up products
-// with SiLU and the hidden rows' terms; down product, weighted by the gates;
-// the slots of a token added in order.  The products are fp4_matmul_thin.cu's:
+// Four launches (NVFP4 five): slots sorted by expert and x into terms; gate and up
+// products with SiLU; (NVFP4) the hidden rows into terms; down product, weighted by
+// the gates; the slots of a token added in order.  The products are fp4_matmul_thin.cu's:
 // 128 weight rows on the tensor-memory lanes (64 gate and 64 up rows) by kTok
 // tokens' terms, the contracted dimension of a tile split over a cluster where
 // there are few tiles; partial results travel with their terms already added.
@@ -52,9 +54,10 @@ struct Rows {
   float* unit;      // [slots] NVFP4: what a scale of 1 stands for in term 0
 };
 struct Plan {
-  int32_t* segments;     // how many
+  int32_t* counts;       // segments, sorted slots
   int4* table;           // [segments] expert, first sorted slot, slots
   int32_t* slot_of_row;  // [slots] slot of a sorted one
+  int32_t* scale_row;    // [slots] where a sorted one's scales begin: segment * kScaleRows + row
 };
 
 // ---------------------------------------------------------------------------
@@ -67,8 +70,6 @@ constexpr int kScaleRows = 128;              // of a segment's scale tiles
 struct PrepArgs {
   const uint16_t* x;
   const int32_t* ids;
-  const float* amax;  // of the gate and up weights; NULL: MXFP4
-  int amax_per_expert;
   int slots, topk, experts, width, tok;
   Rows x_rows;
   float* h_unit;
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
   int* ids = lists;                      // [slots]
   int* row0 = ids + p.slots;             // [experts + 1] first sorted slot
   int* seg0 = row0 + p.experts + 1;      // [experts + 1] first segment
-  __shared__ float largest[kPrepWarps], sums[kPrepWarps];
+  __shared__ float largest[kPrepWarps];
   __shared__ int2 place[kMaxTopk];  // of a choice: its sorted slot (-1: dropped), and the row of its first scales
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int parts = (p.width + kPrepPart - 1) / kPrepPart;
@@ -123,9 +124,9 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
   // (first the wait: the next kernel reads what precedes this one ahead of its own)
   grid_dependency_wait();
   grid_launch_dependents();
-  // The row's largest finite element and the sum of magnitudes.
+  // The row's largest finite element.
   const uint16_t* row = p.x + (int64_t)token * p.width;
-  float m = 0.0f, sum = 0.0f;
+  float m = 0.0f;
 #pragma unroll 2
   for (int k = 8 * tid; k < p.width; k += 8 * kPrepThreads) {
     const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + k));
@@ -134,27 +135,21 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float a = fabsf(v[i]);
-      if (a <= kFltMax) {
-        m = fmaxf(m, a);
-        sum = __fadd_rn(sum, a);
-      }
+      if (a <= kFltMax) m = fmaxf(m, a);
     }
   }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, d));
-  }
-  if (lane == 0) largest[w] = m, sums[w] = sum;
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  if (lane == 0) largest[w] = m;
   group_slots(p.ids, p.slots, p.experts, p.tok, ids, row0, seg0, kPrepThreads);
-  m = largest[0], sum = sums[0];
+  m = largest[0];
 #pragma unroll
-  for (int i = 1; i < kPrepWarps; ++i) m = fmaxf(m, largest[i]), sum = __fadd_rn(sum, sums[i]);
+  for (int i = 1; i < kPrepWarps; ++i) m = fmaxf(m, largest[i]);
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     for (int e = tid; e < p.experts; e += kPrepThreads)
       for (int r = row0[e], i = seg0[e]; r < row0[e + 1]; r += p.tok, ++i)
         p.plan.table[i] = make_int4(e, r, min(p.tok, row0[e + 1] - r), 0);
-    if (tid == 0) *p.plan.segments = seg0[p.experts];
+    if (tid == 0) p.plan.counts[0] = seg0[p.experts], p.plan.counts[1] = row0[p.experts];
   }
   // This CTA's share of the token's choices: how many earlier slots chose the same expert.
   for (int j = blockIdx.y + w * gridDim.y; j < p.topk; j += kPrepWarps * gridDim.y) {
@@ -184,15 +179,10 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
     const int r = place[j].x, n0 = place[j].y % kScaleRows, seg = place[j].y / kScaleRows;
     if (r < 0) continue;
     if (part == 0 && tid == 0) {
-      const int slot = token * p.topk + j, e = ids[slot];
-      p.plan.slot_of_row[r] = slot;
+      p.plan.slot_of_row[r] = token * p.topk + j;
+      p.plan.scale_row[r] = place[j].y;
       p.x_rows.unit[r] = unit;
-      if constexpr (kBlock == 16) {
-        const float bound = __fmul_rn(p.amax[p.amax_per_expert ? e : 0], sum);
-        p.h_unit[r] = unit_of(fminf(__fmul_rn(2.0f * bound, bound), kFltMax));
-      } else {
-        p.h_unit[r] = 1.0f;
-      }
+      if (kBlock == 32) p.h_unit[r] = 1.0f;
     }
     if (k < p.width)
 #pragma unroll
@@ -201,6 +191,54 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
     if (k < (p.width + 63) / 64 * 64)
       put_scale<kBlock>(p.x_rows.scales + seg * tiles * kScaleTile, n0, k, scale);
   }
+}
+
+// NVFP4: the hidden rows into terms, a CTA kPrepPart elements of one.
+struct CutArgs {
+  const float* hidden;  // [sorted slot][width]
+  int width;
+  Rows rows;
+  Plan plan;
+};
+
+__global__ void __launch_bounds__(kPrepThreads) cut_hidden_kernel(const __grid_constant__ CutArgs p) {
+  __shared__ float largest[kPrepWarps];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int parts = (p.width + kPrepPart - 1) / kPrepPart;
+  const int r = blockIdx.x / parts, part = blockIdx.x % parts;
+  // (first the wait: the next kernel reads what precedes this one ahead of its own)
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (r >= __ldcg(&p.plan.counts[1])) return;
+  const float* row = p.hidden + (int64_t)r * p.width;
+  const int64_t k = (int64_t)part * kPrepPart + 128 * w + 4 * lane;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (k < p.width) {
+    const float4 u = __ldcg(reinterpret_cast<const float4*>(row + k));
+    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+  }
+  float m = 0.0f;  // the row's largest finite element
+#pragma unroll 2
+  for (int i = 4 * tid; i < p.width; i += 4 * kPrepThreads) {
+    const float4 u = __ldcg(reinterpret_cast<const float4*>(row + i));
+    m = fmaxf(fmaxf(m, finite_magnitude(u.x)), fmaxf(finite_magnitude(u.y), fmaxf(finite_magnitude(u.z), finite_magnitude(u.w))));
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  if (lane == 0) largest[w] = m;
+  __syncthreads();
+  m = largest[0];
+#pragma unroll
+  for (int i = 1; i < kPrepWarps; ++i) m = fmaxf(m, largest[i]);
+  const float unit = unit_of(m);
+  if (part == 0 && tid == 0) p.rows.unit[r] = unit;
+  const int64_t tiles = (p.width + 63) / 64, row_bytes = p.width / 2;
+  const int at = __ldcg(&p.plan.scale_row[r]);
+  const uint32_t scale = to_terms<16>(v, unit, [&](int i, uint16_t codes) {
+    if (k < p.width) *reinterpret_cast<uint16_t*>(p.rows.codes + ((int64_t)r * kTerms + i) * row_bytes + k / 2) = codes;
+  });
+  if (k < tiles * 64)  // (the last ones padded to a step of 64 with zeros)
+    put_scale<16>(p.rows.scales + at / kScaleRows * tiles * kScaleTile, at % kScaleRows, k, scale);
 }
 
 // ---------------------------------------------------------------------------
@@ -221,7 +259,8 @@ struct MlpKernelArgs {
   int slots;
   Plan plan;
   Rows in;                   // the activations' terms
-  Rows out;                  // up: the hidden rows'
+  float* hidden;             // up, NVFP4: the hidden rows, [sorted slot][inner]
+  Rows out;                  // up, MXFP4: the hidden rows' terms
   const float* gates;        // down
   float* parts;              // down: [slots][rows]
   int tiles;                 // of an expert's weights
@@ -299,7 +338,7 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
   // waited for its own predecessor before it let this one begin.
   int segs;
   if constexpr (kDown)
-    segs = __ldcg(p.plan.segments);  // (two kernels back; from L2, as this memory served earlier calls)
+    segs = __ldcg(p.plan.counts);  // (two kernels back or more; from L2, as this memory served earlier calls)
   else
     group_slots(p.ids, p.slots, p.experts, kTok, ids, row0, seg0, kThreads), segs = seg0[p.experts];
   tcgen05_before_sync();
@@ -500,16 +539,14 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
       // this CTA's tokens of the segment, all or its share
       const int first = split == 1 ? 0 : rank * own, mine = max(0, min(split == 1 ? kTok : own, seg.z - first));
       // what lane n needs to know of token first + n, ahead of the sums
-      float unit = 0.0f, more = 0.0f;  // of its terms; down: its gate, up: the unit of its hidden row's terms
+      float unit = 0.0f, gate_of = 0.0f;  // of its terms; down: its gate
       int slot = 0;
       if (lane < mine) {
         const int row = seg.y + first + lane;
         unit = __fmul_rn(p.in.unit[row], factor);
         if constexpr (kDown) {
           slot = p.plan.slot_of_row[row];
-          more = p.gates[slot];
-        } else {
-          more = p.out.unit[row];
+          gate_of = p.gates[slot];
         }
       }
       ok = mbar_wait(&bar->tfull[buf], tphase);
@@ -557,7 +594,7 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
         const int o = kWeights * tile + r;
         for (int n = 0; n < mine; ++n) {
           const float v = __fmul_rn(results[n * kWeights + r], __shfl_sync(0xFFFFFFFFu, unit, n));
-          const float weighted = __fmul_rn(v, __shfl_sync(0xFFFFFFFFu, more, n));
+          const float weighted = __fmul_rn(v, __shfl_sync(0xFFFFFFFFu, gate_of, n));
           const int64_t to = (int64_t)__shfl_sync(0xFFFFFFFFu, slot, n) * p.rows + o;
           if (o < p.rows) p.parts[to] = weighted;
         }
@@ -569,7 +606,7 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
         for (int n = 2 * w + (lane >> 4); n - (lane >> 4) < mine; n += 2 * kOutWarps) {
           const bool there = n < mine;
           const int row = seg.y + first + n;
-          const float x_unit = __shfl_sync(0xFFFFFFFFu, unit, n & 31), h_unit = __shfl_sync(0xFFFFFFFFu, more, n & 31);
+          const float x_unit = __shfl_sync(0xFFFFFFFFu, unit, n & 31);
           float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           if (there && f < p.inner) {
             const float4 a = *reinterpret_cast<const float4*>(results + n * kWeights + 4 * (lane & 15));
@@ -581,12 +618,17 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
               v[i] = __fmul_rn(__fdiv_rn(z, __fadd_rn(1.0f, expf(-z))), __fmul_rn(up[i], x_unit));
             }
           }
-          uint8_t* codes_at = p.out.codes + (int64_t)row * kTerms * (p.inner / 2) + f / 2;
-          const uint32_t scale = to_terms<kBlock>(v, there ? h_unit : 1.0f, [&](int i, uint16_t codes) {
-            if (there && f < p.inner) *reinterpret_cast<uint16_t*>(codes_at + (int64_t)i * (p.inner / 2)) = codes;
-          });
-          if (there)
-            put_scale<kBlock>(p.out.scales + segment * out_tiles * kScaleTile, (first + n) * kTerms, f, scale);
+          if constexpr (kBlock == 16) {
+            if (there && f < p.inner)
+              *reinterpret_cast<float4*>(p.hidden + (int64_t)row * p.inner + f) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+            uint8_t* codes_at = p.out.codes + (int64_t)row * kTerms * (p.inner / 2) + f / 2;
+            const uint32_t scale = to_terms<kBlock>(v, 1.0f, [&](int i, uint16_t codes) {
+              if (there && f < p.inner) *reinterpret_cast<uint16_t*>(codes_at + (int64_t)i * (p.inner / 2)) = codes;
+            });
+            if (there)
+              put_scale<kBlock>(p.out.scales + segment * out_tiles * kScaleTile, (first + n) * kTerms, f, scale);
+          }
         }
         together(true);  // the results may be overwritten
       }
@@ -662,6 +704,7 @@ int64_t most_segments(const ExpertMlpArgs& a) {
 // The workspace, cut into its parts.
 struct Workspace {
   Rows x, h;
+  float* hidden;
   Plan plan;
   float* parts;
   size_t bytes;
@@ -682,9 +725,11 @@ Workspace cut(const ExpertMlpArgs& a) {
   ws.h.codes = take(slots * kTerms * (a.inner / 2));
   ws.h.scales = take(segs * ((a.inner + per - 1) / per) * kScaleTile);
   ws.h.unit = reinterpret_cast<float*>(take(4 * slots));
-  ws.plan.segments = reinterpret_cast<int32_t*>(take(4));
+  ws.hidden = reinterpret_cast<float*>(take(a.block == 16 ? 4 * slots * a.inner : 0));
+  ws.plan.counts = reinterpret_cast<int32_t*>(take(8));
   ws.plan.table = reinterpret_cast<int4*>(take(16 * segs));
   ws.plan.slot_of_row = reinterpret_cast<int32_t*>(take(4 * slots));
+  ws.plan.scale_row = reinterpret_cast<int32_t*>(take(4 * slots));
   ws.parts = reinterpret_cast<float*>(take(4 * slots * a.hidden));
   ws.bytes = used;
   return ws;
@@ -738,9 +783,16 @@ cudaError_t launch_products(const ExpertMlpArgs& a, const Workspace& ws, const L
   p.ids = a.ids;
   p.slots = (int)slots;
   MlpKernelArgs up = p, down = p;
-  up.rows = (int)(2 * a.inner), up.width = (int)a.hidden, up.in = ws.x, up.out = ws.h;
+  up.rows = (int)(2 * a.inner), up.width = (int)a.hidden, up.in = ws.x, up.out = ws.h, up.hidden = ws.hidden;
   down.rows = (int)a.hidden, down.width = (int)a.inner, down.in = ws.h;
-  const cudaError_t e = launch_product<false, kTok, kBlock>(a.up, up, slots, used, ctx);
+  cudaError_t e = launch_product<false, kTok, kBlock>(a.up, up, slots, used, ctx);
+  if (e == cudaSuccess && kBlock == 16) {
+    CutArgs c = {ws.hidden, (int)a.inner, ws.h, ws.plan};
+    void* args[] = {&c};
+    e = launch_dependent(reinterpret_cast<const void*>(cut_hidden_kernel),
+                         dim3((unsigned)(slots * ((a.inner + kPrepPart - 1) / kPrepPart))), dim3(kPrepThreads), 0, ctx.stream,
+                         args);
+  }
   return e != cudaSuccess ? e : launch_product<true, kTok, kBlock>(a.down, down, slots, used, ctx);
 }
 
@@ -750,8 +802,6 @@ cudaError_t launch_layer(const ExpertMlpArgs& a, const LaunchCtx& ctx) {
   PrepArgs p = {};
   p.x = static_cast<const uint16_t*>(a.x);
   p.ids = a.ids;
-  p.amax = a.up.amax;
-  p.amax_per_expert = a.up.amax_per_row;
   p.slots = (int)(a.tokens * a.topk);
   p.topk = a.topk;
   p.experts = a.experts;

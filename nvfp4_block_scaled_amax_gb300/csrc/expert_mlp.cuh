@@ -94,6 +94,11 @@ __device__ __forceinline__ void put_scale(uint8_t* segment, int n0, int64_t elem
     if (term < kTerms) tile[n % 32 * 16 + n / 32 * 4] = (uint8_t)byte;
   }
 }
+// A number's magnitude, of what is not finite 0.
+__device__ __forceinline__ float finite_magnitude(float v) {
+  const float a = fabsf(v);
+  return a <= kFltMax ? a : 0.0f;
+}
 // Power of two at which scales up to 448 reach a sixth of `largest`.
 __device__ __forceinline__ float unit_of(float largest) {
   const int e = (int)(__float_as_uint(largest) >> 23) - 127;  // floor(log2)

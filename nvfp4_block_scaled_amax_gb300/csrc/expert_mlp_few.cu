@@ -7,9 +7,11 @@
 //
 // The first kernel cuts x into terms itself, each CTA its share of the
 // contracted dimension, while the first weights are on their way; both tokens
-// are columns for every expert, whoever chose it.  The second one sums over all
-// chosen experts of a row tile in one cluster, an accumulator each, and so has
-// y in hand.
+// are columns for every expert, whoever chose it.  It leaves the hidden rows in
+// FP32, with the largest value of each tile of 64, and the second one cuts them
+// the same way, a stage at a time, as the row's largest value is known by then.  It
+// sums over all chosen experts of a row tile in one cluster, an accumulator
+// each, and so has y in hand.
 #include "expert_mlp.cuh"
 
 namespace nvfp4 {
@@ -35,9 +37,9 @@ struct FewArgs {
   int amax_per_expert;
   int rows, width, inner;
   int tiles;             // of an expert's weights
-  uint8_t* h_codes;      // [experts chosen][kBN][inner / 2]
-  uint8_t* h_scales;     // [experts chosen][scale tiles][512]
-  float* h_unit;         // [experts chosen][kTok]
+  float* hidden;         // [experts chosen][kTok][inner]
+  float* largest;        // [experts chosen][kTok][h_tiles]: the largest finite magnitudes of 64 each
+  int h_tiles;
   uint16_t* y;           // down
   unsigned* status;
 };
@@ -54,7 +56,8 @@ struct Barriers {
   uint64_t terms;        // up: x's terms are there
   uint64_t got, taken;   // the cluster's partial results
   uint32_t tmem;
-  float largest[kTermWarps][kTok], sums[kTermWarps][kTok];
+  float largest[kTermWarps][kTok];      // up: of x
+  float unit[kTok * kMaxChoices];       // down: of the hidden rows' terms
   Chosen chosen;
 };
 
@@ -89,37 +92,44 @@ struct Layout {
   }
 };
 
-// x's largest finite element and its sum of magnitudes: warp `me` of kTermWarps, its part.
+// x's largest finite element: warp `me` of kTermWarps, its part.
 __device__ __forceinline__ void look_at_x(const FewArgs& p, int me, Barriers& bar) {
   const int lane = threadIdx.x & 31;
   for (int token = 0; token < p.tokens; ++token) {
     const uint4* row = reinterpret_cast<const uint4*>(p.x + (int64_t)token * p.width);
-    float m = 0.0f, sum = 0.0f;
+    float m = 0.0f;
 #pragma unroll 2
     for (int k = 32 * me + lane; k < p.width / 8; k += 32 * kTermWarps) {
       const uint4 u = __ldg(row + k);
       const float v[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
                           bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = fabsf(v[i]), b = a <= kFltMax ? a : 0.0f;
-        m = fmaxf(m, b), sum = __fadd_rn(sum, b);
-      }
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_magnitude(v[i]));
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-      sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, d));
-    }
-    if (lane == 0) bar.largest[me][token] = m, bar.sums[me][token] = sum;
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    if (lane == 0) bar.largest[me][token] = m;
   }
+}
+
+// 128 elements of a token (four a lane, from k on, the lane's first) into a
+// stage's terms: rows of 128 bytes, 16-byte places swizzled by the row, and behind
+// them (`scales`) the blocks' scales.
+template <int kBlock>
+__device__ __forceinline__ void cut_part(float (&v)[4], float unit, int token, int k, uint8_t* codes_at, uint8_t* scales) {
+  const int in_stage = k % kStageK, b = in_stage / 2;
+  const uint32_t scale = to_terms<kBlock>(v, unit, [&](int i, uint16_t codes) {
+    const int n = token * kTerms + i;
+    *reinterpret_cast<uint16_t*>(codes_at + n * kStageRow + (((b >> 4) ^ (n & 7)) * 16) + (b & 15)) = codes;
+  });
+  put_scale<kBlock>(scales, token * kTerms, in_stage, scale);
 }
 
 // ---------------------------------------------------------------------------
 template <bool kDown, int kBlock>
 __global__ void __launch_bounds__(kThreads, 2)
-few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                  const __grid_constant__ FewArgs p, int stages, int split, int resident) {
+few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ FewArgs p, int stages, int split,
+                  int resident) {
   using L = Layout<kDown, kBlock>;
   using F = Format<kBlock>;
   extern __shared__ uint8_t smem_raw[];
@@ -134,7 +144,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
   if (w == kOutWarps) {
     if (lane == 0) {
       for (int i = 0; i < stages; ++i) {
-        mbar_init(&bar->full[i], 2);
+        mbar_init(&bar->full[i], kDown ? 2 + 2 * p.tokens : 2);  // the copies, the weights' scales (and the terms)
         mbar_init(&bar->empty[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
@@ -146,7 +156,6 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
       mbar_init(&bar->taken, kOutWarps * split);
       fence_mbar_init();
       tma_prefetch_desc(&wmap);
-      if (kDown) tma_prefetch_desc(&xmap);
     }
   } else if (w == kOutWarps + 1) {
     tmem_alloc(&bar->tmem, L::kTmemCols);
@@ -160,7 +169,6 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     grid_launch_dependents();
   }
   if (w == 0) find_chosen(p, bar->chosen);
-  float sum[kTok] = {0.0f, 0.0f};
   if (!kDown && w != kOutWarps && w != kOutWarps + 1) look_at_x(p, w < kOutWarps ? w : w - 2, *bar);
   tcgen05_before_sync();
   __syncthreads();
@@ -186,9 +194,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
       float m = bar->largest[0][i];
-      sum[i] = bar->sums[0][i];
 #pragma unroll
-      for (int j = 1; j < kTermWarps; ++j) m = fmaxf(m, bar->largest[j][i]), sum[i] = __fadd_rn(sum[i], bar->sums[j][i]);
+      for (int j = 1; j < kTermWarps; ++j) m = fmaxf(m, bar->largest[j][i]);
       unit[i] = kBlock == 16 ? unit_of(m) : 1.0f;
     }
     // 128 elements of a token at a time, up to the last step of 64 padded with zeros
@@ -201,13 +208,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         const uint2 u = __ldg(reinterpret_cast<const uint2*>(p.x + (int64_t)token * p.width + k));
         v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
       }
-      const int in_stage = k % kStageK, b = in_stage / 2;
       uint8_t* stage = x_terms + (k / kStageK - i0) * L::kXBytes;
-      const uint32_t scale = to_terms<kBlock>(v, token == 0 ? unit[0] : unit[1], [&](int i, uint16_t codes) {
-        const int n = token * kTerms + i;  // (rows of 128 bytes, 16-byte places swizzled by the row)
-        *reinterpret_cast<uint16_t*>(stage + n * kStageRow + (((b >> 4) ^ (n & 7)) * 16) + (b & 15)) = codes;
-      });
-      put_scale<kBlock>(stage + L::kXCodes, token * kTerms, in_stage, scale);
+      cut_part<kBlock>(v, token == 0 ? unit[0] : unit[1], token, k, stage, stage + L::kXCodes);
     }
     fence_proxy_async_shared();
     __syncwarp();
@@ -215,8 +217,6 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
   };
 
   if (w == kOutWarps) {
-    const int scale_tiles = (p.width + 4 * kBlock - 1) / (4 * kBlock);
-    auto scale_bytes = [&](int kb) { return (uint32_t)min(F::kTiles, scale_tiles - kb * F::kTiles) * kScaleTile; };
     // Stage i of tile t: its expert (of those chosen) and its place along the contracted dimension.
     auto expert_of = [&](int t, int i) { return kDown ? i / nkb : t / p.tiles; };
     auto weights = [&](int t, int i, uint32_t s) {
@@ -224,19 +224,9 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
       const int row = chosen.expert[e] * p.rows + tile * kTileRows;
       if (elect_one()) {
         const uint32_t dst = smem_u32(smem + s * L::kStageBytes), full = smem_u32(&bar->full[s]);
-        mbar_arrive_expect_tx(&bar->full[s], L::kWCodes + (kDown ? L::kXCodes + scale_bytes(kb) : 0));
+        mbar_arrive_expect_tx(&bar->full[s], L::kWCodes);
         tma_load(dst, &wmap, kb * kStageRow, row, full);
         if (!kDown) tma_load(dst + L::kWCodes / 2, &wmap, kb * kStageRow, row + p.inner, full);
-      }
-      __syncwarp();
-    };
-    auto activations = [&](int i, uint32_t s) {  // down
-      const int e = i / nkb, kb = i - e * nkb;
-      if (elect_one()) {
-        const uint32_t dst = smem_u32(smem + s * L::kStageBytes) + L::kWCodes, full = smem_u32(&bar->full[s]);
-        tma_load(dst, &xmap, kb * kStageRow, e * kBN, full);
-        bulk_load(dst + L::kXCodes + F::kScaleBytes,
-                  p.h_scales + ((int64_t)e * scale_tiles + kb * F::kTiles) * kScaleTile, scale_bytes(kb), &bar->full[s]);
       }
       __syncwarp();
     };
@@ -258,7 +248,6 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
           }
           weights(t, i, s);
         }
-        if (kDown) activations(i, s);
         ++sent;
         if (++s == (uint32_t)stages) {
           s = 0;
@@ -363,6 +352,54 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
   } else {
     if (kDown) grid_dependency_wait(), grid_launch_dependents();
     else cut_x(w);
+    // down: the share's hidden rows into terms, parts of 128 elements dealt out to these warps: stage q / per_stage
+    // of the ring, of its expert the token and the half of the stage.  (A warp is one stage, or two of a token's,
+    // ahead of itself, which a ring of two allows.)
+    const int per_stage = 2 * p.tokens;
+    uint32_t used = 0;  // stages of the ring before this tile's
+    auto hidden_at = [&](int q, int& row, int& k) {
+      const int i = i0 + q / per_stage, e = i / nkb, at = q % per_stage;
+      row = kTok * e + (at >> 1), k = (i - e * nkb) * kStageK + 128 * (at & 1) + 4 * lane;
+    };
+    auto read_hidden = [&](int q, float (&v)[4]) {
+      int row, k;
+      hidden_at(q, row, k);
+      float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (q < per_stage * (i1 - i0) && k < p.width && (chosen.by >> row & 1))
+        u = __ldcg(reinterpret_cast<const float4*>(p.hidden + (int64_t)row * p.width + k));
+      v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+    };
+    auto cut_hidden = [&]() {
+      float next[4];
+      read_hidden(w, next);
+      for (int q = w; q < per_stage * (i1 - i0); q += kOutWarps) {
+        float v[4] = {next[0], next[1], next[2], next[3]};
+        read_hidden(q + kOutWarps, next);
+        const uint32_t use = used + q / per_stage, slot = use % stages;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar->empty[slot], ((use / stages) & 1) ^ 1))) return false;
+        int row, k;
+        hidden_at(q, row, k);
+        uint8_t* to = smem + slot * L::kStageBytes + L::kWCodes;
+        if (k - 4 * lane < p.width)
+          cut_part<kBlock>(v, kBlock == 16 ? bar->unit[row] : 1.0f, row % kTok, k, to, to + L::kXCodes + F::kScaleBytes);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->full[slot]);
+      }
+      used += i1 - i0;
+      return true;
+    };
+    if (kDown && kBlock == 16) {
+      for (int row = w; row < kTok * n_experts; row += kOutWarps) {
+        float m = 0.0f;
+        if (chosen.by >> row & 1)
+          for (int i = lane; i < p.h_tiles; i += 32) m = fmaxf(m, __ldcg(p.largest + row * p.h_tiles + i));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        if (lane == 0) bar->unit[row] = unit_of(m);
+      }
+      together(true);
+    }
     const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
     const int r = 32 * w + lane;
     uint32_t buf = 0, tphase = 0, round = 0;
@@ -374,13 +411,14 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
       for (int j = 0; j < p.topk; ++j)
         if (p.ids[token * p.topk + j] == e) gate = __fadd_rn(gate, p.gates[token * p.topk + j]);
       const float factor = kBlock == 16 ? __fdiv_rn(p.amax[p.amax_per_expert ? e : 0], 2688.0f) : 1.0f;
-      weight = __fmul_rn(__fmul_rn(p.h_unit[lane], factor), gate);
+      weight = __fmul_rn(__fmul_rn(kBlock == 16 ? bar->unit[lane] : 1.0f, factor), gate);
     }
     for (int t = t0; t < tiles && ok; t += step) {
       const int e0 = kDown ? 0 : t / p.tiles, tile = kDown ? t : t - e0 * p.tiles;
       // the tokens that this CTA finishes: all, or the one with its rank
       const int first = split == 1 ? 0 : rank, end = min(p.tokens, split == 1 ? kTok : rank + 1);
-      ok = mbar_wait(&bar->tfull[buf], tphase);
+      if (kDown) ok = cut_hidden();
+      ok = ok && mbar_wait(&bar->tfull[buf], tphase);
       if (ok && split > 1) ok = mbar_wait_cluster(&bar->taken, (round & 1) ^ 1, p.status);
       if (!(ok = together(ok))) break;
       tcgen05_after_sync();
@@ -440,12 +478,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         if (w == 0 && end > first) {
           const bool there = token < end && (chosen.by >> (kTok * e0 + token) & 1);
           const float x_unit = __fmul_rn(token == 0 ? unit[0] : unit[1], factor);
-          float h_unit = 1.0f;
-          if (kBlock == 16) {
-            const float bound = __fmul_rn(p.amax[p.amax_per_expert ? chosen.expert[e0] : 0], token == 0 ? sum[0] : sum[1]);
-            h_unit = unit_of(fminf(__fmul_rn(2.0f * bound, bound), kFltMax));
-          }
-          float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m = 0.0f;
           if (there && f < p.inner) {
             const float4 a = *reinterpret_cast<const float4*>(results + (token - first) * kWeights + 4 * (lane & 15));
             const float4 b = *reinterpret_cast<const float4*>(results + (token - first) * kWeights + 64 + 4 * (lane & 15));
@@ -454,17 +487,14 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             for (int i = 0; i < 4; ++i) {
               const float z = __fmul_rn(gate[i], x_unit);
               v[i] = __fmul_rn(__fdiv_rn(z, __fadd_rn(1.0f, expf(-z))), __fmul_rn(up[i], x_unit));
+              m = fmaxf(m, finite_magnitude(v[i]));
             }
+            *reinterpret_cast<float4*>(p.hidden + (int64_t)(kTok * e0 + token) * p.inner + f) =
+                make_float4(v[0], v[1], v[2], v[3]);
           }
-          const bool mine = token < end;
-          uint8_t* codes_at = p.h_codes + (int64_t)(e0 * kBN + token * kTerms) * (p.inner / 2) + f / 2;
-          const uint32_t scale = to_terms<kBlock>(v, h_unit, [&](int i, uint16_t codes) {
-            if (mine && f < p.inner) *reinterpret_cast<uint16_t*>(codes_at + i * (p.inner / 2)) = codes;
-          });
-          if (mine)
-            put_scale<kBlock>(p.h_scales + (int64_t)e0 * ((p.inner + 4 * kBlock - 1) / (4 * kBlock)) * kScaleTile,
-                              token * kTerms, f, scale);
-          if (mine && tile == 0 && (lane & 15) == 0) p.h_unit[kTok * e0 + token] = h_unit;
+#pragma unroll
+          for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+          if (there && (lane & 15) == 0) p.largest[(kTok * e0 + token) * p.h_tiles + tile] = m;
         }
         together(true);  // the results may be overwritten
       }
@@ -498,6 +528,7 @@ int64_t most_experts(const ExpertMlpArgs& a) {
   const int64_t slots = a.tokens * a.topk;
   return slots < a.experts ? slots : a.experts;
 }
+int64_t hidden_tiles(const ExpertMlpArgs& a) { return (a.inner + kWeights / 2 - 1) / (kWeights / 2); }
 // CTAs of a cluster that share a tile's stages: as many as fit beside one another, up to four, two stages each
 // at least (one token, two of 8 experts of 4096 x 2048: 14.4 us; up to eight 14.6, two 15.8, unshared 17.4).
 int split_of(int64_t tiles, int64_t stages, const LaunchCtx& ctx) {
@@ -506,26 +537,24 @@ int split_of(int64_t tiles, int64_t stages, const LaunchCtx& ctx) {
   return 1;
 }
 int up_split(const ExpertMlpArgs& a, const LaunchCtx& ctx) {
-  return split_of(most_experts(a) * ((a.inner + 63) / 64), stages_of(a.hidden), ctx);
+  return split_of(most_experts(a) * hidden_tiles(a), stages_of(a.hidden), ctx);
 }
 
 struct Workspace {
-  uint8_t *codes, *scales;
-  float* unit;
+  float *hidden, *largest;
   size_t bytes;
 };
 Workspace cut(const ExpertMlpArgs& a) {
   Workspace ws = {};
-  const int64_t experts = most_experts(a), per = 4 * a.block;
+  const int64_t rows = kTok * most_experts(a);
   uint8_t* at = static_cast<uint8_t*>(a.workspace);
   auto take = [&](int64_t bytes) {
     uint8_t* p = at + ws.bytes;
     ws.bytes += (size_t)((bytes + 127) / 128 * 128);
-    return p;
+    return reinterpret_cast<float*>(p);
   };
-  ws.codes = take(experts * kBN * (a.inner / 2));
-  ws.scales = take(experts * ((a.inner + per - 1) / per) * kScaleTile);
-  ws.unit = reinterpret_cast<float*>(take(4 * kTok * experts));
+  ws.hidden = take(4 * rows * a.inner);
+  ws.largest = take(4 * rows * hidden_tiles(a));
   return ws;
 }
 
@@ -539,12 +568,11 @@ cudaError_t launch_product(const ExpertMlpArgs& a, FewArgs p, const LaunchCtx& c
   p.scale = weights.scale;
   p.amax = weights.amax;
   p.amax_per_expert = weights.amax_per_row;
-  p.tiles = kDown ? (p.rows + kWeights - 1) / kWeights : (p.inner + kWeights / 2 - 1) / (kWeights / 2);
-  CUtensorMap wmap, xmap = {};
+  p.h_tiles = (int)hidden_tiles(a);
+  p.tiles = kDown ? (p.rows + kWeights - 1) / kWeights : p.h_tiles;
+  CUtensorMap wmap;
   cudaError_t e = make_fp8_tensor_map(&wmap, weights.data, (int64_t)p.experts * p.rows, p.width / 2,
                                       kDown ? kWeights : kWeights / 2);
-  if (e == cudaSuccess && kDown)
-    e = make_fp8_tensor_map(&xmap, p.h_codes, most_experts(a) * kBN, p.width / 2, kBN);
   if (e != cudaSuccess) return e;
   const int64_t tiles = kDown ? p.tiles : most_experts(a) * p.tiles;
   int split = kDown ? split_of(tiles, most_experts(a) * stages_of(p.width), ctx) : up_split(a, ctx);
@@ -558,7 +586,7 @@ cudaError_t launch_product(const ExpertMlpArgs& a, FewArgs p, const LaunchCtx& c
   e = allow_smem(reinterpret_cast<const void*>(kernel), kPerCta, allowed);
   if (e != cudaSuccess) return e;
   const int64_t room = 2 * ctx.num_sms / split;
-  void* args[] = {&wmap, &xmap, &p, &stages, &split, &resident};
+  void* args[] = {&wmap, &p, &stages, &split, &resident};
   return launch_dependent(reinterpret_cast<const void*>(kernel), dim3((unsigned)((tiles < room ? tiles : room) * split)),
                           dim3(kThreads), rest + stages * L::kStageBytes, ctx.stream, args, split);
 }
@@ -584,9 +612,8 @@ cudaError_t launch_few_tokens(const ExpertMlpArgs& a, const LaunchCtx& ctx) {
   p.tokens = (int)a.tokens;
   p.topk = a.topk;
   p.experts = a.experts;
-  p.h_codes = ws.codes;
-  p.h_scales = ws.scales;
-  p.h_unit = ws.unit;
+  p.hidden = ws.hidden;
+  p.largest = ws.largest;
   p.y = static_cast<uint16_t*>(a.y);
   p.status = ctx.status;
   const cudaError_t e = a.block == 16 ? launch_product<false, 16>(a, p, ctx) : launch_product<false, 32>(a, p, ctx);

@@ -13,7 +13,7 @@ function beside the call.
 For decoding, a whole layer of gated experts over 4-bit weights:
 
     up, down = quantize_experts(gate_up), quantize_experts(down)      # [E, 2 F, H], [E, H, F], once
-    y = expert_mlp(x, up, down, expert_ids, gates)                    # two to four launches
+    y = expert_mlp(x, up, down, expert_ids, gates)                    # two to five launches
 """
 from __future__ import annotations
 
