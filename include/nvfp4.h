@@ -555,9 +555,9 @@ nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, in
  * [experts][hidden][inner]; both of one format (block 16 or 32), compact scales,
  * amax one float, or with ROW_SCALED one for each expert.  A choice outside 0..num_experts - 1 (-1, say)
  * adds nothing; a token with none left gives zero.
- * Sums are FP32; x and h enter a product as sums of six 4-bit operands, which
- * leave at most 2^-17 (NVFP4) or 2^-16 (MXFP4) of the largest value of each block,
- * or 2^-34 of the largest of an NVFP4 row of x or h; y is rounded once.  A token with
+ * Sums are FP32; x and h enter a product as sums of eight 4-bit operands, which
+ * leave at most 2^-23 (NVFP4) or 2^-22 (MXFP4) of the largest value of each block,
+ * or 2^-40 of the largest of an NVFP4 row of x or h; y is rounded once.  A token with
  * an infinity or a NaN, in x or in h, gives NaN.
  * tokens * topk <= NVFP4_MAX_MLP_SLOTS, hidden and inner multiples of 32 up to
  * NVFP4_MAX_MLP_WIDTH.  workspace: nvfp4_expert_mlp_workspace bytes of device

@@ -11,20 +11,21 @@
 //
 // Terms.  A block (16 or 32 elements, as the weights') has one scale s, at which
 // its largest element is at most 6 (NVFP4: the next E4M3 number above a sixth of it,
-// MXFP4: the next power of two), and six rows of E2M1 codes, counting in s, s / 4, s /
+// MXFP4: the next power of two), and eight rows of E2M1 codes, counting in s, s / 4, s /
 // 32, s / 256, ...: a code of the first is off by at most s, which is 4 of the next
 // unit; from then on codes are off by at most half a unit, which is 4 of the next
-// again.  Six terms leave s 2^-15, which is 2^-17.4 (NVFP4) or 2^-16.5 (MXFP4) of the
-// block's largest element, far below the 2^-9 of the BF16 output.  Every step but the
-// choice of codes is exact in FP32, and the rows of a token are added with their
-// ratios after the product.  They are rows beside the others: N = 6 tokens, where
-// few rows leave an MMA's columns empty anyway.
+// again.  Eight terms leave s 2^-21, which is 2^-23.4 (NVFP4) or 2^-22.5 (MXFP4) of the
+// block's largest element, about what the FP32 sums lose: a BF16 element keeps all of
+// its own bits down to 2^-14 of its block's largest.  (Six left 2^-17.4 and took 2 to
+// 3 % less time.)  Every step but the choice of codes is exact in FP32, and the rows of a token are
+// added with their ratios after the product.  They are rows beside the others: N = 8
+// tokens, where few rows leave an MMA's columns empty anyway.
 // E4M3 scales span 17 powers of two; they count in units of their row, so that a
-// row's small blocks lose nothing until 2^-34 of its largest.  The unit comes from
+// row's small blocks lose nothing until 2^-40 of its largest.  The unit comes from
 // the row's largest element, which of a hidden row is not known before all of its
 // tiles are: NVFP4 keeps the hidden rows in FP32 and cuts them in a launch of their
 // own.  (A unit from a bound, |g|, |u| <= amax sum|x|, would spare the launch but
-// hold h to 2^-34 of a number that may be any multiple of it.)  MXFP4's powers
+// hold h to 2^-40 of a number that may be any multiple of it.)  MXFP4's powers
 // of two need no unit, and its hidden rows are cut where they are made.
 //
 // Four launches (NVFP4 five): slots sorted by expert and x into terms; gate and up
@@ -277,13 +278,13 @@ struct Barriers {
 template <int kTok, int kBlock>
 struct Layout {
   using F = Format<kBlock>;
-  static constexpr int kBN = (kTok * kTerms + 15) / 16 * 16;  // (the last rows of 16: of whichever segment follows)
+  static constexpr int kBN = kTok * kTerms;
   static constexpr int kWCodes = kWeights * kStageRow;
   static constexpr int kCodes = kWCodes + kBN * kStageRow;
   static constexpr int kStageBytes = kCodes + 2 * F::kScaleBytes;
   static constexpr int kCols = 2 * kBN + 2 * F::kCols;
   static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
-  static_assert(kCols <= 256 && kStageBytes % 1024 == 0, "tensor memory of two CTAs; swizzled operands");
+  static_assert(kBN % 16 == 0 && kCols <= 256 && kStageBytes % 1024 == 0, "tensor memory of two CTAs; swizzled operands");
   static constexpr int kResultBytes = kTok * kWeights * 4;  // a tile's results
   static __host__ __device__ int own(int split) { return (kTok + split - 1) / split; }  // tokens a CTA of a cluster joins
   static __host__ __device__ int share_bytes(int split) {
@@ -689,12 +690,13 @@ __global__ void __launch_bounds__(256) join_slots_kernel(const float* __restrict
 // Host side
 // ---------------------------------------------------------------------------
 // Tokens of a segment: more cost columns that few experts fill, fewer read the
-// weights of a popular expert again.  Eight where experts have four on average or
-// fewer (13 tokens, 4 of 16 experts of 2720 x 1184: 27.1 us against 30.3 with
-// sixteen); with eight on average there is no difference (64 tokens, 4 of 32
-// experts of 4096 x 1536: 72.4 and 71.5).
+// weights of a popular expert again.  Fourteen are the most whose columns fit twice into
+// half of the tensor memory, beside the scales.  Eight where experts have four on average
+// or fewer (13 tokens, 4 of 16 experts of 2720 x 1184: 27.1 us against 30.3 with
+// sixteen, six terms each); with eight on average there is no difference (64 tokens, 4
+// of 32 experts of 4096 x 1536: 72.4 and 71.5).
 int tokens_per_segment(int64_t tokens, int64_t slots, int64_t experts) {
-  return tokens <= 2 ? 2 : tokens <= 8 || slots <= 4 * experts ? 8 : 16;
+  return tokens <= 2 ? 2 : tokens <= 8 || slots <= 4 * experts ? 8 : 14;
 }
 int64_t most_segments(const ExpertMlpArgs& a) {
   const int64_t slots = a.tokens * a.topk, used = slots < a.experts ? slots : a.experts;
@@ -821,7 +823,7 @@ cudaError_t launch_layer(const ExpertMlpArgs& a, const LaunchCtx& ctx) {
   if (e != cudaSuccess) return e;
   e = p.tok == 2 ? launch_products<2, kBlock>(a, ws, ctx)
       : p.tok == 8 ? launch_products<8, kBlock>(a, ws, ctx)
-                   : launch_products<16, kBlock>(a, ws, ctx);
+                   : launch_products<14, kBlock>(a, ws, ctx);
   if (e != cudaSuccess) return e;
   int rows = (int)a.hidden, tokens = (int)a.tokens, topk = a.topk, experts = a.experts;
   const float* slots = ws.parts;

@@ -9,7 +9,7 @@
 namespace nvfp4 {
 namespace fp4 {
 
-constexpr int kTerms = 6;
+constexpr int kTerms = 8;
 
 // ---------------------------------------------------------------------------
 // Terms
@@ -51,9 +51,9 @@ __device__ __forceinline__ uint32_t to_terms(float (&v)[4], float unit, Put&& pu
     inv = byte == 0 ? 0.0f : __fdividef(1.0f, value);
     if (!(q <= 449.0f)) byte = 127u, inv = 0.0f;  // not finite: the whole row becomes NaN
   } else {
-    // the next power of two not below a sixth of the largest (and 2^-107, so that no term's leaves FP32's range)
+    // the next power of two not below a sixth of the largest (and 2^-105, so that no term's leaves FP32's range)
     const uint32_t bits = __float_as_uint(m), e = (bits >> 23) + ((bits & 0x7FFFFFu) > 0x400000u);
-    byte = e < 22u ? 20u : e - 2u;
+    byte = e < 24u ? 22u : e - 2u;
     value = __uint_as_float(byte << 23);
     inv = __uint_as_float((254u - byte) << 23);
     if (!(m <= kFltMax)) byte = 255u, inv = 0.0f;
@@ -99,10 +99,10 @@ __device__ __forceinline__ float finite_magnitude(float v) {
   const float a = fabsf(v);
   return a <= kFltMax ? a : 0.0f;
 }
-// Power of two at which scales up to 448 reach a sixth of `largest`.
+// Power of two at which scales up to 448 reach a sixth of `largest` (and 2^-95: as above).
 __device__ __forceinline__ float unit_of(float largest) {
   const int e = (int)(__float_as_uint(largest) >> 23) - 127;  // floor(log2)
-  return __uint_as_float((uint32_t)(max(-100, e - 10) + 127) << 23);
+  return __uint_as_float((uint32_t)(max(-95, e - 10) + 127) << 23);
 }
 
 __device__ __forceinline__ void store_async(uint32_t dst, float v, uint32_t bar) {
