@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
   float m = 0.0f;
 #pragma unroll 2
   for (int k = 8 * tid; k < p.width; k += 8 * kPrepThreads) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + k));
+    const uint4 u = *reinterpret_cast<const uint4*>(row + k);
     const float v[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
                         bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
 #pragma unroll
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
   const int64_t tiles = (p.width + 4 * kBlock - 1) / (4 * kBlock), row_bytes = p.width / 2;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (k < p.width) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + k));
+    const uint2 u = *reinterpret_cast<const uint2*>(row + k);
     v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
   }
   uint16_t codes[kTerms];
@@ -495,6 +495,7 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
   } else if (w > kOutWarps + 1) {
     const int mine = w - kOutWarps - 2, active = active_scale_warps(stages);
     bool waited = false;
+    stale_lines_gone();
     if (mine < active) {
       uint32_t s = 0, phase = 1, it = 0;
       const CompactScales<kBlock> scales(p.scale, p.width, (int64_t)p.experts * p.rows);
@@ -503,7 +504,8 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
         for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
           if ((it & (active - 1)) == (uint32_t)mine) {
             uint32_t v[4][F::kTiles];
-            scales.read(r0, kWeights, kb, v, kDown ? 0 : p.inner - kWeights / 2);
+            const int64_t gap = kDown ? 0 : p.inner - kWeights / 2;
+            scales.read(r0, kWeights, kb, v, gap);
             if (!waited && it >= (uint32_t)stages) {
               grid_dependency_wait();
               grid_launch_dependents();
@@ -658,8 +660,8 @@ expert_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_con
 }
 
 // y[t] = the sum of a token's weighted results in the order of its choices.
-__global__ void __launch_bounds__(256) join_slots_kernel(const float* __restrict__ parts, const int32_t* __restrict__ ids,
-                                                         int topk, int experts, int rows, int tokens, uint16_t* y) {
+__global__ void __launch_bounds__(256) join_slots_kernel(const float* parts, const int32_t* ids, int topk,
+                                                         int experts, int rows, int tokens, uint16_t* y) {
   grid_begin();
   const int per = rows / 4;
   for (int i = blockIdx.x * 256 + threadIdx.x; i < tokens * per; i += gridDim.x * 256) {

@@ -100,7 +100,7 @@ __device__ __forceinline__ void look_at_x(const FewArgs& p, int me, Barriers& ba
     float m = 0.0f;
 #pragma unroll 2
     for (int k = 32 * me + lane; k < p.width / 8; k += 32 * kTermWarps) {
-      const uint4 u = __ldg(row + k);
+      const uint4 u = row[k];
       const float v[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
                           bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
 #pragma unroll
@@ -205,7 +205,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
       if (k - 4 * lane >= p.width) continue;
       float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       if (k < p.width) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p.x + (int64_t)token * p.width + k));
+        const uint2 u = *reinterpret_cast<const uint2*>(p.x + (int64_t)token * p.width + k);
         v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
       }
       uint8_t* stage = x_terms + (k / kStageK - i0) * L::kXBytes;
@@ -321,7 +321,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     }
     if (!ok) report_timeout(p.status);
   } else if (w > kOutWarps + 1) {
-    if (kDown) grid_launch_dependents();
+    bool waited = !kDown;
+    if (kDown) stale_lines_gone();
     const int mine = w - kOutWarps - 2, active = active_scale_warps(stages);
     if (!kDown) cut_x(kOutWarps + mine);
     if (mine < active) {
@@ -332,8 +333,13 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
           if ((it & (active - 1)) == (uint32_t)mine) {
             const int e = kDown ? i / nkb : t / p.tiles, kb = kDown ? i - e * nkb : i, tile = kDown ? t : t - e * p.tiles;
             uint32_t v[4][F::kTiles];
-            scales.read((int64_t)chosen.expert[e] * p.rows + tile * kTileRows, kWeights, kb, v,
-                        kDown ? 0 : p.inner - kWeights / 2);
+            const int64_t row = (int64_t)chosen.expert[e] * p.rows + tile * kTileRows, gap = kDown ? 0 : p.inner - kWeights / 2;
+            if (!waited && it >= (uint32_t)stages) {
+              grid_dependency_wait();
+              grid_launch_dependents();
+              waited = true;
+            }
+            scales.read(row, kWeights, kb, v, gap);
             ok = mbar_wait(&bar->empty[s], phase);
             if (ok) {
               scales.write(smem_u32(smem + s * L::kStageBytes) + L::kWCodes + (kDown ? L::kXCodes : 0), v);
@@ -348,6 +354,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
           }
         }
       if (!ok) report_timeout(p.status);
+    }
+    if (!waited) {
+      grid_dependency_wait();
+      grid_launch_dependents();
     }
   } else {
     if (kDown) grid_dependency_wait(), grid_launch_dependents();

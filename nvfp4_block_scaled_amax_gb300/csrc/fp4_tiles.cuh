@@ -137,6 +137,12 @@ __device__ __forceinline__ const uint8_t* swizzled_at(const Fp4Side& s, int64_t 
 // of a row are 16 (MXFP4: 8) bytes; where rows are not multiples of so many they
 // lie at any alignment and are put together from two aligned groups of so many
 // bytes, each of which holds at least one byte of the row.
+//
+// A kernel may begin before the one that writes its operands ends, so scales are
+// not constant while it runs: no .nc loads.  Warps that read ahead of the wait for the
+// kernel before fence first (stale_lines_gone).  L1 is of use where a row's stages share
+// sectors (4096 x 4096 x 4128 44 us, past L1 54); whole sectors are better off without
+// it (8192 x 8192 x 8192 167 us past L1, 179 through it).
 template <int kBlock>
 struct CompactScales {
   static constexpr int kWords = Format<kBlock>::kTiles, kGroup = 4 * kWords;
@@ -152,10 +158,12 @@ struct CompactScales {
 
   static __device__ __forceinline__ void group(const uint8_t* p, bool there, uint32_t* w) {
     if constexpr (kWords == 4) {
-      const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+      const uint4* q = reinterpret_cast<const uint4*>(p);
+      const uint4 v = there ? *q : make_uint4(0, 0, 0, 0);
       w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else {
-      const uint2 v = there ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+      const uint2* q = reinterpret_cast<const uint2*>(p);
+      const uint2 v = there ? *q : make_uint2(0, 0);
       w[0] = v.x, w[1] = v.y;
     }
   }
@@ -240,11 +248,11 @@ struct CompactScales {
         group(p + kGroup, row + 32 * g < rows && two, w + kWords);
       } else if (row + 32 * g < rows) {
         if constexpr (kWords == 4) {
-          asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+          asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                        : "l"(p));
         } else {
-          const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+          const uint4 q = *reinterpret_cast<const uint4*>(p);
           w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
         }
       }
@@ -258,6 +266,13 @@ struct CompactScales {
       sts_v4(to + j * kScaleTile + 16 * (threadIdx.x & 31), v[0][j], v[1][j], v[2][j], v[3][j]);
   }
 };
+
+// Ahead of the wait for the kernel before, a warp reads what kernels wrote that were over
+// before that one let this one begin.  They have written to L2, but L1 may hold lines of
+// the same memory from earlier calls (weights that are loaded anew in place); loads
+// behind a fence do not take those.  (Reading past L1 instead: 13 tokens, 4 of 16 experts of
+// 2720 x 1184 29.5 us, with the fence 27.8, as without either.)
+__device__ __forceinline__ void stale_lines_gone() { __threadfence(); }
 
 // The stages are dealt out to the warps that do this, so that the loads of
 // several are in flight; to no more warps than there are slots, for a warp's stage

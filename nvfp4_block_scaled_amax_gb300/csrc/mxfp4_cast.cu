@@ -387,11 +387,12 @@ __device__ __forceinline__ void decode8(uint32_t q, float s, float (&v)[8]) {
   }
 }
 
-// A thread reads half a block, 8 bytes, and writes its 16 values.
+// A thread reads half a block, 8 bytes, and writes its 16 values.  (The operand may be
+// written by the kernel before, beside which this one begins: nothing here is __restrict__.)
 template <bool kOutBf16>
-__global__ void __launch_bounds__(kThreads) mxfp4_dequantize_kernel(const uint8_t* __restrict__ data,
-                                                                    const uint8_t* __restrict__ scale, int64_t halves,
-                                                                    int64_t cols, int swizzled, void* out) {
+__global__ void __launch_bounds__(kThreads) mxfp4_dequantize_kernel(const uint8_t* data, const uint8_t* scale,
+                                                                    int64_t halves, int64_t cols, int swizzled,
+                                                                    void* out) {
   grid_begin();
   const int64_t per_row = cols / 16;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < halves; i += (int64_t)gridDim.x * kThreads) {
