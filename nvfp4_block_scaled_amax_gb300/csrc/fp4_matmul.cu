@@ -23,8 +23,8 @@
 // alone (one MMA a stage) take 80 us, about as long as the MMAs alone at this clock:
 // the two bound it together.  Without the scales' way into tensor memory it would
 // be 95; each half of B's scales sent to both CTAs at once (multicast) changes nothing.
-// 4096 x 4096 x 4096: swizzled scales 26 us, with an amax for each row of both 26.3 (75 when
-// every warp worked the columns' factors out for itself), compact scales 31.
+// 4096 x 4096 x 4096: swizzled scales 25.5 us, with an amax for each row of both 26.3 (75 when
+// every warp worked the columns' factors out for itself), compact scales 32.
 #include "fp4_tiles.cuh"
 
 namespace nvfp4 {
@@ -44,6 +44,7 @@ struct __align__(16) Barriers {
   uint64_t full[kStages], empty[kStages], tfull[2], tempty;
   uint32_t tmem;
   uint32_t pad;
+  uint4 heard;  // (word of the second CTA's pieces; nobody reads it)
 };
 
 template <int kBlock>
@@ -55,6 +56,18 @@ struct Layout {
   static_assert(kStageBytes % 1024 == 0, "swizzled operands");
   static_assert(kScaleCols + 3 * Format<kBlock>::kCols <= 512, "tensor memory");
 };
+
+// Word to the first CTA that a piece of scales of the second is in its place.  A thread
+// of the first CTA issues the copies that read it, so the hand-over is one between
+// CTAs.  An arrival would have to release at cluster scope, for which a warp waits about a
+// microsecond (4096 x 4096 x 4096 45 us, 8192 x 8192 x 8192 292; 60 and 420 if an idle
+// warp does it for all).  The bytes of an asynchronous store are counted on the
+// barrier with such a release, and the warp goes on: 32 and 191 us.  (An arrival of CTA
+// scope, which promises nothing to the other CTA, takes 28.5 and 168.)
+constexpr int kWord = 16;
+__device__ __forceinline__ void tell_first(Barriers* bar, int slot) {
+  store_async(map_to_cta(smem_u32(&bar->heard), 0), 0.0f, 0.0f, 0.0f, 0.0f, map_to_cta(smem_u32(&bar->full[slot]), 0));
+}
 
 // An item: a tile of 256 x 256, or its left or right half.
 struct Item {
@@ -80,7 +93,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   if (w == 0) {
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) {
-        mbar_init(&bar->full[i], 1 + 2 * pieces);  // the copies (and the pieces of each CTA)
+        mbar_init(&bar->full[i], 1 + pieces);  // the copies (word of the second CTA's pieces among them); the first's pieces
         mbar_init(&bar->empty[i], 1);
       }
       mbar_init(&bar->tfull[0], 1);
@@ -134,7 +147,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
         if (elect_one()) {
           if (rank == 0)
             mbar_arrive_expect_tx(&bar->full[s], 2 * (kCodes + (p.a.swizzled ? L::kScales : 0) +
-                                                      (p.b.swizzled ? 2 * L::kScales : 0)));
+                                                      (p.b.swizzled ? 2 * L::kScales : 0)) + pieces * kWord);
           const uint32_t dst = smem_u32(smem + s * L::kStageBytes);
           const uint32_t full = map_to_cta(smem_u32(&bar->full[s]), 0);
           tma_load_pair(dst, &amap, kb * kStageRow, arow, full);
@@ -172,7 +185,7 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
       tphase ^= 1;
       const uint32_t d = tmem + buf * kSecond;
       for (int kb = 0; kb < nkb; ++kb) {
-        if (!mbar_wait(&bar->full[s], phase)) {
+        if (!(pieces ? mbar_wait_acquire(&bar->full[s], phase) : mbar_wait(&bar->full[s], phase))) {
           ok = false;
           break;
         }
@@ -213,10 +226,10 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
     if (!ok) report_timeout(p.status);
   } else if (w >= kFirstScale && w < kFirstScale + kPairScaleWarps) {
     // A warp puts a piece of two stages in order, whose loads are in flight together: a
-    // row's 16 bytes of one stage are half a sector (4096 x 4096 x 4096 31 us, a stage at
-    // a time 35).  At most three pairs of stages are dealt out at once: a warp that
-    // wrote stage i waits for stage i + 5 next, or an earlier one; it knows that stage i -
-    // kStages is over, so what it waits for is at most one phase of the barrier away.
+    // row's 16 bytes of one stage are half a sector (a stage at a time took 13 % longer).
+    // At most three pairs of stages are dealt out at once: a warp that wrote stage i
+    // waits for stage i + 5 next, or an earlier one; it knows that stage i - kStages is
+    // over, so what it waits for is at most one phase of the barrier away.
     static_assert(kStages == 5, "three pairs");
     const int active = min(kPairScaleWarps, 3 * pieces);
     if (w - kFirstScale < active) {
@@ -246,12 +259,14 @@ matmul_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
               ok = ok && mbar_wait(&bar->empty[slot[h]], use[h]);
               if (!ok) break;
               if (there) of_a.write(smem_u32(smem + slot[h] * L::kStageBytes) + kCodes + piece * L::kScales, v[h]);
-              // What the first CTA's tensor-core copies read here is ordered by the
-              // fence; the arrival carries nothing else, so it needs no cluster-scope
-              // release, which would wait for every load in flight.
               fence_proxy_async_shared();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&bar->full[slot[h]]), 0));
+              if (lane == 0) {
+                if (rank == 0)
+                  mbar_arrive(&bar->full[slot[h]]);
+                else
+                  tell_first(bar, slot[h]);
+              }
             }
           }
           s = two ? slot[1] : slot[0], phase = two ? use[1] : use[0];

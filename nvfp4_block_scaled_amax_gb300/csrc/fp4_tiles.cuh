@@ -28,6 +28,7 @@ using fp8::mbar_arrive;
 using fp8::mbar_arrive_cluster;
 using fp8::mbar_arrive_cluster_release;
 using fp8::mbar_wait;
+using fp8::mbar_wait_acquire;
 using fp8::mbar_wait_cluster;
 using fp8::operand_desc;
 using fp8::report_timeout;

@@ -180,6 +180,19 @@ __device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return mbar_wait_at(smem_u32(bar), parity);
 }
+// The same, for what threads of other CTAs of the cluster released with their arrivals.
+__device__ __forceinline__ bool mbar_wait_acquire(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 524288;\n"
+      "W:\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n @p bra D;\n"
+      " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra W;\n"
+      "D:\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // One warp's role gave up waiting: for nvfp4_device_status.
 __device__ __forceinline__ void report_timeout(unsigned* status) { atomicOr(status, kStatusWaitTimeout); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
