@@ -28,7 +28,8 @@ few tokens (``experts``).
 
 Paths for "1d" / "2d" / "rht": "single_pass" (one persistent kernel: amax,
 grid barrier, cast; x read from HBM once; needs a small workspace, which
-this module keeps per device and stream) and "two_pass" (an amax kernel,
+this module keeps per device and stream, or takes from the graph that is
+being captured) and "two_pass" (an amax kernel,
 then the cast kernel; needed for skip_amax).  "auto" picks single_pass for
 1d / 2d when it applies and two_pass for rht (measured faster there).
 """
@@ -162,7 +163,11 @@ _workspaces: dict = {}
 def single_pass_workspace(device: torch.device, stream: int) -> torch.Tensor:
     """The zero-initialised workspace of the single-pass kernels for one
     device and stream (calls on one stream never overlap, so they may share
-    it; the kernels leave it ready for the next call)."""
+    it; the kernels leave it ready for the next call).  While the current
+    stream is captured each call gets its own, zeroed in the graph: graphs
+    captured on one stream may run at the same time."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(_lib.SINGLE_PASS_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
     key = (device.index, stream)
     ws = _workspaces.get(key)
     if ws is None:
@@ -272,7 +277,8 @@ class QuantizePlan:
     the flags, the output struct and, for the single-pass path, the
     workspace -- and each call then only passes them to the library with the
     stream.  The tensors must stay allocated, at the same addresses, for the
-    plan's lifetime (the plan keeps references to them).  Arguments as
+    plan's lifetime (the plan keeps references to them).  Plans captured into
+    graphs that may run at the same time need a workspace each.  Arguments as
     ``quantize``; ``out`` defaults to buffers allocated here.
 
         plan = QuantizePlan(x, "2d", swizzled=True)
