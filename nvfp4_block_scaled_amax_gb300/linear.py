@@ -42,10 +42,28 @@ def quantize_linear(weight: torch.Tensor, format: str = "mxfp4", training: bool 
     return _cast(weight, format, training, "2d" if weight.dim() == 2 and weight.shape[0] % 16 == 0 else "1d")
 
 
+def _weight_shape(weight: torch.Tensor | FP4Tensor | NVFP4Tensor) -> tuple[int, int]:
+    if isinstance(weight, torch.Tensor):
+        if weight.dim() != 2:
+            raise ValueError("a linear layer takes matrices")
+        return tuple(weight.shape)
+    if weight.row is None:
+        raise ValueError("the product needs the row-wise cast of the weight")
+    N, half = weight.row.data.shape
+    return N, 2 * half
+
+
 def linear_layer(x: torch.Tensor, weight: torch.Tensor | FP4Tensor | NVFP4Tensor, format: str = "mxfp4",
                  training: bool = True) -> tuple[torch.Tensor, LinearSaved | None]:
     """y = x weight^T [T, N] in x's type, x [T, K] bfloat16 or float32, weight [N, K] or its casts
     (``quantize_linear``).  K a multiple of 32; training: T and N too, and what ``linear_layer_grad`` needs is kept."""
+    N, K = _weight_shape(weight)
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x [T, {K}] for a weight [{N}, {K}], got {tuple(x.shape)}")
+    if K % 32:
+        raise ValueError(f"K must be a multiple of 32, got {K}")
+    if training and (x.shape[0] % 32 or N % 32):
+        raise ValueError(f"the gradients contract T and N: multiples of 32, got {x.shape[0]} and {N}")
     if isinstance(weight, torch.Tensor):
         weight = quantize_linear(weight, format, training)
     elif training and weight.col is None:
@@ -56,7 +74,10 @@ def linear_layer(x: torch.Tensor, weight: torch.Tensor | FP4Tensor | NVFP4Tensor
 
 
 def linear_layer_grad(dy: torch.Tensor, saved: LinearSaved) -> tuple[torch.Tensor, torch.Tensor]:
-    """(dx [T, K] in dy's type, dweight [N, K] float32)."""
+    """(dx [T, K] in dy's type, dweight [N, K] float32), dy [T, N]."""
+    shape = saved.x.row.data.shape[0], saved.weight.row.data.shape[0]
+    if dy.shape != shape:
+        raise ValueError(f"dy must be {shape}, got {tuple(dy.shape)}")
     q = _cast(dy, saved.format, True, "1d")
     return matmul_fp4(q.row, saved.weight.col, out_dtype=dy.dtype), \
         matmul_fp4(q.col, saved.x.col, out_dtype=torch.float32)
