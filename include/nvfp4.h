@@ -563,7 +563,9 @@ nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, in
  * NVFP4_MAX_MLP_WIDTH.  workspace: nvfp4_expert_mlp_workspace bytes of device
  * memory, 128-byte aligned, contents irrelevant, not shared by calls that can run
  * at the same time.  Four launches (NVFP4 five); two for one or two tokens with
- * up to eight choices in all.
+ * up to eight choices in all, as long as a CTA's share of x, cut into 4 bits, stays
+ * in shared memory: 12 * 256 elements, and the CTAs that share x are 4, 2 or 1, as
+ * many as fit beside one another for all 64-row tiles of the chosen experts.
  */
 #define NVFP4_MAX_MLP_SLOTS 1024
 #define NVFP4_MAX_MLP_WIDTH 10240

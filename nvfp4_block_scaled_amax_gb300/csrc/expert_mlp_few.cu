@@ -1,5 +1,6 @@
 // expert_mlp_few.cu -- the layer of expert_mlp.cu for one or two tokens and up to
-// eight choices in all, in two launches: what the four launches there take to
+// eight choices in all (and x's terms in shared memory, see few_tokens), in two
+// launches: what the four launches there take to
 // begin is most of the time of so little work (one token to two of eight experts
 // of 4096 x 2048: 20.6 us there and 14.4 here, of which reading the weights takes
 // 4.2; the rest is the start of two launches, the cut of x and of the hidden values
@@ -606,7 +607,10 @@ cudaError_t launch_product(const ExpertMlpArgs& a, FewArgs p, const LaunchCtx& c
 bool few_tokens(const ExpertMlpArgs& a, const LaunchCtx& ctx) {
   if (a.tokens > kTok || a.tokens * a.topk > kMaxChoices) return false;
   const int split = up_split(a, ctx);
-  return (stages_of(a.hidden) + split - 1) / split <= kMaxResident;  // x's terms stay in shared memory
+  // x's terms stay in shared memory, beside three stages of weights at least; where a CTA's share is
+  // longer (many tiles, none of them shared) it would leave fewer, and the layer has work enough for
+  // the launches of expert_mlp.cu.
+  return (stages_of(a.hidden) + split - 1) / split <= kMaxResident;
 }
 
 size_t few_tokens_workspace(const ExpertMlpArgs& a) {
