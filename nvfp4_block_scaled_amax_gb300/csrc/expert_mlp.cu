@@ -35,13 +35,15 @@
 // tokens' terms, the contracted dimension of a tile split over a cluster where
 // there are few tiles; partial results travel with their terms already added.
 //
-// Measured: 13 tokens, 4 of 16 experts of 2720 x 1184 (MXFP4) 26.2 us, where reading
-// the weights takes 15.5; 64 tokens, 4 of 32 experts of 4096 x 1536 (NVFP4) 72 us of
-// 51.  Of the 72, 7 go by until the terms are there (the first three stages of
-// weights of every CTA are read meanwhile), 5 between the two products and 4 for
-// the join; in between, weights and scales come at 5.9 TB/s.  Not kept, as the time
-// stayed or grew: the next weights, or the next product's, or the next tile's
-// scales fetched into L2 ahead; two stages of scales a warp.
+// Measured: 13 tokens, 4 of 16 experts of 2720 x 1184 (MXFP4) 27.8 us, where reading
+// the weights takes 15.5; 64 tokens, 4 of 32 experts of 4096 x 1536 (NVFP4) 77 us of
+// 51 (72 with six terms and hidden rows that were cut tile by tile).  Weights and scales
+// come at 5.9 TB/s while they come; the rest are steps that wait for one another:
+// about 7 us until x's terms are there (the first three stages of weights of every
+// CTA are read meanwhile), the hidden rows' way from one product to the next, and
+// 4 for the join.  Not kept, as the time stayed or grew: the next weights, or the
+// next product's, or the next tile's scales fetched into L2 ahead; two stages of
+// scales a warp.
 #include "expert_mlp.cuh"
 
 namespace nvfp4 {
@@ -694,9 +696,9 @@ __global__ void __launch_bounds__(256) join_slots_kernel(const float* parts, con
 // Tokens of a segment: more cost columns that few experts fill, fewer read the
 // weights of a popular expert again.  Fourteen are the most whose columns fit twice into
 // half of the tensor memory, beside the scales.  Eight where experts have four on average
-// or fewer (13 tokens, 4 of 16 experts of 2720 x 1184: 27.1 us against 30.3 with
-// sixteen, six terms each); with eight on average there is no difference (64 tokens, 4
-// of 32 experts of 4096 x 1536: 72.4 and 71.5).
+// or fewer (13 tokens, 4 of 16 experts of 2720 x 1184: 27.8 us against 31.0 with
+// fourteen); with eight on average there is hardly a difference (64 tokens, 4 of 32
+// experts of 4096 x 1536: 77.6 with eight, 77.0).
 int tokens_per_segment(int64_t tokens, int64_t slots, int64_t experts) {
   return tokens <= 2 ? 2 : tokens <= 8 || slots <= 4 * experts ? 8 : 14;
 }
@@ -755,8 +757,8 @@ cudaError_t launch_product(const Fp4Side& weights, MlpKernelArgs p, int64_t slot
   p.status = ctx.status;
   const int64_t tiles = segments * p.tiles, stages_k = (p.width + kStageK - 1) / kStageK;
   // A tile's stages are shared by up to four CTAs where they fit beside one another, two
-  // stages each at least (6 tokens, one of 2 experts of 8192 x 1024: 18.4 us, unshared 21.1;
-  // 8 tokens, one expert of 4096 x 2048: 15.8, unshared 17.1, by up to eight 17.0).
+  // stages each at least (6 tokens, one of 2 experts of 8192 x 1024: 21.6 us, unshared 25.5, by
+  // up to eight 22.7; 8 tokens, one expert of 4096 x 2048: 19.9, 20.8 and 20.8).
   int split = 1;
   for (int s = 4; s >= 2 && split == 1; s /= 2)
     if (tiles * s <= 2 * ctx.num_sms && stages_k >= 2 * s) split = s;
@@ -815,8 +817,9 @@ cudaError_t launch_layer(const ExpertMlpArgs& a, const LaunchCtx& ctx) {
   p.h_unit = ws.h.unit;
   p.plan = ws.plan;
   void* args[] = {&p};
-  // Few tokens' choices are dealt to more CTAs, as far as two fit on an SM (the layer for 13 tokens:
-  // 27.1 to 26.2 us; with a CTA for each choice of 64 tokens 73.2 instead of 72.3).
+  // Few tokens' choices are dealt to more CTAs, as far as two fit on an SM (one token, 32 of 64 experts of
+  // 2048 x 512: 27.6 us, by one CTA for all of a token's 34.0; 13 tokens, 4 of 16 experts of 2720 x 1184: 27.8
+  // and 28.0; with a CTA for each choice of 64 tokens, 4 of 32 experts of 4096 x 1536, 77.6 instead of 77.0).
   const unsigned groups = (unsigned)(a.tokens * ((a.hidden + kPrepPart - 1) / kPrepPart));
   int64_t shares = 2 * ctx.num_sms / groups;
   shares = shares < 1 ? 1 : shares < a.topk ? shares : a.topk;

@@ -1,9 +1,8 @@
 // expert_mlp_few.cu -- the layer of expert_mlp.cu for one or two tokens and up to
 // eight choices in all (and x's terms in shared memory, see few_tokens), in two
-// launches: what the four launches there take to
-// begin is most of the time of so little work (one token to two of eight experts
-// of 4096 x 2048: 20.6 us there and 14.4 here, of which reading the weights takes
-// 4.2; the rest is the start of two launches, the cut of x and of the hidden values
+// launches: what the launches there take to begin is most of the time of so little
+// work (one token to two of eight experts of 4096 x 2048: 19.9 us there and 15.8
+// here, of which reading the weights takes 4.2; the rest is the start of two launches, the cut of x and of the hidden values
 // into terms, and the clusters' joins, one after the other).
 //
 // The first kernel cuts x into terms itself, each CTA its share of the
@@ -541,7 +540,7 @@ int64_t most_experts(const ExpertMlpArgs& a) {
 }
 int64_t hidden_tiles(const ExpertMlpArgs& a) { return (a.inner + kWeights / 2 - 1) / (kWeights / 2); }
 // CTAs of a cluster that share a tile's stages: as many as fit beside one another, up to four, two stages each
-// at least (one token, two of 8 experts of 4096 x 2048: 14.4 us; up to eight 14.6, two 15.8, unshared 17.4).
+// at least (one token, two of 8 experts of 4096 x 2048: 15.8 us, by up to eight too, two 17.6, unshared 20.0).
 int split_of(int64_t tiles, int64_t stages, const LaunchCtx& ctx) {
   for (int s = 4; s >= 2; s /= 2)
     if (tiles * s <= 2 * ctx.num_sms && stages >= 2 * s) return s;
