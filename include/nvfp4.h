@@ -557,7 +557,7 @@ nvfp4_status nvfp4_fp4_matmul(const nvfp4_operand* a, const nvfp4_operand* b, in
  * adds nothing; a token with none left gives zero.
  * Sums are FP32; x and h enter a product as sums of eight 4-bit operands, which
  * leave at most 2^-23 (NVFP4) or 2^-22 (MXFP4) of the largest value of each block,
- * or 2^-40 of the largest of an NVFP4 row of x or h; y is rounded once.  A token with
+ * or 2^-39 of the largest of an NVFP4 row of x or h; y is rounded once.  A token with
  * an infinity or a NaN, in x or in h, gives NaN.
  * tokens * topk <= NVFP4_MAX_MLP_SLOTS, hidden and inner multiples of 32 up to
  * NVFP4_MAX_MLP_WIDTH.  workspace: nvfp4_expert_mlp_workspace bytes of device

@@ -21,11 +21,11 @@
 // added with their ratios after the product.  They are rows beside the others: N = 8
 // tokens, where few rows leave an MMA's columns empty anyway.
 // E4M3 scales span 17 powers of two; they count in units of their row, so that a
-// row's small blocks lose nothing until 2^-40 of its largest.  The unit comes from
+// row's small blocks lose nothing until 2^-39 of its largest.  The unit comes from
 // the row's largest element, which of a hidden row is not known before all of its
 // tiles are: NVFP4 keeps the hidden rows in FP32 and cuts them in a launch of their
 // own.  (A unit from a bound, |g|, |u| <= amax sum|x|, would spare the launch but
-// hold h to 2^-40 of a number that may be any multiple of it.)  MXFP4's powers
+// hold h to 2^-39 of a number that may be any multiple of it.)  MXFP4's powers
 // of two need no unit, and its hidden rows are cut where they are made.
 //
 // Four launches (NVFP4 five): slots sorted by expert and x into terms; gate and up

@@ -111,8 +111,8 @@ def expert_mlp(x: torch.Tensor, up: FP4Operand, down: FP4Operand, expert_ids: to
     tokens: x [T, H] bfloat16, expert_ids int32 and gates float32 [T, topk], up [E, 2 F, H] (an expert's gate rows, then
     its up rows) and down [E, H, F] 4-bit operands of one format with compact scales (``quantize_experts``).  Ids outside
     0 .. E - 1 are dropped.  T * topk <= 1024; H and F multiples of 32, at most 10240.  Sums are float32; what x and the
-    hidden values are held in leaves at most 2^-22 of the largest value of each of their blocks, whatever the weights'
-    amaxes.  An expert's weights are read again for every 14 of its tokens (8 where experts have few), so that many tokens
+    hidden values are held in leaves at most 2^-22 of the largest value of each of their blocks (NVFP4: or 2^-39 of their
+    row's), whatever the weights' amaxes.  An expert's weights are read again for every 14 of its tokens (8 where experts have few), so that many tokens
     an expert are not what this is for; ``expert_layer`` has no such limit, over weights in 8 bits."""
     E, F2, H = _check_operand("up", up, 3)
     Ed, Hd, F = _check_operand("down", down, 3)
